@@ -84,7 +84,8 @@ enum moe_status {
   MOE_EFILL = -6          /* a slot-pool fill (host -> HBM expert copy) failed */
 };
 
-enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 };
+/* MOE_F16 is an operand type of the dense operators (moe_linear_*, moe_gated_*) only. */
+enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 };
 
 /* Device error word bits (moe_check_device_error). */
 enum moe_device_error {
@@ -456,6 +457,96 @@ MOE_API int moe_pool_unlend(moe_pool* pool, void* stream);
  * then releases the compute stream with MOE_DERR_FILL set and returns MOE_EFILL (Betelgeuse article,
  * "what bit-exact means": a failed expert read is an error, never zero weights).  -1 = off. */
 MOE_API int moe_pool_debug_fail_copies(moe_pool* pool, int32_t after_n);
+
+/* ---- Dense operators ------------------------------------------------------------------------
+ * What stands beside the routed experts in a model and has plain 16-bit weights: a dense shared
+ * expert or the dense feed-forward blocks of its first layers, projections, the output head; each
+ * with its backward pass.  Row-major matrices, one row per token; a weight is [n_out][n_in]:
+ *
+ *   linear  z = x W^T + b               y = act(z) + r                       (b, r optional)
+ *           dz = dy * act'(z)           dx = dz W    dW = dz^T x    db = sum_t dz
+ *   gated   g = x Wg^T + bg, u = x Wu^T + bu         h = act(g) * u
+ *           dg = dh * u * act'(g)       du = dh * act(g)
+ *           dx = dg Wg + du Wu          dWg = dg^T x   dWu = du^T x   dbg = sum_t dg   dbu = sum_t du
+ *
+ * A gated block whose h goes through a linear (W [hidden][F], r = the routed layer's fp32 y) adds a
+ * dense shared expert to moe_layer_forward's output.
+ *
+ * Conventions, beyond those at the top of this file:
+ *   - dims->dtype is the type of x, every weight, bias, saved pre-activation, h, incoming gradient
+ *     and result of a backward pass: MOE_BF16 or MOE_F16 (anything else: MOE_EUNSUPPORTED).  y and r of the
+ *     linear share y_dtype: dims->dtype or MOE_F32.
+ *   - ld* is a matrix's row stride in elements, at least its row length and at most MOE_DENSE_MAX_LD;
+ *     rows may start at any element-aligned address (a slice of a wider tensor, an odd width).  Rows
+ *     of 16-byte aligned addresses, strides and lengths run the asynchronous-copy kernels, others a
+ *     slower variant of them.  A misaligned element (odd address) is MOE_EINVAL.
+ *   - 1 <= n_in, n_out <= MOE_DENSE_MAX_WIDTH; 1 <= n_tokens <= MOE_DENSE_MAX_TOKENS (beyond:
+ *     MOE_EUNSUPPORTED).
+ *   - Sums are fp32 in a fixed order, so equal calls give equal bits.  Up to
+ *     MOE_DENSE_ROW_TOKENS tokens a forward pass gives a token the same bits alone and in any batch.
+ *     Results are rounded to their type once (to nearest even); a value beyond fp16's range becomes infinite, as the
+ *     type has it.  The backward passes round dz (dg, du) to dims->dtype before the matrix products;
+ *     the bias gradients sum it unrounded.
+ *   - Outputs must not overlap inputs or each other, except y on r exactly (same address and
+ *     stride).  A NULL output of a backward pass is not computed; at least one must be given.
+ *   - `ws` as everywhere: moe_dense_workspace_bytes(dims, n_tokens, backward) bytes, cleared once
+ *     with moe_workspace_init.  The layer's calls and these may share one, ordered on one stream.
+ */
+#define MOE_DENSE_MAX_WIDTH (1 << 20)
+#define MOE_DENSE_MAX_LD (1 << 22)
+#define MOE_DENSE_MAX_TOKENS (1 << 24)
+#define MOE_DENSE_ROW_TOKENS 16
+
+/* MOE_ACT_GELU is z * Phi(z) (erf), MOE_ACT_GELU_TANH its tanh form; relu'(0) = 0.  The gated block
+ * takes any of them as its act (MOE_ACT_NONE: the bilinear block h = g * u). */
+enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_RELU = 4,
+               MOE_ACT_SIGMOID = 5 };
+
+typedef struct moe_dense_dims {
+  int32_t n_in;   /* row length of x and of every weight */
+  int32_t n_out;  /* rows of each weight; row length of y, z (g, u, h) */
+  int32_t dtype;  /* MOE_BF16 or MOE_F16 */
+  int32_t act;    /* moe_act */
+} moe_dense_dims;
+
+/* Workspace bytes that the forward calls (backward = 0) or all calls (backward = 1) with `dims` need
+ * for up to `max_tokens` tokens; 0 if dims are invalid or max_tokens out of range. */
+MOE_API size_t moe_dense_workspace_bytes(const moe_dense_dims* dims, int32_t max_tokens, int32_t backward);
+
+/* y [n_tokens][n_out] (y_dtype) = act(x W^T + bias) + residual.
+ *   x [n_tokens][n_in]; w [n_out][n_in]; bias [n_out] or NULL; residual [n_tokens][n_out] of
+ *   y_dtype or NULL (ld_residual is then ignored); pre [n_tokens][n_out] or NULL receives z for the
+ *   backward pass (ld_pre ignored when NULL). */
+MOE_API int moe_linear_forward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
+                               int64_t ldw, const void* bias_or_null, const void* residual_or_null, int64_t ld_residual,
+                               void* y, int64_t ldy, int32_t y_dtype, void* pre_or_null, int64_t ld_pre, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* Gradients of moe_linear_forward's act(x W^T + bias); the residual's is dy itself.
+ *   pre = the saved z (required unless act is MOE_ACT_NONE; then ignored); dy [n_tokens][n_out];
+ *   dx [n_tokens][n_in], dw [n_out][n_in], dbias [n_out]: NULL = not wanted. */
+MOE_API int moe_linear_backward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
+                                int64_t ldw, const void* pre_or_null, int64_t ld_pre, const void* dy, int64_t ld_dy,
+                                void* dx_or_null, int64_t ld_dx, void* dw_or_null, int64_t ld_dw, void* dbias_or_null,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* h [n_tokens][n_out] = act(x Wg^T + bias_gate) * (x Wu^T + bias_up); both projections, the activation and the
+ * product in one pass.  w_gate and w_up [n_out][n_in] may be the halves of one [2 n_out][n_in]
+ * tensor.  gate / up [n_tokens][n_out] or NULL receive g and u for the backward pass (both or neither). */
+MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens,
+                              const void* w_gate, int64_t ld_wg, const void* w_up, int64_t ld_wu,
+                              const void* bias_gate_or_null, const void* bias_up_or_null, void* h, int64_t ldh,
+                              void* gate_or_null, int64_t ld_gate, void* up_or_null, int64_t ld_up, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* Gradients of moe_gated_forward.  gate, up = the saved g and u; dh [n_tokens][n_out]; every output
+ * NULL = not wanted. */
+MOE_API int moe_gated_backward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens,
+                               const void* w_gate, int64_t ld_wg, const void* w_up, int64_t ld_wu, const void* gate,
+                               int64_t ld_gate, const void* up, int64_t ld_up, const void* dh, int64_t ld_dh,
+                               void* dx_or_null, int64_t ld_dx, void* dw_gate_or_null, int64_t ld_dwg,
+                               void* dw_up_or_null, int64_t ld_dwu, void* dbias_gate_or_null, void* dbias_up_or_null,
+                               void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

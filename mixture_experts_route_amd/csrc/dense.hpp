@@ -1,0 +1,241 @@
+// The dense operators' types, activations, epilogue and launch arguments (moe_linear_*, moe_gated_*).
+#pragma once
+
+#include <math.h>
+
+#include "kernels.hpp"
+
+namespace moe {
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+
+// Operand types: 8-value vectors, the matrix step and 4-value vectors for the epilogue.
+template <typename T>
+struct Operand;
+template <>
+struct Operand<__bf16> {
+  typedef bf16x8 v8;
+  typedef bf16x4 v4;
+  static MOE_DEV float4v mma(v8 a, v8 b, float4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+};
+template <>
+struct Operand<_Float16> {
+  typedef half8 v8;
+  typedef half4 v4;
+  static MOE_DEV float4v mma(v8 a, v8 b, float4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+};
+
+// ---- activations ----------------------------------------------------------------------------------
+// sigmoid by the hardware's exp2 and reciprocal (each within 1 ulp): relative error about
+// (2 + |z|) 2^-24, below a 16-bit output's half step by a factor of 2^10 and at fp32's own level for an
+// fp32 output.  exp2 overflowing to infinity gives 0, its underflow 1, as the function does.
+MOE_DEV float fast_sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
+
+constexpr float kGeluC = 0.79788456080286536f;  // sqrt(2 / pi)
+constexpr float kGeluK = 0.044715f;
+
+MOE_DEV float act_value(int act, float z) {
+  switch (act) {
+    case MOE_ACT_SILU: return z * fast_sigmoid(z);
+    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case MOE_ACT_GELU_TANH: return z * fast_sigmoid(2.0f * kGeluC * z * (1.0f + kGeluK * z * z));  // (1 + tanh v) / 2 = sigmoid(2 v)
+    case MOE_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case MOE_ACT_SIGMOID: return fast_sigmoid(z);
+    default: return z;
+  }
+}
+
+// s = sigmoid(z) and c = 1 - s without cancellation (e s, with e = exp(-z) kept finite; NaN passes).
+MOE_DEV void fast_sigmoid_pair(float z, float& s, float& c) {
+  float e = __builtin_amdgcn_exp2f(z * -1.44269504088896341f);
+  e = e > 1e37f ? 1e37f : e;
+  s = __builtin_amdgcn_rcpf(1.0f + e);
+  c = e * s;
+}
+
+// Value and derivative together (the gated block's backward pass needs both).
+MOE_DEV void act_both(int act, float z, float& v, float& d) {
+  switch (act) {
+    case MOE_ACT_SILU: {
+      float s, c;
+      fast_sigmoid_pair(z, s, c);
+      v = z * s;
+      d = s * (1.0f + z * c);
+      break;
+    }
+    case MOE_ACT_GELU: {
+      const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+      v = z * cdf;
+      d = cdf + z * 0.39894228040143268f * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+      break;
+    }
+    case MOE_ACT_GELU_TANH: {
+      float s, c;
+      fast_sigmoid_pair(2.0f * kGeluC * z * (1.0f + kGeluK * z * z), s, c);
+      v = z * s;
+      d = s + z * s * c * (2.0f * kGeluC * (1.0f + 3.0f * kGeluK * z * z));
+      break;
+    }
+    case MOE_ACT_RELU:
+      v = z > 0.0f ? z : (z != z ? z : 0.0f);
+      d = z > 0.0f ? 1.0f : 0.0f;
+      break;
+    case MOE_ACT_SIGMOID: {
+      float s, c;
+      fast_sigmoid_pair(z, s, c);
+      v = s;
+      d = s * c;
+      break;
+    }
+    default:
+      v = z;
+      d = 1.0f;
+  }
+}
+
+// ---- epilogues ------------------------------------------------------------------------------------
+enum DenseEpiKind { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2 };
+
+struct DenseEpi {
+  void* y[2];          // the output (kEpiStore: one per batch)
+  int64_t ldy[2];
+  const void* bias[2];  // linear: [0]; gated: gate, up
+  const void* res;
+  int64_t ldr;
+  void* pre[2];        // saved z; g and u
+  int64_t ldp[2];
+  int32_t y_f32;       // linear: y and res are fp32
+  int32_t act;
+  int32_t vec;         // every matrix above may be moved 4 elements at a time (rows and strides aligned to that)
+};
+
+// 4 consecutive elements of a row, or the first n of them.
+template <typename T>
+MOE_DEV void load4(const void* base, int64_t off, int n, bool vec, float v[4]) {
+  const T* p = (const T*)base + off;
+  if (vec) {
+    typedef T v4 __attribute__((ext_vector_type(4)));
+    const v4 t = *(const v4*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)t[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? (float)p[i] : 0.0f;
+  }
+}
+template <typename T>
+MOE_DEV void store4(void* base, int64_t off, int n, bool vec, const float v[4]) {
+  T* p = (T*)base + off;
+  if (vec) {
+    typedef T v4 __attribute__((ext_vector_type(4)));
+    v4 t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = (T)v[i];
+    *(v4*)p = t;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = (T)v[i];
+  }
+}
+
+// Output elements (i, j .. j + n - 1), n = 1..4 (n = 4 whenever e.vec): s0 = the fp32 sums (gated: the gate's), s1 = the up's.
+template <typename T, int KIND>
+MOE_DEV void finish4(const DenseEpi& e, int batch, int64_t i, int j, int n, float s0[4], float s1[4]) {
+  const bool vec = e.vec;
+  if constexpr (KIND == kEpiStore) {
+    store4<T>(e.y[batch], i * e.ldy[batch] + j, n, vec, s0);
+  } else if constexpr (KIND == kEpiLinear) {
+    if (e.bias[0]) {
+      float b[4];
+      load4<T>(e.bias[0], j, n, vec, b);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s0[c] += b[c];
+    }
+    if (e.pre[0]) store4<T>(e.pre[0], i * e.ldp[0] + j, n, vec, s0);
+    if (e.act != MOE_ACT_NONE) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s0[c] = act_value(e.act, s0[c]);
+    }
+    if (e.res) {
+      float r[4];
+      if (e.y_f32)
+        load4<float>(e.res, i * e.ldr + j, n, vec, r);
+      else
+        load4<T>(e.res, i * e.ldr + j, n, vec, r);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s0[c] += r[c];
+    }
+    if (e.y_f32)
+      store4<float>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
+    else
+      store4<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
+  } else {
+    if (e.bias[0]) {
+      float b[4];
+      load4<T>(e.bias[0], j, n, vec, b);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s0[c] += b[c];
+    }
+    if (e.bias[1]) {
+      float b[4];
+      load4<T>(e.bias[1], j, n, vec, b);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s1[c] += b[c];
+    }
+    if (e.pre[0]) {
+      store4<T>(e.pre[0], i * e.ldp[0] + j, n, vec, s0);
+      store4<T>(e.pre[1], i * e.ldp[1] + j, n, vec, s1);
+    }
+    float h[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) h[c] = act_value(e.act, s0[c]) * s1[c];
+    store4<T>(e.y[0], i * e.ldy[0] + j, n, vec, h);
+  }
+}
+
+// ---- tile products: out[i][j] = sum_r A(i, r) B(j, r) ------------------------------------------------
+// An operand is stored with its reduction index contiguous (kRows: A[i][r]) or its output index
+// contiguous (kCols: A[r][i]).
+//   forward     A = x   kRows, B = W   kRows   (gated: B[0] = Wg, B[1] = Wu, both sums per output)
+//   dx          A = dz  kRows, B = W   kCols   (gated: two segments, dg Wg then du Wu, in one sum)
+//   dW          A = dz  kCols, B = x   kCols   (gated: two batches, dg and du)
+enum OperandOrder { kRows = 0, kCols = 1 };
+struct TileArgs {
+  const void* a[2];
+  const void* b[2];
+  int64_t lda[2], ldb[2];
+  int32_t M, N, R;         // outputs i, j; reduction per segment
+  int32_t nseg, nbatch;    // 1 or 2 each
+  int32_t tiles_i, tiles_j;
+  int32_t splits;          // workgroups sharing a tile's reduction, joined through `part`
+  float* part;
+  int32_t* arrived;        // per tile, zero between calls
+  DenseEpi epi;
+};
+
+// dz of a backward pass: dz0 = dy * act'(pre0) (dy itself without an activation), or gated dz0 = dh * u * act'(g),
+// dz1 = dh * act(g) with pre0 = g, pre1 = u; rows of ldz elements, zero from N to ldz.  Column sums of the
+// unrounded values over runs of kGradRows rows go to `part` [run][mats][N] when wanted.
+constexpr int kGradRows = 64;
+struct GradArgs {
+  const void* dy;
+  const void* pre0;
+  const void* pre1;
+  int64_t ld_dy, ldp0, ldp1, ldz;
+  void* dz0;  // NULL: the sums only
+  void* dz1;
+  float* part;  // NULL: no sums
+  int32_t T, N;
+  int32_t act;
+};
+
+// dense_tile_*.hip, dense_grad.hip (dtype: MOE_BF16 or MOE_F16)
+hipError_t launch_tile(int dtype, const TileArgs& a, int order_a, int order_b, int epi_kind, hipStream_t st);
+hipError_t launch_grad_in(int dtype, const GradArgs& a, bool gated, hipStream_t st);
+hipError_t launch_bias_sum(int dtype, const float* part, int runs, int mats, int N, void* db0, void* db1, hipStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,322 @@
+// The dense operators' C interface (moe_linear_*, moe_gated_*): host-side validation, workspace carving
+// and launches.  Nothing is enqueued when a call returns an error.
+#include "dense.hpp"
+
+namespace moe {
+
+// Workspace: control words, then for a backward pass dz (gated: dg, du) in the operands' type with rows
+// padded to whole 16-byte chunks, and the bias gradients' partial sums.
+struct DenseWs {
+  size_t dz0, dz1, bias_part, total;
+  int64_t ldz;
+};
+
+static size_t dense_align(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Two matrices whatever the call (one size serves the linear and the gated block).
+static DenseWs dense_ws(const moe_dense_dims* d, int64_t T, bool backward) {
+  DenseWs L{};
+  size_t off = kCtrlBytes;
+  if (backward) {
+    const int64_t runs = (T + kGradRows - 1) / kGradRows;
+    L.ldz = ((int64_t)d->n_out + 7) / 8 * 8;
+    L.dz0 = off;
+    off = dense_align(off + 2 * (size_t)(T * L.ldz));
+    L.dz1 = off;
+    off = dense_align(off + 2 * (size_t)(T * L.ldz));
+    L.bias_part = off;
+    off = dense_align(off + sizeof(float) * 2 * (size_t)(runs * d->n_out));
+  }
+  L.total = off;
+  return L;
+}
+
+static int check_dense(const moe_dense_dims* d) {
+  if (!d || d->n_in < 1 || d->n_out < 1) return MOE_EINVAL;
+  if (d->n_in > MOE_DENSE_MAX_WIDTH || d->n_out > MOE_DENSE_MAX_WIDTH) return MOE_EUNSUPPORTED;
+  if (d->dtype != MOE_BF16 && d->dtype != MOE_F16) return MOE_EUNSUPPORTED;
+  if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_SIGMOID) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+static int check_tokens(int32_t T) {
+  if (T < 1) return MOE_EINVAL;
+  return T > MOE_DENSE_MAX_TOKENS ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
+// Collects the checks of a call's matrices: element-aligned, rows that do not overlap, strides in range.
+struct Mats {
+  int rc = MOE_OK;
+  void fail(int code) {
+    if (rc == MOE_OK) rc = code;
+  }
+  void need(const void* p, int64_t ld, int64_t len, int elem = 2) {
+    if (!p) fail(MOE_EINVAL);
+    else opt(p, ld, len, elem);
+  }
+  void opt(const void* p, int64_t ld, int64_t len, int elem = 2) {
+    if (!p) return;
+    if ((uintptr_t)p % elem || ld < len) fail(MOE_EINVAL);
+    else if (ld > MOE_DENSE_MAX_LD) fail(MOE_EUNSUPPORTED);
+  }
+  void vec(const void* p) { opt(p, 1, 1); }
+};
+
+static int check_dense_ws(const moe_dense_dims* d, int32_t T, bool backward, const void* ws, size_t ws_bytes) {
+  if (!ws || ((uintptr_t)ws & 255)) return MOE_EWORKSPACE;
+  return ws_bytes < dense_ws(d, T, backward).total ? MOE_EWORKSPACE : MOE_OK;
+}
+
+static int dense_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
+
+// 4-element accesses: rows start and stay aligned to 4 elements.
+static bool vec4(const void* p, int64_t ld, int elem = 2) { return !p || ((uintptr_t)p % (4 * elem) == 0 && ld % 4 == 0); }
+
+static uint8_t* ws_at(void* ws, size_t off) { return (uint8_t*)ws + off; }
+
+// dx = sum over mats of dz[m] W[m], then dW[m] = dz[m]^T x.
+static int run_products(const moe_dense_dims* d, int mats, const void* x, int64_t ldx, int32_t T, const void* const* w,
+                        const int64_t* ldw, const void* const* dz, int64_t ldz, void* dx, int64_t ld_dx, void* const* dw,
+                        const int64_t* ld_dw, hipStream_t st) {
+  if (dx) {
+    TileArgs a{};
+    for (int m = 0; m < mats; ++m) {
+      a.a[m] = dz[m];
+      a.lda[m] = ldz;
+      a.b[m] = w[m];
+      a.ldb[m] = ldw[m];
+    }
+    a.M = T;
+    a.N = d->n_in;
+    a.R = d->n_out;
+    a.nseg = mats;
+    a.nbatch = 1;
+    a.epi.y[0] = dx;
+    a.epi.ldy[0] = ld_dx;
+    a.epi.vec = d->n_in % 4 == 0 && vec4(dx, ld_dx);
+    const int rc = dense_status(launch_tile(d->dtype, a, kRows, kCols, kEpiStore, st));
+    if (rc) return rc;
+  }
+  TileArgs a{};
+  a.M = d->n_out;
+  a.N = d->n_in;
+  a.R = T;
+  a.nseg = 1;
+  a.b[0] = a.b[1] = x;
+  a.ldb[0] = a.ldb[1] = ldx;
+  a.epi.vec = d->n_in % 4 == 0;
+  for (int m = 0; m < mats; ++m) {
+    if (!dw[m]) continue;
+    a.a[a.nbatch] = dz[m];
+    a.lda[a.nbatch] = ldz;
+    a.epi.y[a.nbatch] = dw[m];
+    a.epi.ldy[a.nbatch] = ld_dw[m];
+    a.epi.vec = a.epi.vec && vec4(dw[m], ld_dw[m]);
+    ++a.nbatch;
+  }
+  return a.nbatch ? dense_status(launch_tile(d->dtype, a, kCols, kCols, kEpiStore, st)) : MOE_OK;
+}
+
+hipError_t launch_tile_bf16(const TileArgs& a, int oa, int ob, int kind, hipStream_t st);
+hipError_t launch_tile_f16(const TileArgs& a, int oa, int ob, int kind, hipStream_t st);
+
+hipError_t launch_tile(int dtype, const TileArgs& a, int oa, int ob, int kind, hipStream_t st) {
+  return dtype == MOE_BF16 ? launch_tile_bf16(a, oa, ob, kind, st) : launch_tile_f16(a, oa, ob, kind, st);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+MOE_API size_t moe_dense_workspace_bytes(const moe_dense_dims* dims, int32_t max_tokens, int32_t backward) {
+  if (check_dense(dims) != MOE_OK || check_tokens(max_tokens) != MOE_OK) return 0;
+  return dense_ws(dims, max_tokens, backward != 0).total;
+}
+
+MOE_API int moe_linear_forward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
+                               int64_t ldw, const void* bias_or_null, const void* residual_or_null, int64_t ld_residual,
+                               void* y, int64_t ldy, int32_t y_dtype, void* pre_or_null, int64_t ld_pre, void* ws,
+                               size_t ws_bytes, void* stream) {
+  int rc = check_dense(dims);
+  if (rc || (rc = check_tokens(n_tokens))) return rc;
+  if (y_dtype != dims->dtype && y_dtype != MOE_F32) return MOE_EUNSUPPORTED;
+  const int ye = y_dtype == MOE_F32 ? 4 : 2;
+  Mats m;
+  m.need(x, ldx, dims->n_in);
+  m.need(w, ldw, dims->n_in);
+  m.need(y, ldy, dims->n_out, ye);
+  m.opt(residual_or_null, ld_residual, dims->n_out, ye);
+  m.opt(pre_or_null, ld_pre, dims->n_out);
+  m.vec(bias_or_null);
+  if (m.rc) return m.rc;
+  if ((rc = check_dense_ws(dims, n_tokens, false, ws, ws_bytes))) return rc;
+  TileArgs a{};
+  a.a[0] = x;
+  a.lda[0] = ldx;
+  a.b[0] = w;
+  a.ldb[0] = ldw;
+  a.M = n_tokens;
+  a.N = dims->n_out;
+  a.R = dims->n_in;
+  a.nseg = a.nbatch = 1;
+  a.epi.y[0] = y;
+  a.epi.ldy[0] = ldy;
+  a.epi.y_f32 = y_dtype == MOE_F32;
+  a.epi.bias[0] = bias_or_null;
+  a.epi.res = residual_or_null;
+  a.epi.ldr = ld_residual;
+  a.epi.pre[0] = pre_or_null;
+  a.epi.ldp[0] = ld_pre;
+  a.epi.act = dims->act;
+  a.epi.vec = dims->n_out % 4 == 0 && vec4(y, ldy, ye) && vec4(residual_or_null, ld_residual, ye) &&
+              vec4(pre_or_null, ld_pre) && vec4(bias_or_null, 0);
+  return dense_status(launch_tile(dims->dtype, a, kRows, kRows, kEpiLinear, (hipStream_t)stream));
+}
+
+MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens,
+                              const void* w_gate, int64_t ld_wg, const void* w_up, int64_t ld_wu,
+                              const void* bias_gate_or_null, const void* bias_up_or_null, void* h, int64_t ldh,
+                              void* gate_or_null, int64_t ld_gate, void* up_or_null, int64_t ld_up, void* ws,
+                              size_t ws_bytes, void* stream) {
+  int rc = check_dense(dims);
+  if (rc || (rc = check_tokens(n_tokens))) return rc;
+  if (!gate_or_null != !up_or_null) return MOE_EINVAL;
+  Mats m;
+  m.need(x, ldx, dims->n_in);
+  m.need(w_gate, ld_wg, dims->n_in);
+  m.need(w_up, ld_wu, dims->n_in);
+  m.need(h, ldh, dims->n_out);
+  m.opt(gate_or_null, ld_gate, dims->n_out);
+  m.opt(up_or_null, ld_up, dims->n_out);
+  m.vec(bias_gate_or_null);
+  m.vec(bias_up_or_null);
+  if (m.rc) return m.rc;
+  if ((rc = check_dense_ws(dims, n_tokens, false, ws, ws_bytes))) return rc;
+  TileArgs a{};
+  a.a[0] = x;
+  a.lda[0] = ldx;
+  a.b[0] = w_gate;
+  a.b[1] = w_up;
+  a.ldb[0] = ld_wg;
+  a.ldb[1] = ld_wu;
+  a.M = n_tokens;
+  a.N = dims->n_out;
+  a.R = dims->n_in;
+  a.nseg = a.nbatch = 1;
+  a.epi.y[0] = h;
+  a.epi.ldy[0] = ldh;
+  a.epi.bias[0] = bias_gate_or_null;
+  a.epi.bias[1] = bias_up_or_null;
+  a.epi.pre[0] = gate_or_null;
+  a.epi.pre[1] = up_or_null;
+  a.epi.ldp[0] = ld_gate;
+  a.epi.ldp[1] = ld_up;
+  a.epi.act = dims->act;
+  a.epi.vec = dims->n_out % 4 == 0 && vec4(h, ldh) && vec4(gate_or_null, ld_gate) && vec4(up_or_null, ld_up) &&
+              vec4(bias_gate_or_null, 0) && vec4(bias_up_or_null, 0);
+  return dense_status(launch_tile(dims->dtype, a, kRows, kRows, kEpiGated, (hipStream_t)stream));
+}
+
+MOE_API int moe_linear_backward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
+                                int64_t ldw, const void* pre_or_null, int64_t ld_pre, const void* dy, int64_t ld_dy,
+                                void* dx_or_null, int64_t ld_dx, void* dw_or_null, int64_t ld_dw, void* dbias_or_null,
+                                void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_dense(dims);
+  if (rc || (rc = check_tokens(n_tokens))) return rc;
+  if (!dx_or_null && !dw_or_null && !dbias_or_null) return MOE_EINVAL;
+  const bool act = dims->act != MOE_ACT_NONE;
+  Mats m;
+  m.need(x, ldx, dims->n_in);
+  m.need(w, ldw, dims->n_in);
+  if (act) m.need(pre_or_null, ld_pre, dims->n_out);
+  m.need(dy, ld_dy, dims->n_out);
+  m.opt(dx_or_null, ld_dx, dims->n_in);
+  m.opt(dw_or_null, ld_dw, dims->n_in);
+  m.vec(dbias_or_null);
+  if (m.rc) return m.rc;
+  if ((rc = check_dense_ws(dims, n_tokens, true, ws, ws_bytes))) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  const DenseWs L = dense_ws(dims, n_tokens, true);
+  // without an activation dz is dy itself, and is copied only to give its rows whole 16-byte chunks
+  const bool products = dx_or_null || dw_or_null;
+  const bool whole = (uintptr_t)dy % 16 == 0 && ld_dy % 8 == 0 && dims->n_out % 8 == 0;
+  const bool make = products && (act || !whole);
+  if (make || dbias_or_null) {
+    GradArgs g{};
+    g.dy = dy;
+    g.pre0 = act ? pre_or_null : nullptr;
+    g.ld_dy = ld_dy;
+    g.ldp0 = ld_pre;
+    g.ldz = L.ldz;
+    g.dz0 = make ? ws_at(ws, L.dz0) : nullptr;
+    g.part = dbias_or_null ? (float*)ws_at(ws, L.bias_part) : nullptr;
+    g.T = n_tokens;
+    g.N = dims->n_out;
+    g.act = dims->act;
+    if ((rc = dense_status(launch_grad_in(dims->dtype, g, false, st)))) return rc;
+    if (dbias_or_null &&
+        (rc = dense_status(launch_bias_sum(dims->dtype, g.part, (n_tokens + kGradRows - 1) / kGradRows, 1, dims->n_out,
+                                           dbias_or_null, nullptr, st))))
+      return rc;
+  }
+  const void* dz = make ? ws_at(ws, L.dz0) : dy;
+  return run_products(dims, 1, x, ldx, n_tokens, &w, &ldw, &dz, make ? L.ldz : ld_dy, dx_or_null, ld_dx, &dw_or_null,
+                      &ld_dw, st);
+}
+
+MOE_API int moe_gated_backward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens,
+                               const void* w_gate, int64_t ld_wg, const void* w_up, int64_t ld_wu, const void* gate,
+                               int64_t ld_gate, const void* up, int64_t ld_up, const void* dh, int64_t ld_dh,
+                               void* dx_or_null, int64_t ld_dx, void* dw_gate_or_null, int64_t ld_dwg,
+                               void* dw_up_or_null, int64_t ld_dwu, void* dbias_gate_or_null, void* dbias_up_or_null,
+                               void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_dense(dims);
+  if (rc || (rc = check_tokens(n_tokens))) return rc;
+  const bool sums = dbias_gate_or_null || dbias_up_or_null;
+  const bool products = dx_or_null || dw_gate_or_null || dw_up_or_null;
+  if (!products && !sums) return MOE_EINVAL;
+  Mats m;
+  m.need(x, ldx, dims->n_in);
+  m.need(w_gate, ld_wg, dims->n_in);
+  m.need(w_up, ld_wu, dims->n_in);
+  m.need(gate, ld_gate, dims->n_out);
+  m.need(up, ld_up, dims->n_out);
+  m.need(dh, ld_dh, dims->n_out);
+  m.opt(dx_or_null, ld_dx, dims->n_in);
+  m.opt(dw_gate_or_null, ld_dwg, dims->n_in);
+  m.opt(dw_up_or_null, ld_dwu, dims->n_in);
+  m.vec(dbias_gate_or_null);
+  m.vec(dbias_up_or_null);
+  if (m.rc) return m.rc;
+  if ((rc = check_dense_ws(dims, n_tokens, true, ws, ws_bytes))) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  const DenseWs L = dense_ws(dims, n_tokens, true);
+  GradArgs g{};
+  g.dy = dh;
+  g.pre0 = gate;
+  g.pre1 = up;
+  g.ld_dy = ld_dh;
+  g.ldp0 = ld_gate;
+  g.ldp1 = ld_up;
+  g.ldz = L.ldz;
+  g.dz0 = products ? ws_at(ws, L.dz0) : nullptr;
+  g.dz1 = products ? ws_at(ws, L.dz1) : nullptr;
+  g.part = sums ? (float*)ws_at(ws, L.bias_part) : nullptr;
+  g.T = n_tokens;
+  g.N = dims->n_out;
+  g.act = dims->act;
+  if ((rc = dense_status(launch_grad_in(dims->dtype, g, true, st)))) return rc;
+  if (sums && (rc = dense_status(launch_bias_sum(dims->dtype, g.part, (n_tokens + kGradRows - 1) / kGradRows, 2,
+                                                 dims->n_out, dbias_gate_or_null, dbias_up_or_null, st))))
+    return rc;
+  const void* w[2] = {w_gate, w_up};
+  const int64_t ldw[2] = {ld_wg, ld_wu};
+  const void* dz[2] = {g.dz0, g.dz1};
+  void* dw[2] = {dw_gate_or_null, dw_up_or_null};
+  const int64_t ld_dw[2] = {ld_dwg, ld_dwu};
+  return products ? run_products(dims, 2, x, ldx, n_tokens, w, ldw, dz, L.ldz, dx_or_null, ld_dx, dw, ld_dw, st) : MOE_OK;
+}
+
+}  // extern "C"

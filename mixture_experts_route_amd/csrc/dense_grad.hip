@@ -1,0 +1,136 @@
+// The elementwise part of the dense operators' backward passes: dz from dy and the saved pre-activations,
+// and the bias gradients' sums.
+#include "dense.hpp"
+
+namespace moe {
+
+// 8 consecutive elements from `e` of a row of N (zeros past N), any alignment.
+template <typename T>
+MOE_DEV void load8f(const void* base, int64_t off, int e, int N, float v[8]) {
+  const T* p = (const T*)base + off + e;
+  if (e + 8 <= N) {
+    typedef T v8 __attribute__((ext_vector_type(8)));
+    typedef v8 __attribute__((aligned(2))) v8_u;
+    const v8 t = *(const v8_u*)p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)t[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = e + i < N ? (float)p[i] : 0.0f;
+  }
+}
+
+// Memory-bound: reads dy and the saved values once, writes dz once.  A workgroup takes 512 columns (8 per
+// lane, 16 bytes a load) x kGradRows rows; its 4 waves take every fourth row and keep the column sums of
+// their rows in registers, added over the waves in LDS in wave order.
+template <typename T, bool GATED>
+__global__ __launch_bounds__(256) void k_grad_in(GradArgs a) {
+  __shared__ float red[3][2][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.y * 512 + lane * 8;
+  const int t0 = blockIdx.x * kGradRows;
+  const int t1 = a.T - t0 < kGradRows ? a.T : t0 + kGradRows;
+  float sum0[8] = {}, sum1[8] = {};
+  if (e < a.ldz) {
+    for (int t = t0 + wave; t < t1; t += 4) {
+      float dy[8], z0[8], z1[8];
+      load8f<T>(a.dy, (int64_t)t * a.ld_dy, e, a.N, dy);
+      if (GATED) {
+        float g[8], u[8];
+        load8f<T>(a.pre0, (int64_t)t * a.ldp0, e, a.N, g);
+        load8f<T>(a.pre1, (int64_t)t * a.ldp1, e, a.N, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v, d;
+          act_both(a.act, g[i], v, d);
+          z0[i] = dy[i] * u[i] * d;
+          z1[i] = dy[i] * v;
+        }
+      } else if (a.act != MOE_ACT_NONE) {
+        float g[8];
+        load8f<T>(a.pre0, (int64_t)t * a.ldp0, e, a.N, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v, d;
+          act_both(a.act, g[i], v, d);
+          z0[i] = dy[i] * d;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z0[i] = dy[i];
+      }
+      typename Operand<T>::v8 o;
+      if (a.dz0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = (T)z0[i];
+        *(typename Operand<T>::v8*)((T*)a.dz0 + (int64_t)t * a.ldz + e) = o;
+        if (GATED) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = (T)z1[i];
+          *(typename Operand<T>::v8*)((T*)a.dz1 + (int64_t)t * a.ldz + e) = o;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum0[i] += z0[i];
+        if (GATED) sum1[i] += z1[i];
+      }
+    }
+  }
+  if (!a.part) return;
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      red[wave - 1][0][lane * 8 + i] = sum0[i];
+      if (GATED) red[wave - 1][1][lane * 8 + i] = sum1[i];
+    }
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  constexpr int mats = GATED ? 2 : 1;
+  float* out = a.part + (int64_t)blockIdx.x * mats * a.N;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (e + i >= a.N) break;
+#pragma unroll
+    for (int w = 0; w < 3; ++w) {
+      sum0[i] += red[w][0][lane * 8 + i];
+      if (GATED) sum1[i] += red[w][1][lane * 8 + i];
+    }
+    out[e + i] = sum0[i];
+    if (GATED) out[a.N + e + i] = sum1[i];
+  }
+}
+
+// db[m][n] = sum over runs of part[run][m][n], in run order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_bias_sum(const float* part, int runs, int mats, int N, T* db0, T* db1) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= mats * N) return;
+  T* db = c < N ? db0 : db1;
+  if (!db) return;
+  float s = 0.0f;
+  for (int r = 0; r < runs; ++r) s += part[(int64_t)r * mats * N + c];
+  db[c < N ? c : c - N] = (T)s;
+}
+
+hipError_t launch_grad_in(int dtype, const GradArgs& a, bool gated, hipStream_t st) {
+  const dim3 grid((uint32_t)((a.T + kGradRows - 1) / kGradRows), (uint32_t)((a.ldz + 511) / 512));
+  if (dtype == MOE_BF16) {
+    if (gated) k_grad_in<__bf16, true><<<grid, 256, 0, st>>>(a);
+    else k_grad_in<__bf16, false><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (gated) k_grad_in<_Float16, true><<<grid, 256, 0, st>>>(a);
+    else k_grad_in<_Float16, false><<<grid, 256, 0, st>>>(a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_bias_sum(int dtype, const float* part, int runs, int mats, int N, void* db0, void* db1, hipStream_t st) {
+  const uint32_t grid = (uint32_t)((mats * (int64_t)N + 255) / 256);
+  if (dtype == MOE_BF16) k_bias_sum<__bf16><<<grid, 256, 0, st>>>(part, runs, mats, N, (__bf16*)db0, (__bf16*)db1);
+  else k_bias_sum<_Float16><<<grid, 256, 0, st>>>(part, runs, mats, N, (_Float16*)db0, (_Float16*)db1);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -22,7 +22,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP, MOE_EDEVICE, MOE_EFILL = 0, -1, -2, -3, -4, -5, -6
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_DECODE_MAX_TOKENS, MOE_DECODE_MAX_TOKENS_NARROW = 16, 8
 DERR_EXPERT_ID, DERR_SLOT, DERR_NOT_RESIDENT, DERR_NAN, DERR_FILL, DERR_DUP_ID, DERR_RANGE = 1, 2, 4, 8, 16, 32, 64
 
@@ -33,6 +33,8 @@ EXPORTS = [
     "moe_pool_create", "moe_pool_destroy", "moe_pool_arm", "moe_pool_serve", "moe_pool_get_stats",
     "moe_pool_get_table", "moe_pool_get_profile", "moe_profile_seed", "moe_pool_lend", "moe_pool_unlend",
     "moe_pool_debug_fail_copies", "moe_prefill_plan_get", "moe_debug_force_prefill_plan",
+    "moe_dense_workspace_bytes", "moe_linear_forward", "moe_linear_backward", "moe_gated_forward",
+    "moe_gated_backward",
 ]
 
 
@@ -61,6 +63,13 @@ class moe_prefill_plan(ctypes.Structure):
                 ("router_rows", ctypes.c_int32)]
 
 
+class moe_dense_dims(ctypes.Structure):
+    _fields_ = [("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_SIGMOID = range(6)
+MOE_DENSE_MAX_WIDTH, MOE_DENSE_MAX_LD, MOE_DENSE_MAX_TOKENS, MOE_DENSE_ROW_TOKENS = 1 << 20, 1 << 22, 1 << 24, 16
+
 MOE_GEMM_PIPE128, MOE_GEMM_PIPE64_DEEP, MOE_GEMM_GENERAL = 0, 1, 2
 
 
@@ -82,6 +91,8 @@ _D = ctypes.POINTER(moe_dims)
 _W = ctypes.POINTER(moe_layer_weights)
 _B = ctypes.POINTER(moe_doorbell)
 _PP = ctypes.POINTER(ctypes.c_void_p)
+_DD = ctypes.POINTER(moe_dense_dims)
+_L = ctypes.c_int64
 
 _sig = {
     "moe_expert_blob_bytes": (_SZ, [_D]),
@@ -111,6 +122,13 @@ _sig = {
     "moe_pool_debug_fail_copies": (ctypes.c_int, [_P, _I]),
     "moe_prefill_plan_get": (ctypes.c_int, [_D, _I, ctypes.POINTER(moe_prefill_plan)]),
     "moe_debug_force_prefill_plan": (ctypes.c_int, [ctypes.POINTER(moe_prefill_plan)]),
+    "moe_dense_workspace_bytes": (_SZ, [_DD, _I, _I]),
+    "moe_linear_forward": (ctypes.c_int, [_DD, _P, _L, _I, _P, _L, _P, _P, _L, _P, _L, _I, _P, _L, _P, _SZ, _P]),
+    "moe_linear_backward": (ctypes.c_int, [_DD, _P, _L, _I, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _SZ, _P]),
+    "moe_gated_forward": (ctypes.c_int, [_DD, _P, _L, _I, _P, _L, _P, _L, _P, _P, _P, _L, _P, _L, _P, _L, _P, _SZ,
+                                         _P]),
+    "moe_gated_backward": (ctypes.c_int, [_DD, _P, _L, _I, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P,
+                                          _L, _P, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -152,6 +170,8 @@ def dtype_code(t) -> int:
         return MOE_F32
     if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
         return MOE_BF16
+    if t.dtype == torch.float16:  # the dense operators' operands only; the layer's calls refuse it
+        return MOE_F16
     raise TypeError(f"unsupported activation dtype {t.dtype}")
 
 
@@ -255,6 +275,99 @@ def moe_layer_forward_static(d: moe_dims, w: moe_layer_weights, table, x, n_toke
                                          ctypes.byref(bell) if bell else None, _ptr(x), xd, n_tokens, _ptr(y),
                                          _ptr(topk_ids), _ptr(topk_w), _ptr(device_error), _stream(stream)),
            "moe_layer_forward_static")
+
+
+# ---------------------------------------------------------------------------------------------
+# dense operators
+# ---------------------------------------------------------------------------------------------
+
+def dense_dims(n_in: int, n_out: int, dtype: int, act: int = MOE_ACT_NONE) -> moe_dense_dims:
+    return moe_dense_dims(int(n_in), int(n_out), int(dtype), int(act))
+
+
+def moe_dense_workspace_bytes(d: moe_dense_dims, max_tokens: int, backward: bool = False) -> int:
+    return _lib.moe_dense_workspace_bytes(ctypes.byref(d), max_tokens, int(backward))
+
+
+class _DenseCall:
+    """Marshals one dense call: a tensor's sizes, strides, type and device are checked here (the C
+    interface sees addresses only), and the call runs on the tensors' device."""
+
+    def __init__(self, name: str, x, ws, stream):
+        self.name, self.device = name, x.device
+        self.ws = (self._on_device("ws", ws).data_ptr(), ws.numel() * ws.element_size())
+        self.stream = stream
+
+    def _fail(self, arg: str):
+        raise MoeError(MOE_EINVAL, f"{self.name}, {arg}")
+
+    def _on_device(self, arg: str, t):
+        if not t.is_cuda or t.device != self.device:
+            self._fail(arg)
+        return t
+
+    def mat(self, arg: str, t, rows: int, cols: int, dtype: int):
+        """(address, row stride) of a row-major [rows][cols] tensor; (None, 0) for None."""
+        if t is None:
+            return None, 0
+        self._on_device(arg, t)
+        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or dtype_code(t) != dtype:
+            self._fail(arg)
+        if cols > 1 and t.stride(1) != 1:
+            self._fail(arg)
+        return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+    def vec(self, arg: str, t, n: int, dtype: int):
+        if t is None:
+            return None
+        self._on_device(arg, t)
+        if t.dim() != 1 or t.shape[0] != n or dtype_code(t) != dtype or (n > 1 and t.stride(0) != 1):
+            self._fail(arg)
+        return t.data_ptr()
+
+    def __call__(self, d: moe_dense_dims, *args):
+        with torch.cuda.device(self.device):
+            stream = _stream(self.stream)
+            _check(getattr(_lib, self.name)(ctypes.byref(d), *args, *self.ws, stream), self.name)
+
+
+def moe_linear_forward(d: moe_dense_dims, x, n_tokens: int, w, y, ws, bias=None, residual=None, pre=None, stream=None):
+    """``y = act(x w^T + bias) + residual``; y and residual in the operands' type or float32."""
+    c, (K, N, T) = _DenseCall("moe_linear_forward", x, ws, stream), (d.n_in, d.n_out, n_tokens)
+    yd = dtype_code(y)
+    c(d, *c.mat("x", x, T, K, d.dtype), T, *c.mat("w", w, N, K, d.dtype), c.vec("bias", bias, N, d.dtype),
+      *c.mat("residual", residual, T, N, yd), *c.mat("y", y, T, N, yd), yd, *c.mat("pre", pre, T, N, d.dtype))
+
+
+def moe_linear_backward(d: moe_dense_dims, x, n_tokens: int, w, dy, ws, pre=None, dx=None, dw=None, dbias=None,
+                        stream=None):
+    """Gradients of ``act(x w^T + bias)`` from ``dy`` and the saved ``pre``; outputs that are None are not computed."""
+    c, (K, N, T) = _DenseCall("moe_linear_backward", x, ws, stream), (d.n_in, d.n_out, n_tokens)
+    c(d, *c.mat("x", x, T, K, d.dtype), T, *c.mat("w", w, N, K, d.dtype), *c.mat("pre", pre, T, N, d.dtype),
+      *c.mat("dy", dy, T, N, d.dtype), *c.mat("dx", dx, T, K, d.dtype), *c.mat("dw", dw, N, K, d.dtype),
+      c.vec("dbias", dbias, N, d.dtype))
+
+
+def moe_gated_forward(d: moe_dense_dims, x, n_tokens: int, w_gate, w_up, h, ws, gate_bias=None, up_bias=None, gate=None,
+                      up=None, stream=None):
+    """``h = act(x w_gate^T + gate_bias) * (x w_up^T + up_bias)``; ``gate`` and ``up`` receive the two factors'
+    pre-activations for the backward pass."""
+    c, (K, N, T) = _DenseCall("moe_gated_forward", x, ws, stream), (d.n_in, d.n_out, n_tokens)
+    c(d, *c.mat("x", x, T, K, d.dtype), T, *c.mat("w_gate", w_gate, N, K, d.dtype),
+      *c.mat("w_up", w_up, N, K, d.dtype), c.vec("gate_bias", gate_bias, N, d.dtype),
+      c.vec("up_bias", up_bias, N, d.dtype), *c.mat("h", h, T, N, d.dtype), *c.mat("gate", gate, T, N, d.dtype),
+      *c.mat("up", up, T, N, d.dtype))
+
+
+def moe_gated_backward(d: moe_dense_dims, x, n_tokens: int, w_gate, w_up, gate, up, dh, ws, dx=None, dw_gate=None,
+                       dw_up=None, dgate_bias=None, dup_bias=None, stream=None):
+    """Gradients of moe_gated_forward from ``dh`` and the saved ``gate`` and ``up``; None: not computed."""
+    c, (K, N, T) = _DenseCall("moe_gated_backward", x, ws, stream), (d.n_in, d.n_out, n_tokens)
+    c(d, *c.mat("x", x, T, K, d.dtype), T, *c.mat("w_gate", w_gate, N, K, d.dtype),
+      *c.mat("w_up", w_up, N, K, d.dtype), *c.mat("gate", gate, T, N, d.dtype), *c.mat("up", up, T, N, d.dtype),
+      *c.mat("dh", dh, T, N, d.dtype), *c.mat("dx", dx, T, K, d.dtype), *c.mat("dw_gate", dw_gate, N, K, d.dtype),
+      *c.mat("dw_up", dw_up, N, K, d.dtype), c.vec("dgate_bias", dgate_bias, N, d.dtype),
+      c.vec("dup_bias", dup_bias, N, d.dtype))
 
 
 def raw(name: str):
