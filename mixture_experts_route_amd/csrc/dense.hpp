@@ -48,6 +48,23 @@ MOE_DEV float act_value(int act, float z) {
   }
 }
 
+// act_value of 8 values, the activation chosen once for all of them.
+MOE_DEV void act_values(int act, float (&v)[8]) {
+#define MOE_ACT_CASE(A)                                   \
+  case A:                                                 \
+    _Pragma("unroll") for (int c = 0; c < 8; ++c) v[c] = act_value(A, v[c]); \
+    break;
+  switch (act) {
+    MOE_ACT_CASE(MOE_ACT_SILU)
+    MOE_ACT_CASE(MOE_ACT_GELU)
+    MOE_ACT_CASE(MOE_ACT_GELU_TANH)
+    MOE_ACT_CASE(MOE_ACT_RELU)
+    MOE_ACT_CASE(MOE_ACT_SIGMOID)
+    default: break;
+  }
+#undef MOE_ACT_CASE
+}
+
 // s = sigmoid(z) and c = 1 - s without cancellation (e s, with e = exp(-z) kept finite; NaN passes).
 MOE_DEV void fast_sigmoid_pair(float z, float& s, float& c) {
   float e = __builtin_amdgcn_exp2f(z * -1.44269504088896341f);
@@ -109,91 +126,84 @@ struct DenseEpi {
   int64_t ldp[2];
   int32_t y_f32;       // linear: y and res are fp32
   int32_t act;
-  int32_t vec;         // every matrix above may be moved 4 elements at a time (rows and strides aligned to that)
+  int32_t vec;         // every matrix above may be moved 8 elements at a time (16-byte aligned rows)
 };
 
-// 4 consecutive elements of a row, or the first n of them.
+// 8 consecutive elements of a row as fp32, or the first n of them.
 template <typename T>
-MOE_DEV void load4(const void* base, int64_t off, int n, bool vec, float v[4]) {
+MOE_DEV void load8(const void* base, int64_t off, int n, bool vec, float (&v)[8]) {
   const T* p = (const T*)base + off;
-  if (vec) {
-    typedef T v4 __attribute__((ext_vector_type(4)));
-    const v4 t = *(const v4*)p;
+  if (vec && n == 8) {
+    typedef T v8 __attribute__((ext_vector_type(8)));
+    typedef v8 v8_16 __attribute__((aligned(16)));
+    const v8 t = *(const v8_16*)p;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (float)t[i];
+    for (int c = 0; c < 8; ++c) v[c] = (float)t[c];
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < n ? (float)p[i] : 0.0f;
+    for (int c = 0; c < 8; ++c) v[c] = c < n ? (float)p[c] : 0.0f;
   }
 }
 template <typename T>
-MOE_DEV void store4(void* base, int64_t off, int n, bool vec, const float v[4]) {
+MOE_DEV void store8(void* base, int64_t off, int n, bool vec, const float (&v)[8]) {
   T* p = (T*)base + off;
-  if (vec) {
-    typedef T v4 __attribute__((ext_vector_type(4)));
-    v4 t;
+  if (vec && n == 8) {
+    typedef T v8 __attribute__((ext_vector_type(8)));
+    typedef v8 v8_16 __attribute__((aligned(16)));
+    v8 t;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = (T)v[i];
-    *(v4*)p = t;
+    for (int c = 0; c < 8; ++c) t[c] = (T)v[c];
+    *(v8_16*)p = t;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = (T)v[i];
+    for (int c = 0; c < 8; ++c)
+      if (c < n) p[c] = (T)v[c];
   }
 }
 
-// Output elements (i, j .. j + n - 1), n = 1..4 (n = 4 whenever e.vec): s0 = the fp32 sums (gated: the gate's), s1 = the up's.
+// Outputs (i, j .. j + n - 1), n = 1..8, j a multiple of 8: s0 = the fp32 sums (gated: the gate's), s1 = the up's.
 template <typename T, int KIND>
-MOE_DEV void finish4(const DenseEpi& e, int batch, int64_t i, int j, int n, float s0[4], float s1[4]) {
+MOE_DEV void finish8(const DenseEpi& e, int batch, int64_t i, int j, int n, float (&s0)[8], float (&s1)[8]) {
   const bool vec = e.vec;
   if constexpr (KIND == kEpiStore) {
-    store4<T>(e.y[batch], i * e.ldy[batch] + j, n, vec, s0);
-  } else if constexpr (KIND == kEpiLinear) {
-    if (e.bias[0]) {
-      float b[4];
-      load4<T>(e.bias[0], j, n, vec, b);
+    store8<T>(batch ? e.y[1] : e.y[0], i * (batch ? e.ldy[1] : e.ldy[0]) + j, n, vec, s0);
+    return;
+  }
+  float t[8];
+  if (e.bias[0]) {
+    load8<T>(e.bias[0], j, n, vec, t);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s0[c] += b[c];
-    }
-    if (e.pre[0]) store4<T>(e.pre[0], i * e.ldp[0] + j, n, vec, s0);
-    if (e.act != MOE_ACT_NONE) {
+    for (int c = 0; c < 8; ++c) s0[c] += t[c];
+  }
+  if constexpr (KIND == kEpiGated) {
+    if (e.bias[1]) {
+      load8<T>(e.bias[1], j, n, vec, t);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s0[c] = act_value(e.act, s0[c]);
+      for (int c = 0; c < 8; ++c) s1[c] += t[c];
     }
+  }
+  if (e.pre[0]) {
+    store8<T>(e.pre[0], i * e.ldp[0] + j, n, vec, s0);
+    if constexpr (KIND == kEpiGated) store8<T>(e.pre[1], i * e.ldp[1] + j, n, vec, s1);
+  }
+  act_values(e.act, s0);
+  if constexpr (KIND == kEpiGated) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) s0[c] *= s1[c];
+    store8<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
+  } else {
     if (e.res) {
-      float r[4];
       if (e.y_f32)
-        load4<float>(e.res, i * e.ldr + j, n, vec, r);
+        load8<float>(e.res, i * e.ldr + j, n, vec, t);
       else
-        load4<T>(e.res, i * e.ldr + j, n, vec, r);
+        load8<T>(e.res, i * e.ldr + j, n, vec, t);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s0[c] += r[c];
+      for (int c = 0; c < 8; ++c) s0[c] += t[c];
     }
     if (e.y_f32)
-      store4<float>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
+      store8<float>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
     else
-      store4<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
-  } else {
-    if (e.bias[0]) {
-      float b[4];
-      load4<T>(e.bias[0], j, n, vec, b);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s0[c] += b[c];
-    }
-    if (e.bias[1]) {
-      float b[4];
-      load4<T>(e.bias[1], j, n, vec, b);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s1[c] += b[c];
-    }
-    if (e.pre[0]) {
-      store4<T>(e.pre[0], i * e.ldp[0] + j, n, vec, s0);
-      store4<T>(e.pre[1], i * e.ldp[1] + j, n, vec, s1);
-    }
-    float h[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) h[c] = act_value(e.act, s0[c]) * s1[c];
-    store4<T>(e.y[0], i * e.ldy[0] + j, n, vec, h);
+      store8<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
   }
 }
 
@@ -204,18 +214,50 @@ MOE_DEV void finish4(const DenseEpi& e, int batch, int64_t i, int j, int n, floa
 //   dx          A = dz  kRows, B = W   kCols   (gated: two segments, dg Wg then du Wu, in one sum)
 //   dW          A = dz  kCols, B = x   kCols   (gated: two batches, dg and du)
 enum OperandOrder { kRows = 0, kCols = 1 };
+// Where workgroups share a tile's reduction they leave their fp32 sums in the workspace, and a second launch adds them in
+// split order and applies the epilogue: [split][mat][i][part_ld], mat = the batch (gated: gate, up).
+constexpr size_t kDensePartBytes = 32u << 20;
+constexpr int kMaxSplits = 8;
+
 struct TileArgs {
   const void* a[2];
   const void* b[2];
   int64_t lda[2], ldb[2];
   int32_t M, N, R;         // outputs i, j; reduction per segment
+  int32_t len_a;           // readable elements of A's rows (kRows): R, or more where what follows is zeros
   int32_t nseg, nbatch;    // 1 or 2 each
   int32_t tiles_i, tiles_j;
-  int32_t splits;          // workgroups sharing a tile's reduction, joined through `part`
+  int32_t splits;          // workgroups sharing a tile's reduction
   float* part;
-  int32_t* arrived;        // per tile, zero between calls
+  size_t part_bytes;
   DenseEpi epi;
 };
+// moe_debug_force_dense_plan: the tile kernel (MOE_DENSE_AUTO: chosen by size) and the splits (0: chosen by size).
+struct DensePlan {
+  int kernel, splits;
+};
+extern DensePlan g_dense_plan;
+
+inline size_t split_bytes(int splits, int mats, int64_t M, int64_t N) {
+  return sizeof(float) * splits * mats * (size_t)(M * ((N + 7) / 8 * 8));
+}
+MOE_DEV float* part_at(const TileArgs& a, int split, int mats, int mat, int64_t i, int j) {
+  const int64_t ld = (a.N + 7) / 8 * 8;
+  return a.part + (((int64_t)split * mats + mat) * a.M + i) * ld + j;
+}
+
+// finish8, or for a split reduction the sums parked for the second launch.
+template <typename T, int KIND>
+MOE_DEV void finish_or_park(const TileArgs& a, int split, int batch, int64_t i, int j, int n, float (&s0)[8], float (&s1)[8]) {
+  if (a.splits == 1) {
+    finish8<T, KIND>(a.epi, batch, i, j, n, s0, s1);
+  } else if constexpr (KIND == kEpiGated) {
+    store8<float>(part_at(a, split, 2, 0, i, j), 0, 8, true, s0);
+    store8<float>(part_at(a, split, 2, 1, i, j), 0, 8, true, s1);
+  } else {
+    store8<float>(part_at(a, split, a.nbatch, batch, i, j), 0, 8, true, s0);
+  }
+}
 
 // dz of a backward pass: dz0 = dy * act'(pre0) (dy itself without an activation), or gated dz0 = dh * u * act'(g),
 // dz1 = dh * act(g) with pre0 = g, pre1 = u; rows of ldz elements, zero from N to ldz.  Column sums of the
@@ -235,6 +277,8 @@ struct GradArgs {
 
 // dense_tile_*.hip, dense_grad.hip (dtype: MOE_BF16 or MOE_F16)
 hipError_t launch_tile(int dtype, const TileArgs& a, int order_a, int order_b, int epi_kind, hipStream_t st);
+hipError_t launch_rows(int dtype, const TileArgs& a, int epi_kind, hipStream_t st);  // dense_rows.hip: M <= MOE_DENSE_ROW_TOKENS
+hipError_t launch_finish(int dtype, const TileArgs& a, int epi_kind, hipStream_t st);  // dense_grad.hip
 hipError_t launch_grad_in(int dtype, const GradArgs& a, bool gated, hipStream_t st);
 hipError_t launch_bias_sum(int dtype, const float* part, int runs, int mats, int N, void* db0, void* db1, hipStream_t st);
 

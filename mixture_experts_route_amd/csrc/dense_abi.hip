@@ -4,19 +4,33 @@
 
 namespace moe {
 
-// Workspace: control words, then for a backward pass dz (gated: dg, du) in the operands' type with rows
+DensePlan g_dense_plan = {MOE_DENSE_AUTO, 0};
+
+// Workspace: control words, the sums of split reductions, then for a backward pass dz (gated: dg, du) in the operands' type with rows
 // padded to whole 16-byte chunks, and the bias gradients' partial sums.
 struct DenseWs {
-  size_t dz0, dz1, bias_part, total;
+  size_t part, dz0, dz1, bias_part, total;
   int64_t ldz;
 };
 
 static size_t dense_align(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// Room for the sums of split reductions: what kMaxSplits splits of the largest product would take, up to a limit.
+static size_t part_bytes(const moe_dense_dims* d, int64_t T, bool backward) {
+  size_t n = split_bytes(kMaxSplits, 2, T, d->n_out);
+  if (backward) {
+    const size_t dx = split_bytes(kMaxSplits, 1, T, d->n_in), dw = split_bytes(kMaxSplits, 2, d->n_out, d->n_in);
+    n = dx > dw ? dx : dw;
+    if (n < split_bytes(kMaxSplits, 2, T, d->n_out)) n = split_bytes(kMaxSplits, 2, T, d->n_out);
+  }
+  return n < kDensePartBytes ? n : kDensePartBytes;
+}
+
 // Two matrices whatever the call (one size serves the linear and the gated block).
 static DenseWs dense_ws(const moe_dense_dims* d, int64_t T, bool backward) {
   DenseWs L{};
-  size_t off = kCtrlBytes;
+  L.part = kCtrlBytes;
+  size_t off = dense_align(L.part + part_bytes(d, T, backward));
   if (backward) {
     const int64_t runs = (T + kGradRows - 1) / kGradRows;
     L.ldz = ((int64_t)d->n_out + 7) / 8 * 8;
@@ -69,17 +83,25 @@ static int check_dense_ws(const moe_dense_dims* d, int32_t T, bool backward, con
 
 static int dense_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
-// 4-element accesses: rows start and stay aligned to 4 elements.
-static bool vec4(const void* p, int64_t ld, int elem = 2) { return !p || ((uintptr_t)p % (4 * elem) == 0 && ld % 4 == 0); }
+// 8-element accesses at multiples of 8: rows start and stay 16-byte aligned.
+static bool vec8(const void* p, int64_t ld, int elem = 2) { return !p || ((uintptr_t)p % 16 == 0 && ld * elem % 16 == 0); }
+
+static TileArgs tile_args(const moe_dense_dims* d, int64_t T, bool backward, void* ws) {
+  TileArgs a{};
+  a.part = (float*)((uint8_t*)ws + kCtrlBytes);
+  a.part_bytes = part_bytes(d, T, backward);
+  return a;
+}
 
 static uint8_t* ws_at(void* ws, size_t off) { return (uint8_t*)ws + off; }
 
 // dx = sum over mats of dz[m] W[m], then dW[m] = dz[m]^T x.
 static int run_products(const moe_dense_dims* d, int mats, const void* x, int64_t ldx, int32_t T, const void* const* w,
-                        const int64_t* ldw, const void* const* dz, int64_t ldz, void* dx, int64_t ld_dx, void* const* dw,
-                        const int64_t* ld_dw, hipStream_t st) {
+                        const int64_t* ldw, const void* const* dz, int64_t ldz, int32_t len_dz,
+                        void* dx, int64_t ld_dx, void* const* dw,
+                        const int64_t* ld_dw, void* ws, hipStream_t st) {
   if (dx) {
-    TileArgs a{};
+    TileArgs a = tile_args(d, T, true, ws);
     for (int m = 0; m < mats; ++m) {
       a.a[m] = dz[m];
       a.lda[m] = ldz;
@@ -89,29 +111,30 @@ static int run_products(const moe_dense_dims* d, int mats, const void* x, int64_
     a.M = T;
     a.N = d->n_in;
     a.R = d->n_out;
+    a.len_a = len_dz;
     a.nseg = mats;
     a.nbatch = 1;
     a.epi.y[0] = dx;
     a.epi.ldy[0] = ld_dx;
-    a.epi.vec = d->n_in % 4 == 0 && vec4(dx, ld_dx);
+    a.epi.vec = vec8(dx, ld_dx);
     const int rc = dense_status(launch_tile(d->dtype, a, kRows, kCols, kEpiStore, st));
     if (rc) return rc;
   }
-  TileArgs a{};
+  TileArgs a = tile_args(d, T, true, ws);
   a.M = d->n_out;
   a.N = d->n_in;
   a.R = T;
   a.nseg = 1;
   a.b[0] = a.b[1] = x;
   a.ldb[0] = a.ldb[1] = ldx;
-  a.epi.vec = d->n_in % 4 == 0;
+  a.epi.vec = 1;
   for (int m = 0; m < mats; ++m) {
     if (!dw[m]) continue;
     a.a[a.nbatch] = dz[m];
     a.lda[a.nbatch] = ldz;
     a.epi.y[a.nbatch] = dw[m];
     a.epi.ldy[a.nbatch] = ld_dw[m];
-    a.epi.vec = a.epi.vec && vec4(dw[m], ld_dw[m]);
+    a.epi.vec = a.epi.vec && vec8(dw[m], ld_dw[m]);
     ++a.nbatch;
   }
   return a.nbatch ? dense_status(launch_tile(d->dtype, a, kCols, kCols, kEpiStore, st)) : MOE_OK;
@@ -135,6 +158,12 @@ MOE_API size_t moe_dense_workspace_bytes(const moe_dense_dims* dims, int32_t max
   return dense_ws(dims, max_tokens, backward != 0).total;
 }
 
+MOE_API int moe_debug_force_dense_plan(int32_t kernel, int32_t splits) {
+  if (kernel < MOE_DENSE_AUTO || kernel > MOE_DENSE_TILE_ANY || splits < 0 || splits > kMaxSplits) return MOE_EINVAL;
+  g_dense_plan = {kernel, splits};
+  return MOE_OK;
+}
+
 MOE_API int moe_linear_forward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
                                int64_t ldw, const void* bias_or_null, const void* residual_or_null, int64_t ld_residual,
                                void* y, int64_t ldy, int32_t y_dtype, void* pre_or_null, int64_t ld_pre, void* ws,
@@ -152,14 +181,14 @@ MOE_API int moe_linear_forward(const moe_dense_dims* dims, const void* x, int64_
   m.vec(bias_or_null);
   if (m.rc) return m.rc;
   if ((rc = check_dense_ws(dims, n_tokens, false, ws, ws_bytes))) return rc;
-  TileArgs a{};
+  TileArgs a = tile_args(dims, n_tokens, false, ws);
   a.a[0] = x;
   a.lda[0] = ldx;
   a.b[0] = w;
   a.ldb[0] = ldw;
   a.M = n_tokens;
   a.N = dims->n_out;
-  a.R = dims->n_in;
+  a.R = a.len_a = dims->n_in;
   a.nseg = a.nbatch = 1;
   a.epi.y[0] = y;
   a.epi.ldy[0] = ldy;
@@ -170,9 +199,11 @@ MOE_API int moe_linear_forward(const moe_dense_dims* dims, const void* x, int64_
   a.epi.pre[0] = pre_or_null;
   a.epi.ldp[0] = ld_pre;
   a.epi.act = dims->act;
-  a.epi.vec = dims->n_out % 4 == 0 && vec4(y, ldy, ye) && vec4(residual_or_null, ld_residual, ye) &&
-              vec4(pre_or_null, ld_pre) && vec4(bias_or_null, 0);
-  return dense_status(launch_tile(dims->dtype, a, kRows, kRows, kEpiLinear, (hipStream_t)stream));
+  a.epi.vec = vec8(y, ldy, ye) && vec8(residual_or_null, ld_residual, ye) &&
+              vec8(pre_or_null, ld_pre) && vec8(bias_or_null, 0);
+  hipStream_t st = (hipStream_t)stream;
+  return dense_status(n_tokens <= MOE_DENSE_ROW_TOKENS ? launch_rows(dims->dtype, a, kEpiLinear, st)
+                                                       : launch_tile(dims->dtype, a, kRows, kRows, kEpiLinear, st));
 }
 
 MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens,
@@ -194,7 +225,7 @@ MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t
   m.vec(bias_up_or_null);
   if (m.rc) return m.rc;
   if ((rc = check_dense_ws(dims, n_tokens, false, ws, ws_bytes))) return rc;
-  TileArgs a{};
+  TileArgs a = tile_args(dims, n_tokens, false, ws);
   a.a[0] = x;
   a.lda[0] = ldx;
   a.b[0] = w_gate;
@@ -203,7 +234,7 @@ MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t
   a.ldb[1] = ld_wu;
   a.M = n_tokens;
   a.N = dims->n_out;
-  a.R = dims->n_in;
+  a.R = a.len_a = dims->n_in;
   a.nseg = a.nbatch = 1;
   a.epi.y[0] = h;
   a.epi.ldy[0] = ldh;
@@ -214,9 +245,11 @@ MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t
   a.epi.ldp[0] = ld_gate;
   a.epi.ldp[1] = ld_up;
   a.epi.act = dims->act;
-  a.epi.vec = dims->n_out % 4 == 0 && vec4(h, ldh) && vec4(gate_or_null, ld_gate) && vec4(up_or_null, ld_up) &&
-              vec4(bias_gate_or_null, 0) && vec4(bias_up_or_null, 0);
-  return dense_status(launch_tile(dims->dtype, a, kRows, kRows, kEpiGated, (hipStream_t)stream));
+  a.epi.vec = vec8(h, ldh) && vec8(gate_or_null, ld_gate) && vec8(up_or_null, ld_up) &&
+              vec8(bias_gate_or_null, 0) && vec8(bias_up_or_null, 0);
+  hipStream_t st = (hipStream_t)stream;
+  return dense_status(n_tokens <= MOE_DENSE_ROW_TOKENS ? launch_rows(dims->dtype, a, kEpiGated, st)
+                                                       : launch_tile(dims->dtype, a, kRows, kRows, kEpiGated, st));
 }
 
 MOE_API int moe_linear_backward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
@@ -262,8 +295,9 @@ MOE_API int moe_linear_backward(const moe_dense_dims* dims, const void* x, int64
       return rc;
   }
   const void* dz = make ? ws_at(ws, L.dz0) : dy;
-  return run_products(dims, 1, x, ldx, n_tokens, &w, &ldw, &dz, make ? L.ldz : ld_dy, dx_or_null, ld_dx, &dw_or_null,
-                      &ld_dw, st);
+  return run_products(dims, 1, x, ldx, n_tokens, &w, &ldw, &dz, make ? L.ldz : ld_dy,
+                      make ? (int32_t)L.ldz : dims->n_out, dx_or_null, ld_dx, &dw_or_null,
+                      &ld_dw, ws, st);
 }
 
 MOE_API int moe_gated_backward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens,
@@ -316,7 +350,7 @@ MOE_API int moe_gated_backward(const moe_dense_dims* dims, const void* x, int64_
   const void* dz[2] = {g.dz0, g.dz1};
   void* dw[2] = {dw_gate_or_null, dw_up_or_null};
   const int64_t ld_dw[2] = {ld_dwg, ld_dwu};
-  return products ? run_products(dims, 2, x, ldx, n_tokens, w, ldw, dz, L.ldz, dx_or_null, ld_dx, dw, ld_dw, st) : MOE_OK;
+  return products ? run_products(dims, 2, x, ldx, n_tokens, w, ldw, dz, L.ldz, (int32_t)L.ldz, dx_or_null, ld_dx, dw, ld_dw, ws, st) : MOE_OK;
 }
 
 }  // extern "C"

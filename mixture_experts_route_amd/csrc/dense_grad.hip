@@ -114,6 +114,45 @@ __global__ __launch_bounds__(256) void k_bias_sum(const float* part, int runs, i
   db[c < N ? c : c - N] = (T)s;
 }
 
+// Adds the sums of a split reduction in split order and applies the epilogue: 8 outputs per thread.
+template <typename T, int KIND>
+__global__ __launch_bounds__(256) void k_finish(TileArgs a) {
+  const int chunks = (a.N + 7) / 8;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  constexpr int kMats = KIND == kEpiGated ? 2 : 1;
+  const int mats = KIND == kEpiGated ? 2 : a.nbatch;
+  if (id >= (int64_t)chunks * a.M * (mats / kMats)) return;
+  const int j = (int)(id % chunks) * 8;
+  const int64_t row = id / chunks;
+  const int batch = row >= a.M;
+  const int64_t i = row - (int64_t)batch * a.M;
+  float s[2][8] = {};
+  for (int p = 0; p < a.splits; ++p)
+#pragma unroll
+    for (int m = 0; m < kMats; ++m) {
+      float t[8];
+      load8<float>(part_at(a, p, mats, KIND == kEpiGated ? m : batch, i, j), 0, 8, true, t);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s[m][c] += t[c];
+    }
+  finish8<T, KIND>(a.epi, batch, i, j, a.N - j < 8 ? a.N - j : 8, s[0], s[1]);
+}
+
+template <typename T>
+static void start_finish(const TileArgs& a, int kind, hipStream_t st) {
+  const int64_t threads = (int64_t)((a.N + 7) / 8) * a.M * (kind == kEpiGated ? 1 : a.nbatch);
+  const dim3 grid((uint32_t)((threads + 255) / 256)), block(256);
+  if (kind == kEpiGated) k_finish<T, kEpiGated><<<grid, block, 0, st>>>(a);
+  else if (kind == kEpiLinear) k_finish<T, kEpiLinear><<<grid, block, 0, st>>>(a);
+  else k_finish<T, kEpiStore><<<grid, block, 0, st>>>(a);
+}
+
+hipError_t launch_finish(int dtype, const TileArgs& a, int kind, hipStream_t st) {
+  if (dtype == MOE_BF16) start_finish<__bf16>(a, kind, st);
+  else start_finish<_Float16>(a, kind, st);
+  return hipGetLastError();
+}
+
 hipError_t launch_grad_in(int dtype, const GradArgs& a, bool gated, hipStream_t st) {
   const dim3 grid((uint32_t)((a.T + kGradRows - 1) / kGradRows), (uint32_t)((a.ldz + 511) / 512));
   if (dtype == MOE_BF16) {

@@ -36,19 +36,28 @@ MOE_DEV int chunk_pos(int m, int c) {
   return m * H + (((c >> 1) ^ col_mix<H>(m)) << 4) + ((c & 1) << 3);
 }
 
-// Fragment of outputs o .. o+15 (o a multiple of 16), reduction elements 32 kk ..+31.
+// A lane's LDS byte address for the fragment of outputs o .. o+15 (o a multiple of 16), reduction elements 0..31, of the half
+// tile at byte address `half`.  Fragments of a wave start at o = FR * 16 * (wave's index), FR a power of two, so fragment
+// n's pair index is o / 16 ^ n and every further address differs by a constant or one exclusive or.
+template <int ORDER, int H>
+MOE_DEV uint32_t frag_addr(uint32_t half, int o, int lane) {
+  if constexpr (ORDER == kRows) return half + 2 * chunk_pos<kRows, H>(o + (lane & 15), lane >> 4);
+  const int r = 8 * (lane >> 4) + ((lane & 15) >> 2);
+  return half + 2 * (r * H + (((o >> 4) ^ col_mix<H>(r)) << 4) + ((lane & 3) << 2));
+}
+// Fragment n (16 n outputs on), reduction elements 32 kk ..+31, from such an address; `offset` bytes further on.
 template <typename T, int ORDER, int H>
-MOE_DEV typename Operand<T>::v8 read_frag(const uint16_t* half, int o, int kk, int lane) {
+MOE_DEV typename Operand<T>::v8 read_frag(uint32_t addr, int n, int kk, int offset) {
   typedef typename Operand<T>::v8 v8;
   if constexpr (ORDER == kRows) {
-    return *(const v8*)(half + chunk_pos<kRows, H>(o + (lane & 15), kk * 4 + (lane >> 4)));
+    typedef __attribute__((address_space(3))) const v8 lds8;
+    return *(lds8*)(uintptr_t)((addr ^ (kk * 64)) + (offset + n * 16 * kStepR * 2));
   } else {
     typedef short s4 __attribute__((ext_vector_type(4)));
-    const int r = kk * 32 + 8 * (lane >> 4) + ((lane & 15) >> 2);
-    const uint16_t* p = half + r * H + (((o >> 4) ^ col_mix<H>(r)) << 4) + ((lane & 3) << 2);
     typedef __attribute__((address_space(3))) s4 lds4;
-    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
-    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * H));  // col_mix(r + 4) = col_mix(r)
+    const uint32_t p = (addr ^ (n * 32)) + (offset + kk * 32 * H * 2);
+    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(uintptr_t)p);
+    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(uintptr_t)(p + 4 * H * 2));  // col_mix(r + 4) = col_mix(r)
     struct {
       s4 a, b;
     } v = {lo, hi};
@@ -77,6 +86,41 @@ MOE_DEV TileIndex tile_index(const TileArgs& a, int64_t id, int64_t count) {
   x.ti = (int)group * 8 + (int)(in_group % rows);
   x.tj = (int)(in_group / rows);
   return x;
+}
+
+// ---- epilogue -------------------------------------------------------------------------------------
+// One wave's FI x FJ fragments of outputs (i0.., j0..) (gated: the gate's and the up's) through the wave's own LDS
+// (16-byte chunks swizzled by row), so that a lane finishes 8 consecutive elements and the code of an
+// activation exists once per kernel.
+template <typename T, int KIND, int FI, int FJ>
+MOE_DEV void finish_fragments(const TileArgs& a, const TileIndex& x, int64_t i0, int64_t j0, const float4v (&s0)[FI][FJ],
+                              const float4v (&s1)[FI][FJ], float* lds, int lane) {
+  constexpr int R = FI * 16, C = FJ * 16, kChunks = C / 4, kMask = (kChunks < 8 ? kChunks : 8) - 1;
+  constexpr int kLanes = C / 8, kRowsPer = 64 / kLanes;  // lanes per row, rows per pass
+  auto pos = [&](int r, int c) { return r * C + ((c ^ (r & kMask)) << 2); };
+#pragma unroll
+  for (int f = 0; f < FI; ++f)
+#pragma unroll
+    for (int g = 0; g < FJ; ++g) {
+      const int r = f * 16 + (lane & 15), c = g * 4 + (lane >> 4);
+      *(float4v*)(lds + pos(r, c)) = s0[f][g];
+      if constexpr (KIND == kEpiGated) *(float4v*)(lds + R * C + pos(r, c)) = s1[f][g];
+    }
+  __builtin_amdgcn_wave_barrier();  // one wave: its LDS operations take effect in issue order
+  const int j = (lane % kLanes) * 8;
+  const int n = a.N - (j0 + j) < 8 ? (int)(a.N - (j0 + j)) : 8;
+#pragma clang loop unroll(disable)
+  for (int r = lane / kLanes; r < R; r += kRowsPer) {
+    float v0[8], v1[8];
+    *(float4v*)v0 = *(const float4v*)(lds + pos(r, j / 4));
+    *(float4v*)(v0 + 4) = *(const float4v*)(lds + pos(r, j / 4 + 1));
+    if constexpr (KIND == kEpiGated) {
+      *(float4v*)v1 = *(const float4v*)(lds + R * C + pos(r, j / 4));
+      *(float4v*)(v1 + 4) = *(const float4v*)(lds + R * C + pos(r, j / 4 + 1));
+    }
+    if (i0 + r < a.M && n > 0) finish_or_park<T, KIND>(a, x.split, x.batch, i0 + r, (int)(j0 + j), n, v0, v1);
+  }
+  __builtin_amdgcn_wave_barrier();
 }
 
 // ---- any alignment --------------------------------------------------------------------------------
@@ -138,7 +182,10 @@ __global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
       }
   };
 
-  float4v acc[2][2][2][2] = {};  // [i half][i fragment][j half][j fragment]
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds;
+  const uint32_t addr_a = frag_addr<OA, H>(lds0, wi * 32, lane), addr_b = frag_addr<OB, H>(lds0, wj * 32, lane);
+  constexpr int kHalf = H * kStepR * 2;  // bytes
+  float4v acc[2][2][2][2] = {};  // [i half][j half][i fragment][j fragment]
   fetch(0);
   for (int s = 0; s < total; ++s) {
     __syncthreads();
@@ -159,68 +206,480 @@ __global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int g = 0; g < 2; ++g)
-          fb[h][g] = read_frag<T, OB, H>(lds + (2 + h) * H * kStepR, wj * 32 + g * 16, kk, lane);
+          fb[h][g] = read_frag<T, OB, H>(addr_b, g, kk, (2 + h) * kHalf);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const auto fa = read_frag<T, OA, H>(lds + h * H * kStepR, wi * 32 + f * 16, kk, lane);
+          const auto fa = read_frag<T, OA, H>(addr_a, f, kk, h * kHalf);
 #pragma unroll
           for (int hj = 0; hj < 2; ++hj)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) acc[h][f][hj][g] = Operand<T>::mma(fb[hj][g], fa, acc[h][f][hj][g]);
+            for (int g = 0; g < 2; ++g) acc[h][hj][f][g] = Operand<T>::mma(fb[hj][g], fa, acc[h][hj][f][g]);
         }
     }
   }
 
+  __syncthreads();
+  float* own = (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * 32 * 32;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int64_t i = i0 + h * H + wi * 32 + f * 16 + (lane & 15);
-      if (i >= a.M) continue;
+    for (int hj = 0; hj < (KIND == kEpiGated ? 1 : 2); ++hj)
+      finish_fragments<T, KIND, 2, 2>(a, x, i0 + h * H + wi * 32, j0 + hj * H + wj * 32, acc[h][hj], acc[h][1], own,
+                                      lane);
+}
+
+// ---- 16-byte aligned operands ------------------------------------------------------------------------
+// Asynchronous copy global -> LDS, 16 bytes per lane: lane l's bytes at buffer offset voff land at lds_addr + 16 l
+// (lds_addr wave-uniform); a lane past the resource's bytes writes zeros.  Issued from an assembly block without
+// outputs: the compiler otherwise assumes that any LDS read may depend on any such copy in flight and waits for
+// all of them; here the waits are counted by hand (copies complete in issue order).
+MOE_DEV void copy_to_lds(u32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds_addr), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+
+// Waits until at most N of this wave's copies are outstanding and its LDS reads have returned, then for the
+// workgroup's other waves to have done the same.
+template <int N>
+MOE_DEV void copies_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+// Copies of one operand: WAVES waves, half tiles of H outputs; each wave issues kCopies copies per half tile and step.
+template <int ORDER, int H, int WAVES>
+struct OperandCopy {
+  static constexpr int kCopies = H / 8 / WAVES;  // H * 128 bytes in 1-KiB copies
+  static constexpr int kLines = ORDER == kRows ? 8 : 512 / H;  // lines per copy
+  static constexpr int kLineChunks = ORDER == kRows ? 8 : H / 8;
+  static_assert(kCopies * 8 * WAVES == H, "a half tile is a whole number of copies per wave");
+  // the swizzles of line and line + WAVES * kLines are the same: only the line's bits 0..3 enter them
+  static_assert(kCopies == 1 || (WAVES * kLines) % 16 == 0, "");
+  uint32_t voff[kCopies];  // byte offset of this lane's chunk from the half tile's first element
+  int chunk;               // this lane's chunk of its line
+
+  MOE_DEV void init(int64_t ld, int wave, int lane) {
+    const int line = wave * kLines + lane / kLineChunks, pos = lane % kLineChunks;
+    chunk = ORDER == kRows ? pos ^ (line & 7) : (((pos >> 1) ^ col_mix<H>(line)) << 1) | (pos & 1);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if constexpr (KIND == kEpiGated) {
-          const int64_t j = j0 + wj * 32 + g * 16 + 4 * (lane >> 4);
-          if (j < a.N) {
-            float s0[4], s1[4];
+    for (int d = 0; d < kCopies; ++d)
+      voff[d] = (uint32_t)((line + d * WAVES * kLines) * (uint32_t)ld * 2u + (uint32_t)chunk * 16u);
+  }
+};
+
+// The steps of one half tile, in order: a running address and the steps left, so that issuing a step costs few scalar
+// instructions (a wave issues one instruction per four to five cycles: at ~40 per copy the 64 x 64 tile took 0.35 us a
+// step, whatever was in flight).  SEGS: a second matrix of the same stride follows the first.
+template <int ORDER, int H, int WAVES, bool SEGS>
+struct HalfStream {
+  typedef OperandCopy<ORDER, H, WAVES> Copy;
+  uint64_t p, p1;       // first element of the next step; of the second matrix
+  uint64_t stride;      // bytes from a step to the next
+  int32_t bytes;        // of the resource in a whole step, 0 if the half tile has no outputs
+  int32_t cut;          // what the resource lacks in the last, partial step of a matrix
+  int32_t left, left1;  // steps left in this matrix, the one to be issued included; in the second one
+  int32_t end, end1;    // left's value after a matrix's last step if that is partial and this workgroup's, else one it never takes
+
+  // first: the half tile's first element; outs: its outputs that exist; R: reduction length (kRows: readable elements of a
+  // line); the workgroup takes steps begin .. begin + count - 1 of the one or two matrices of `steps` steps each.
+  MOE_DEV void init(const void* m0, const void* m1, int64_t ld, int64_t o0, int O, int R, int steps, int begin, int count) {
+    const int64_t first = 2 * (ORDER == kRows ? o0 * ld : o0);
+    stride = ORDER == kRows ? 2 * kStepR : 2 * kStepR * (uint64_t)ld;
+    const int n = O - o0 < H ? (int)(O - o0) : H;
+    bytes = n <= 0 ? 0 : ORDER == kRows ? 2 * ((n - 1) * (int32_t)ld + kStepR) : 2 * ((kStepR - 1) * (int32_t)ld + n);
+    const int tail = R - (steps - 1) * kStepR;
+    cut = n <= 0 ? 0 : 2 * (kStepR - tail) * (ORDER == kRows ? 1 : (int32_t)ld);
+    const int in0 = begin >= steps ? 0 : (begin + count < steps ? count : steps - begin);
+    const int b1 = begin > steps ? begin - steps : 0;
+    p = (uint64_t)m0 + first + begin * stride;
+    left = in0;
+    end = cut && begin + count >= steps ? 0 : -(1 << 30);
+    if constexpr (SEGS) {
+      p1 = (uint64_t)m1 + first + b1 * stride;
+      left1 = count - in0;
+      end1 = cut && begin + count >= 2 * steps ? 0 : -(1 << 30);
+      if (left == 0) second();
+    }
+  }
+  MOE_DEV void second() {
+    p = p1;
+    left = left1;
+    end = end1;
+    left1 = 0;
+  }
+  // Issues this wave's copies of the next step.  With no steps left the same number of copies is issued, all past the
+  // resource's end: nothing is read, zeros are written.
+  MOE_DEV void issue(Copy& c, uint32_t lds_addr) {
+    u32x4 rsrc;
+    rsrc[0] = (uint32_t)p;
+    rsrc[1] = (uint32_t)(p >> 32);  // the address's bits 48.. are zero: no stride, no swizzle
+    rsrc[2] = left > 0 ? bytes : 0;
+    rsrc[3] = 0x00020000u;
+    p += stride;
+    --left;
+    const bool tail = left == end;
+    if (__builtin_expect(tail, 0)) {
+      rsrc[2] = bytes - cut;
+      // a kRows line continues past the reduction's end (its next line, or what lies between): those chunks are not read
+      if (ORDER == kRows && c.chunk * 8 >= kStepR - cut / 2)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s0[c] = acc[h][f][0][g][c], s1[c] = acc[h][f][1][g][c];
-            finish4<T, KIND>(a.epi, 0, i, (int)j, a.N - j < 4 ? (int)(a.N - j) : 4, s0, s1);
-          }
-        } else {
+        for (int d = 0; d < Copy::kCopies; ++d) c.voff[d] |= 0x80000000u;
+    }
 #pragma unroll
-          for (int hj = 0; hj < 2; ++hj) {
-            const int64_t j = j0 + hj * H + wj * 32 + g * 16 + 4 * (lane >> 4);
-            if (j < a.N) {
-              float s0[4];
+    for (int d = 0; d < Copy::kCopies; ++d) copy_to_lds(rsrc, lds_addr + d * WAVES * 1024, c.voff[d]);
+    if (ORDER == kRows && __builtin_expect(tail, 0))
 #pragma unroll
-              for (int c = 0; c < 4; ++c) s0[c] = acc[h][f][hj][g][c];
-              finish4<T, KIND>(a.epi, x.batch, i, (int)j, a.N - j < 4 ? (int)(a.N - j) : 4, s0, s0);
-            }
-          }
-        }
+      for (int d = 0; d < Copy::kCopies; ++d) c.voff[d] &= 0x7FFFFFFFu;
+    if constexpr (SEGS) {
+      if (left == 0 && left1 > 0) second();
+    }
+  }
+};
+
+// 64 x 64 tile (gated: 64 x 32 outputs), 4 waves of 32 x 2 x 16, for products with too few large tiles to fill the chip: there
+// a step's arithmetic is short and the time is the copies' latency, so STAGES LDS buffers of one step (64 reduction elements,
+// 16 KB) keep STAGES - 1 steps in flight.  While a step's MFMAs run from registers the next step's fragments are read.
+template <typename T, int OA, int OB, int KIND, int STAGES>
+__global__ __launch_bounds__(256, 2) void k_tile_deep(TileArgs a) {
+  constexpr int W = 4, HI = 64, HJ = 32;
+  constexpr int kBytes = (HI + 2 * HJ) * kStepR * 2;  // of one stage: A, B0, B1
+  typedef typename Operand<T>::v8 v8;
+  constexpr int kCopies = OperandCopy<OA, HI, W>::kCopies + 2 * OperandCopy<OB, HJ, W>::kCopies;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES * kBytes / 2];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave >> 1, wj = wave & 1;
+  const TileIndex x = tile_index(a, blockIdx.x, gridDim.x);
+  constexpr int JT = KIND == kEpiGated ? HJ : 2 * HJ;
+  const int64_t i0 = (int64_t)x.ti * HI, j0 = (int64_t)x.tj * JT;
+
+  const int steps = (a.R + kStepR - 1) / kStepR, total = steps * a.nseg;
+  const int s_begin = (int)((int64_t)total * x.split / a.splits);
+  const int count = (int)((int64_t)total * (x.split + 1) / a.splits) - s_begin;
+
+  constexpr bool kSegs = OA == kRows && OB == kCols, kBatches = OA == kCols;
+  OperandCopy<OA, HI, W> ca;
+  OperandCopy<OB, HJ, W> cb[2];
+  HalfStream<OA, HI, W, kSegs> sa;
+  HalfStream<OB, HJ, W, kSegs> sb[2];
+  ca.init(a.lda[0], wave, lane);
+  sa.init(kBatches && x.batch ? a.a[1] : a.a[0], a.a[1], a.lda[0], i0, a.M, OA == kRows ? a.len_a : a.R, steps, s_begin, count);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    constexpr bool g = KIND == kEpiGated;
+    cb[h].init(a.ldb[g ? h : 0], wave, lane);
+    sb[h].init(a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], j0 + (g ? 0 : h * HJ), a.N, a.R, steps, s_begin, count);
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds;
+  auto copy = [&](uint32_t to) {  // the next step into the stage at `to`
+    sa.issue(ca, to + wave * 1024);
+    sb[0].issue(cb[0], to + HI * kStepR * 2 + wave * 1024);
+    sb[1].issue(cb[1], to + (HI + HJ) * kStepR * 2 + wave * 1024);
+  };
+
+  const uint32_t addr_a = frag_addr<OA, HI>(0, wi * 32, lane);
+  const uint32_t addr_b = frag_addr<OB, HJ>(HI * kStepR * 2, wj * 16, lane);
+  v8 fa[2][2][2], fb[2][2][2];  // [set][fragment or j half][kk]
+  float4v acc[2][2] = {};       // [j half][i fragment]
+  auto read = [&](auto S, uint32_t stage) {
+    constexpr int set = decltype(S)::value;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) fa[set][n][kk] = read_frag<T, OA, HI>(stage + addr_a, n, kk, 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) fb[set][h][kk] = read_frag<T, OB, HJ>(stage + addr_b, 0, kk, h * HJ * kStepR * 2);
+    }
+  };
+  uint32_t here = lds0;  // stage of step k
+  auto next = [&](uint32_t st) { return st == lds0 + (STAGES - 1) * kBytes ? lds0 : st + kBytes; };
+  auto step = [&](auto S) {
+    constexpr int set = decltype(S)::value;
+    copies_barrier<(STAGES - 2) * kCopies>();  // step k + 1 has landed, and every wave has read step k
+    __builtin_amdgcn_sched_barrier(0);
+    copy(here);
+    here = next(here);
+    read(std::integral_constant<int, 1 - set>{}, here);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) acc[h][n] = Operand<T>::mma(fb[set][h][kk], fa[set][n][kk], acc[h][n]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int k = 0; k < STAGES; ++k) copy(lds0 + k * kBytes);
+  copies_barrier<(STAGES - 1) * kCopies>();
+  read(std::integral_constant<int, 0>{}, lds0);
+  int k = 0;
+  for (; k + 1 < count; k += 2) {
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+  }
+  if (k < count) step(std::integral_constant<int, 0>{});
+  copies_barrier<0>();  // no copy may land after the workgroup has given its LDS back
+
+  float* own = (float*)lds + wave * 2 * 512;
+  float4v s[2][2][1];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) s[h][n][0] = acc[h][n];
+#pragma unroll
+  for (int h = 0; h < (KIND == kEpiGated ? 1 : 2); ++h)
+    finish_fragments<T, KIND, 2, 1>(a, x, i0 + wi * 32, j0 + h * HJ + wj * 16, s[h], s[1], own, lane);
+}
+
+// (2 WI FI 16) x (2 WJ FJ 16) tile, WI x WJ waves; a wave's quarter in (i half, j half) is FI x FJ fragments.
+//
+// Two LDS buffers of one step (64 reduction elements) each.  A step is four phases, one per quarter, in the order
+// (A0,B0) (A0,B1) (A1,B1) (A1,B0); while a phase's MFMAs run from registers, the wave reads the fragments that the
+// next phase adds and issues copies of a later step's half tile into the LDS region that was read out last:
+//     phase        MFMA    reads to registers     copies
+//     1 of step k  A0 B0   B1 of k                B0 of k+2
+//     2            A0 B1   A1 of k                B1 of k+2
+//     3            A1 B1   A0 of k+1              A1 of k+2
+//     4            A1 B0   B0 of k+1 (over B1)    A0 of k+3
+// A half tile is thus read six to seven phases after its copies were issued, with one barrier per phase that
+// waits only for the copies older than the last six half tiles.
+template <typename T, int OA, int OB, int KIND, int WI, int WJ, int FI, int FJ>
+__global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
+  constexpr int W = WI * WJ, HI = WI * FI * 16, HJ = WJ * FJ * 16;
+  constexpr int kBuf = 2 * (HI + HJ) * kStepR;  // elements of one buffer: A0 A1 B0 B1
+  typedef typename Operand<T>::v8 v8;
+  constexpr int DA = OperandCopy<OA, HI, W>::kCopies, DB = OperandCopy<OB, HJ, W>::kCopies;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[2 * kBuf];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave / WJ, wj = wave % WJ;
+  const TileIndex x = tile_index(a, blockIdx.x, gridDim.x);
+  constexpr int JT = KIND == kEpiGated ? HJ : 2 * HJ;
+  const int64_t i0 = (int64_t)x.ti * 2 * HI, j0 = (int64_t)x.tj * JT;
+
+  const int steps = (a.R + kStepR - 1) / kStepR, total = steps * a.nseg;
+  const int s_begin = (int)((int64_t)total * x.split / a.splits);
+  const int count = (int)((int64_t)total * (x.split + 1) / a.splits) - s_begin;
+
+  constexpr bool kSegs = OA == kRows && OB == kCols, kBatches = OA == kCols;  // which products have them
+  OperandCopy<OA, HI, W> ca;
+  OperandCopy<OB, HJ, W> cb[2];
+  HalfStream<OA, HI, W, kSegs> sa[2];
+  HalfStream<OB, HJ, W, kSegs> sb[2];
+  ca.init(a.lda[0], wave, lane);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    constexpr bool g = KIND == kEpiGated;
+    sa[h].init(kBatches && x.batch ? a.a[1] : a.a[0], a.a[1], a.lda[0], i0 + h * HI, a.M, OA == kRows ? a.len_a : a.R, steps,
+               s_begin, count);
+    cb[h].init(a.ldb[g ? h : 0], wave, lane);
+    sb[h].init(a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], j0 + (g ? 0 : h * HJ), a.N, a.R, steps, s_begin, count);
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds;
+  const uint32_t mine = lds0 + wave * 1024;
+  // half tile h of its stream's next step, into LDS buffer `buf`
+  auto copy_a = [&](int h, int buf) { sa[h].issue(ca, mine + 2 * (buf * kBuf + h * HI * kStepR)); };
+  auto copy_b = [&](int h, int buf) { sb[h].issue(cb[h], mine + 2 * (buf * kBuf + (2 * HI + h * HJ) * kStepR)); };
+
+  v8 fa[2][FI][2], fb[2][FJ][2];
+  float4v acc[2][2][FI][FJ] = {};  // [i half][j half]
+  uint32_t addr_a = frag_addr<OA, HI>(lds0, wi * FI * 16, lane);
+  uint32_t addr_b = frag_addr<OB, HJ>(lds0 + 2 * 2 * HI * kStepR, wj * FJ * 16, lane);
+  auto read_a = [&](v8 (&f)[FI][2], int h, int buf) {
+    asm volatile("" : "+v"(addr_a));  // the addresses derived from it are formed here, not kept in registers
+    const uint32_t base = addr_a + buf * kBuf * 2;
+#pragma unroll
+    for (int n = 0; n < FI; ++n)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) f[n][kk] = read_frag<T, OA, HI>(base, n, kk, h * HI * kStepR * 2);
+  };
+  auto read_b = [&](v8 (&f)[FJ][2], int h, int buf) {
+    asm volatile("" : "+v"(addr_b));
+    const uint32_t base = addr_b + buf * kBuf * 2;
+#pragma unroll
+    for (int n = 0; n < FJ; ++n)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) f[n][kk] = read_frag<T, OB, HJ>(base, n, kk, h * HJ * kStepR * 2);
+  };
+  auto multiply = [&](int h, int hj, const v8 (&xa)[FI][2], const v8 (&xb)[FJ][2]) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int f = 0; f < FI; ++f)
+#pragma unroll
+        for (int g = 0; g < FJ; ++g) acc[h][hj][f][g] = Operand<T>::mma(xb[g][kk], xa[f][kk], acc[h][hj][f][g]);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  // one step; `p` is the register set that holds B0 (B1 goes to the other one), equal to the LDS buffer
+  auto step = [&](auto P) {
+    constexpr int p = decltype(P)::value, q = 1 - p;
+    copies_barrier<4 * DA + 2 * DB>();
+    __builtin_amdgcn_sched_barrier(0);
+    copy_b(0, p);
+    read_b(fb[q], 1, p);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(0, 0, fa[0], fb[p]);
+    __builtin_amdgcn_sched_barrier(0);
+    copies_barrier<3 * DA + 3 * DB>();
+    __builtin_amdgcn_sched_barrier(0);
+    copy_b(1, p);
+    read_a(fa[1], 1, p);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(0, 1, fa[0], fb[q]);
+    __builtin_amdgcn_sched_barrier(0);
+    copies_barrier<2 * DA + 4 * DB>();
+    __builtin_amdgcn_sched_barrier(0);
+    copy_a(1, p);
+    read_a(fa[0], 0, q);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1, 1, fa[1], fb[q]);
+    __builtin_amdgcn_sched_barrier(0);
+    copies_barrier<3 * DA + 3 * DB>();
+    __builtin_amdgcn_sched_barrier(0);
+    copy_a(0, q);
+    read_b(fb[q], 0, q);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1, 0, fa[1], fb[p]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  copy_a(0, 0);
+  copy_b(0, 0);
+  copy_b(1, 0);
+  copy_a(1, 0);
+  copy_a(0, 1);
+  copy_b(0, 1);
+  copy_b(1, 1);
+  copy_a(1, 1);
+  copies_barrier<3 * DA + 3 * DB>();
+  read_a(fa[0], 0, 0);
+  read_b(fb[0], 0, 0);
+  copies_barrier<3 * DA + 3 * DB>();
+  copy_a(0, 0);
+  int k = 0;
+  for (; k + 1 < count; k += 2) {
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+  }
+  if (k < count) step(std::integral_constant<int, 0>{});
+  copies_barrier<0>();  // no copy may land after the workgroup has given its LDS back
+
+  float* own = (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * FI * FJ * 256;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int hj = 0; hj < (KIND == kEpiGated ? 1 : 2); ++hj)
+      finish_fragments<T, KIND, FI, FJ>(a, x, i0 + h * HI + wi * FI * 16, j0 + hj * HJ + wj * FJ * 16, acc[h][hj],
+                                        acc[h][1], own, lane);
+}
+
+// Row lengths, strides and addresses of both operands are whole 16-byte chunks.
+inline bool whole_chunks(const void* p, int64_t ld, int64_t len) {
+  return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && len % 8 == 0;
+}
+
+// The plan with the least estimated time, in microseconds.  Measured at bf16 and 64 reduction elements per step: a CU draws
+// 45 to 50 KB per microsecond from the L2 whatever is in flight, so a step of a lone workgroup on its CU takes 0.36 us
+// with a 64 x 64 tile (16 KB), 0.63 us with 128 x 128, 1.5 us with 256 x 256; two workgroups side by side (which the two
+// smaller tiles allow) take 0.52 and 0.92 us for a step of each.  Per round of tiles the prologue and epilogue add
+// 1, 2 and 5 us; a split reduction adds a launch and the traffic of its fp32 sums.
+template <int OA, int KIND>
+DensePlan plan_tile(const TileArgs& a) {
+  const int64_t steps = (int64_t)((a.R + kStepR - 1) / kStepR) * a.nseg;
+  const int mats = KIND == kEpiGated ? 2 : a.nbatch;
+  DensePlan best = {MOE_DENSE_TILE256, 1};
+  double least = 1e30;
+  for (int kernel : {MOE_DENSE_TILE64, MOE_DENSE_TILE128, MOE_DENSE_TILE256}) {
+    const int ti = kernel == MOE_DENSE_TILE64 ? 64 : kernel == MOE_DENSE_TILE128 ? 128 : 256, tj = KIND == kEpiGated ? ti / 2 : ti;
+    const int64_t tiles = (((int64_t)a.M + ti - 1) / ti) * (((int64_t)a.N + tj - 1) / tj) * a.nbatch;
+    const double lone = kernel == MOE_DENSE_TILE64 ? 0.36 : kernel == MOE_DENSE_TILE128 ? 0.63 : 1.55;
+    const double pair = kernel == MOE_DENSE_TILE64 ? 0.52 : kernel == MOE_DENSE_TILE128 ? 0.92 : 3.1;
+    const double round = kernel == MOE_DENSE_TILE64 ? 1 : kernel == MOE_DENSE_TILE128 ? 2 : 5;
+    for (int splits = 1; splits <= kMaxSplits; ++splits) {
+      const size_t part = split_bytes(splits, mats, a.M, a.N);
+      if (splits > 1 && (part > a.part_bytes || tiles * splits > 512 || steps / splits < 4)) break;
+      const int64_t per_cu = (tiles * splits + 255) / 256;
+      double t = 3.0 + (per_cu / 2 * pair + per_cu % 2 * lone) * ((steps + splits - 1) / splits) + (per_cu + 1) / 2 * round;
+      if (splits > 1) t += 2.5 + 2.0 * part / 4e6;
+      if (t < least) {
+        least = t;
+        best = {kernel, splits};
       }
     }
+  }
+  return best;
+}
+
+// Tiles of TI x TJ outputs; false if the launch would exceed a grid's limit.
+template <int TI, int TJ, int THREADS>
+bool set_tiles(TileArgs& a, int64_t* count) {
+  a.tiles_i = (a.M + TI - 1) / TI;
+  a.tiles_j = (a.N + TJ - 1) / TJ;
+  *count = (int64_t)a.tiles_i * a.tiles_j * a.nbatch * a.splits;
+  return *count <= (int64_t)0xFFFFFFFF / THREADS;
+}
+
+template <typename T, int OA, int OB, int KIND, int WI, int WJ, int FI, int FJ>
+hipError_t start_tile(TileArgs a, hipStream_t st) {
+  int64_t count;
+  if (!set_tiles<2 * WI * FI * 16, (KIND == kEpiGated ? 1 : 2) * WJ * FJ * 16, 64 * WI * WJ>(a, &count))
+    return hipErrorInvalidConfiguration;
+  k_tile<T, OA, OB, KIND, WI, WJ, FI, FJ><<<dim3((uint32_t)count), dim3(64 * WI * WJ), 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int OA, int OB, int KIND>
+hipError_t start_plan(TileArgs a, int kernel, hipStream_t st) {
+  int64_t count;
+  switch (kernel) {
+    case MOE_DENSE_TILE64:
+      if (!set_tiles<64, KIND == kEpiGated ? 32 : 64, 256>(a, &count)) return hipErrorInvalidConfiguration;
+      k_tile_deep<T, OA, OB, KIND, 5><<<dim3((uint32_t)count), dim3(256), 0, st>>>(a);
+      return hipGetLastError();
+    case MOE_DENSE_TILE128: return start_tile<T, OA, OB, KIND, 2, 2, 2, 2>(a, st);
+    case MOE_DENSE_TILE256: return start_tile<T, OA, OB, KIND, 2, 4, 4, 2>(a, st);
+    default:
+      if (!set_tiles<128, KIND == kEpiGated ? 64 : 128, 256>(a, &count)) return hipErrorInvalidConfiguration;
+      k_tile_any<T, OA, OB, KIND><<<dim3((uint32_t)count), dim3(256), 0, st>>>(a);
+      return hipGetLastError();
+  }
+}
+
+template <typename T, int OA, int OB, int KIND>
+hipError_t launch_tile_k(const TileArgs& args, hipStream_t st) {
+  TileArgs a = args;
+  bool whole = true;
+  for (int m = 0; m < (a.nseg > 1 || a.nbatch > 1 ? 2 : 1); ++m)
+    whole = whole && whole_chunks(a.a[m], a.lda[m], OA == kRows ? a.len_a : a.M);
+  for (int m = 0; m < (KIND == kEpiGated || a.nseg > 1 ? 2 : 1); ++m)
+    whole = whole && whole_chunks(a.b[m], a.ldb[m], OB == kRows ? a.R : a.N);
+  if (a.nseg > 1) whole = whole && a.ldb[0] == a.ldb[1];
+  DensePlan plan = whole ? plan_tile<OA, KIND>(a) : DensePlan{MOE_DENSE_TILE_ANY, 1};
+  if (whole && g_dense_plan.kernel != MOE_DENSE_AUTO) plan = {g_dense_plan.kernel, 1};
+  if (g_dense_plan.splits && plan.kernel != MOE_DENSE_TILE_ANY) {
+    plan.splits = g_dense_plan.splits;
+    while (plan.splits > 1 && split_bytes(plan.splits, KIND == kEpiGated ? 2 : a.nbatch, a.M, a.N) > a.part_bytes)
+      --plan.splits;
+  }
+  a.splits = plan.splits;
+  const hipError_t e = start_plan<T, OA, OB, KIND>(a, plan.kernel, st);
+  return e != hipSuccess || a.splits == 1 ? e : launch_finish(__is_same(T, __bf16) ? MOE_BF16 : MOE_F16, a, KIND, st);
 }
 
 template <typename T>
-hipError_t launch_tile_t(const TileArgs& args, int oa, int ob, int kind, hipStream_t st) {
-  TileArgs a = args;
-  const int jt = kind == kEpiGated ? 64 : 128;
-  a.tiles_i = (a.M + 127) / 128;
-  a.tiles_j = (a.N + jt - 1) / jt;
-  a.splits = 1;
-  const int64_t count = (int64_t)a.tiles_i * a.tiles_j * a.nbatch;
-  if (count > (int64_t)0xFFFFFFFF / 256) return hipErrorInvalidConfiguration;
-  const dim3 grid((uint32_t)count), block(256);
-  if (oa == kRows && ob == kRows && kind == kEpiLinear) k_tile_any<T, kRows, kRows, kEpiLinear><<<grid, block, 0, st>>>(a);
-  else if (oa == kRows && ob == kRows && kind == kEpiGated) k_tile_any<T, kRows, kRows, kEpiGated><<<grid, block, 0, st>>>(a);
-  else if (oa == kRows && ob == kCols && kind == kEpiStore) k_tile_any<T, kRows, kCols, kEpiStore><<<grid, block, 0, st>>>(a);
-  else if (oa == kCols && ob == kCols && kind == kEpiStore) k_tile_any<T, kCols, kCols, kEpiStore><<<grid, block, 0, st>>>(a);
-  else return hipErrorInvalidValue;
-  return hipGetLastError();
+hipError_t launch_tile_t(const TileArgs& a, int oa, int ob, int kind, hipStream_t st) {
+  if (oa == kRows && ob == kRows && kind == kEpiLinear) return launch_tile_k<T, kRows, kRows, kEpiLinear>(a, st);
+  if (oa == kRows && ob == kRows && kind == kEpiGated) return launch_tile_k<T, kRows, kRows, kEpiGated>(a, st);
+  if (oa == kRows && ob == kCols && kind == kEpiStore) return launch_tile_k<T, kRows, kCols, kEpiStore>(a, st);
+  if (oa == kCols && ob == kCols && kind == kEpiStore) return launch_tile_k<T, kCols, kCols, kEpiStore>(a, st);
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_tile_bf16(const TileArgs& a, int oa, int ob, int kind, hipStream_t st);

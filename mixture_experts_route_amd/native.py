@@ -34,7 +34,7 @@ EXPORTS = [
     "moe_pool_get_table", "moe_pool_get_profile", "moe_profile_seed", "moe_pool_lend", "moe_pool_unlend",
     "moe_pool_debug_fail_copies", "moe_prefill_plan_get", "moe_debug_force_prefill_plan",
     "moe_dense_workspace_bytes", "moe_linear_forward", "moe_linear_backward", "moe_gated_forward",
-    "moe_gated_backward",
+    "moe_gated_backward", "moe_debug_force_dense_plan",
 ]
 
 
@@ -123,6 +123,7 @@ _sig = {
     "moe_prefill_plan_get": (ctypes.c_int, [_D, _I, ctypes.POINTER(moe_prefill_plan)]),
     "moe_debug_force_prefill_plan": (ctypes.c_int, [ctypes.POINTER(moe_prefill_plan)]),
     "moe_dense_workspace_bytes": (_SZ, [_DD, _I, _I]),
+    "moe_debug_force_dense_plan": (ctypes.c_int, [_I, _I]),
     "moe_linear_forward": (ctypes.c_int, [_DD, _P, _L, _I, _P, _L, _P, _P, _L, _P, _L, _I, _P, _L, _P, _SZ, _P]),
     "moe_linear_backward": (ctypes.c_int, [_DD, _P, _L, _I, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _SZ, _P]),
     "moe_gated_forward": (ctypes.c_int, [_DD, _P, _L, _I, _P, _L, _P, _L, _P, _P, _P, _L, _P, _L, _P, _L, _P, _SZ,
@@ -289,85 +290,110 @@ def moe_dense_workspace_bytes(d: moe_dense_dims, max_tokens: int, backward: bool
     return _lib.moe_dense_workspace_bytes(ctypes.byref(d), max_tokens, int(backward))
 
 
-class _DenseCall:
-    """Marshals one dense call: a tensor's sizes, strides, type and device are checked here (the C
-    interface sees addresses only), and the call runs on the tensors' device."""
+MOE_DENSE_AUTO, MOE_DENSE_TILE64, MOE_DENSE_TILE128, MOE_DENSE_TILE256, MOE_DENSE_TILE_ANY = range(5)
 
-    def __init__(self, name: str, x, ws, stream):
-        self.name, self.device = name, x.device
-        self.ws = (self._on_device("ws", ws).data_ptr(), ws.numel() * ws.element_size())
-        self.stream = stream
 
-    def _fail(self, arg: str):
-        raise MoeError(MOE_EINVAL, f"{self.name}, {arg}")
+def moe_debug_force_dense_plan(kernel: int = MOE_DENSE_AUTO, splits: int = 0):
+    _check(_lib.moe_debug_force_dense_plan(kernel, splits), "moe_debug_force_dense_plan")
 
-    def _on_device(self, arg: str, t):
-        if not t.is_cuda or t.device != self.device:
-            self._fail(arg)
-        return t
 
-    def mat(self, arg: str, t, rows: int, cols: int, dtype: int):
-        """(address, row stride) of a row-major [rows][cols] tensor; (None, 0) for None."""
-        if t is None:
-            return None, 0
-        self._on_device(arg, t)
-        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or dtype_code(t) != dtype:
-            self._fail(arg)
-        if cols > 1 and t.stride(1) != 1:
-            self._fail(arg)
-        return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+# Tensor types that hold a dtype code's values (16-bit integers: bf16 codes, as elsewhere).
+_DENSE_TYPES = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16, torch.uint16),
+                MOE_F16: (torch.float16,)}
 
-    def vec(self, arg: str, t, n: int, dtype: int):
-        if t is None:
-            return None
-        self._on_device(arg, t)
-        if t.dim() != 1 or t.shape[0] != n or dtype_code(t) != dtype or (n > 1 and t.stride(0) != 1):
-            self._fail(arg)
-        return t.data_ptr()
 
-    def __call__(self, d: moe_dense_dims, *args):
-        with torch.cuda.device(self.device):
-            stream = _stream(self.stream)
-            _check(getattr(_lib, self.name)(ctypes.byref(d), *args, *self.ws, stream), self.name)
+# The device's current stream as an address, without the stream object that torch.cuda.current_stream builds
+# (2.9 against 0.1 us of host time per call, measured, where a one-token kernel takes 4 us).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _dense_fail(where: str):
+    raise MoeError(MOE_EINVAL, where)
+
+
+def _mat(t, rows: int, cols: int, types, device, where: str):
+    """(address, row stride) of a row-major [rows][cols] tensor.  The C interface sees addresses only: a tensor's
+    type, sizes, strides and device are checked here."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype not in types or t.device != device:
+        _dense_fail(where)
+    if stride[1] != 1 and cols > 1:
+        _dense_fail(where)
+    return t.data_ptr(), (stride[0] if rows > 1 else cols)
+
+
+def _opt_mat(t, rows: int, cols: int, types, device, where: str):
+    return (None, 0) if t is None else _mat(t, rows, cols, types, device, where)
+
+
+def _opt_vec(t, n: int, types, device, where: str):
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.dtype not in types or t.device != device or (n > 1 and t.stride(0) != 1):
+        _dense_fail(where)
+    return t.data_ptr()
+
+
+def _dense_call(name: str, d: moe_dense_dims, device, ws, stream, args):
+    """The C call on the tensors' device, on ``stream`` or that device's current one."""
+    if device.type != "cuda" or ws.device != device or not ws.is_contiguous():
+        _dense_fail(f"{name}, device or ws")
+    f, index = getattr(_lib, name), device.index
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        rc = f(ctypes.byref(d), *args, ws.data_ptr(), ws.nbytes, st)
+    else:
+        with torch.cuda.device(index):
+            rc = f(ctypes.byref(d), *args, ws.data_ptr(), ws.nbytes, st)
+    if rc != MOE_OK:
+        raise MoeError(rc, name)
 
 
 def moe_linear_forward(d: moe_dense_dims, x, n_tokens: int, w, y, ws, bias=None, residual=None, pre=None, stream=None):
     """``y = act(x w^T + bias) + residual``; y and residual in the operands' type or float32."""
-    c, (K, N, T) = _DenseCall("moe_linear_forward", x, ws, stream), (d.n_in, d.n_out, n_tokens)
+    K, N, T, dev, ty, at = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_linear_forward, "
     yd = dtype_code(y)
-    c(d, *c.mat("x", x, T, K, d.dtype), T, *c.mat("w", w, N, K, d.dtype), c.vec("bias", bias, N, d.dtype),
-      *c.mat("residual", residual, T, N, yd), *c.mat("y", y, T, N, yd), yd, *c.mat("pre", pre, T, N, d.dtype))
+    yt = _DENSE_TYPES[yd]
+    _dense_call("moe_linear_forward", d, dev, ws, stream, (
+        *_mat(x, T, K, ty, dev, at + "x"), T, *_mat(w, N, K, ty, dev, at + "w"), _opt_vec(bias, N, ty, dev, at + "bias"),
+        *_opt_mat(residual, T, N, yt, dev, at + "residual"), *_mat(y, T, N, yt, dev, at + "y"), yd,
+        *_opt_mat(pre, T, N, ty, dev, at + "pre")))
 
 
 def moe_linear_backward(d: moe_dense_dims, x, n_tokens: int, w, dy, ws, pre=None, dx=None, dw=None, dbias=None,
                         stream=None):
     """Gradients of ``act(x w^T + bias)`` from ``dy`` and the saved ``pre``; outputs that are None are not computed."""
-    c, (K, N, T) = _DenseCall("moe_linear_backward", x, ws, stream), (d.n_in, d.n_out, n_tokens)
-    c(d, *c.mat("x", x, T, K, d.dtype), T, *c.mat("w", w, N, K, d.dtype), *c.mat("pre", pre, T, N, d.dtype),
-      *c.mat("dy", dy, T, N, d.dtype), *c.mat("dx", dx, T, K, d.dtype), *c.mat("dw", dw, N, K, d.dtype),
-      c.vec("dbias", dbias, N, d.dtype))
+    K, N, T, dev, ty, at = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_linear_backward, "
+    _dense_call("moe_linear_backward", d, dev, ws, stream, (
+        *_mat(x, T, K, ty, dev, at + "x"), T, *_mat(w, N, K, ty, dev, at + "w"),
+        *_opt_mat(pre, T, N, ty, dev, at + "pre"), *_mat(dy, T, N, ty, dev, at + "dy"),
+        *_opt_mat(dx, T, K, ty, dev, at + "dx"), *_opt_mat(dw, N, K, ty, dev, at + "dw"),
+        _opt_vec(dbias, N, ty, dev, at + "dbias")))
 
 
 def moe_gated_forward(d: moe_dense_dims, x, n_tokens: int, w_gate, w_up, h, ws, gate_bias=None, up_bias=None, gate=None,
                       up=None, stream=None):
     """``h = act(x w_gate^T + gate_bias) * (x w_up^T + up_bias)``; ``gate`` and ``up`` receive the two factors'
     pre-activations for the backward pass."""
-    c, (K, N, T) = _DenseCall("moe_gated_forward", x, ws, stream), (d.n_in, d.n_out, n_tokens)
-    c(d, *c.mat("x", x, T, K, d.dtype), T, *c.mat("w_gate", w_gate, N, K, d.dtype),
-      *c.mat("w_up", w_up, N, K, d.dtype), c.vec("gate_bias", gate_bias, N, d.dtype),
-      c.vec("up_bias", up_bias, N, d.dtype), *c.mat("h", h, T, N, d.dtype), *c.mat("gate", gate, T, N, d.dtype),
-      *c.mat("up", up, T, N, d.dtype))
+    K, N, T, dev, ty, at = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_gated_forward, "
+    _dense_call("moe_gated_forward", d, dev, ws, stream, (
+        *_mat(x, T, K, ty, dev, at + "x"), T, *_mat(w_gate, N, K, ty, dev, at + "w_gate"),
+        *_mat(w_up, N, K, ty, dev, at + "w_up"), _opt_vec(gate_bias, N, ty, dev, at + "gate_bias"),
+        _opt_vec(up_bias, N, ty, dev, at + "up_bias"), *_mat(h, T, N, ty, dev, at + "h"),
+        *_opt_mat(gate, T, N, ty, dev, at + "gate"), *_opt_mat(up, T, N, ty, dev, at + "up")))
 
 
 def moe_gated_backward(d: moe_dense_dims, x, n_tokens: int, w_gate, w_up, gate, up, dh, ws, dx=None, dw_gate=None,
                        dw_up=None, dgate_bias=None, dup_bias=None, stream=None):
     """Gradients of moe_gated_forward from ``dh`` and the saved ``gate`` and ``up``; None: not computed."""
-    c, (K, N, T) = _DenseCall("moe_gated_backward", x, ws, stream), (d.n_in, d.n_out, n_tokens)
-    c(d, *c.mat("x", x, T, K, d.dtype), T, *c.mat("w_gate", w_gate, N, K, d.dtype),
-      *c.mat("w_up", w_up, N, K, d.dtype), *c.mat("gate", gate, T, N, d.dtype), *c.mat("up", up, T, N, d.dtype),
-      *c.mat("dh", dh, T, N, d.dtype), *c.mat("dx", dx, T, K, d.dtype), *c.mat("dw_gate", dw_gate, N, K, d.dtype),
-      *c.mat("dw_up", dw_up, N, K, d.dtype), c.vec("dgate_bias", dgate_bias, N, d.dtype),
-      c.vec("dup_bias", dup_bias, N, d.dtype))
+    K, N, T, dev, ty, at = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_gated_backward, "
+    _dense_call("moe_gated_backward", d, dev, ws, stream, (
+        *_mat(x, T, K, ty, dev, at + "x"), T, *_mat(w_gate, N, K, ty, dev, at + "w_gate"),
+        *_mat(w_up, N, K, ty, dev, at + "w_up"), *_mat(gate, T, N, ty, dev, at + "gate"),
+        *_mat(up, T, N, ty, dev, at + "up"), *_mat(dh, T, N, ty, dev, at + "dh"),
+        *_opt_mat(dx, T, K, ty, dev, at + "dx"), *_opt_mat(dw_gate, N, K, ty, dev, at + "dw_gate"),
+        *_opt_mat(dw_up, N, K, ty, dev, at + "dw_up"), _opt_vec(dgate_bias, N, ty, dev, at + "dgate_bias"),
+        _opt_vec(dup_bias, N, ty, dev, at + "dup_bias")))
 
 
 def raw(name: str):

@@ -128,6 +128,12 @@ def test_optional_arguments_refused(N):
     assert gated_bwd(N, d, dbg=P + 1) == N.MOE_EINVAL
 
 
+def test_forced_plan_refused(N):
+    f = N.raw("moe_debug_force_dense_plan")
+    for kernel, splits in ((-1, 0), (5, 0), (0, -1), (0, 9)):
+        assert f(kernel, splits) == N.MOE_EINVAL
+
+
 def test_layer_calls_refuse_fp16(N):
     """MOE_F16 is a dense operand type only: the layer's calls keep refusing it."""
     d = N.dims(2048, 768, 512, 10, 1)

@@ -230,6 +230,28 @@ def test_large(N, shape):
     run_gated_backward(N, gen, *shape, F16, 1)
 
 
+@pytest.mark.parametrize("splits", [1, 2, 3, 8])
+@pytest.mark.parametrize("kernel", [1, 2, 3, 4], ids=["tile64", "tile128", "tile256", "any"])
+def test_every_kernel_and_split(N, kernel, splits):
+    """Each tile kernel at sizes inside, at and past its tile, with the reduction in one piece and in parts (fewer steps
+    than parts among them), and the few-token kernel in as many parts."""
+    N.moe_debug_force_dense_plan(kernel, splits)
+    try:
+        for shape in ((20, 64, 40), (64, 320, 64), (130, 1096, 264), (257, 512, 520), (600, 200, 136)):
+            gen = gen_for(17, kernel, splits, *shape)
+            run_linear_forward(N, gen, *shape, BF16, 1, bias=True, res=True, ydt=F32, save=True)
+            run_gated_forward(N, gen, *shape, F16, 1, bias=True, save=True)
+            run_linear_backward(N, gen, *shape, F16, 1)
+            run_gated_backward(N, gen, *shape, BF16, 3)
+        for shape in ((1, 64, 24), (7, 1000, 264), (16, 4160, 40)):
+            gen = gen_for(18, kernel, splits, *shape)
+            run_linear_forward(N, gen, *shape, BF16, 1, bias=True, res=True, ydt=F32, save=True)
+            run_gated_forward(N, gen, *shape, F16, 1, bias=True, save=True)
+            run_gated_forward(N, gen, *shape, BF16, 4, bias=True, pad=1, offset=1)
+    finally:
+        N.moe_debug_force_dense_plan()
+
+
 def test_residual_in_place(N):
     """y on r exactly: every element is read before it is written."""
     for T, K, M, dt, ydt in ((4, 256, 512, BF16, F32), (300, 512, 264, F16, F16), (40, 96, 33, BF16, BF16)):
@@ -246,7 +268,7 @@ def test_residual_in_place(N):
 @pytest.mark.parametrize("dt", [BF16, F16], ids=["bf16", "fp16"])
 def test_equal_calls_give_equal_bits(N, dt):
     """Twice the same call, and (up to the stated count) a token alone and in any batch."""
-    for K, M in ((2048, 768), (256, 4104), (1000, 50)):
+    for K, M in ((2048, 768), (256, 4104), (1000, 50), (4096, 520), (2048, 8200)):
         gen = gen_for(11, K)
         x = rnd(gen, (N.MOE_DENSE_ROW_TOKENS, K), dt)
         w, w2 = rnd(gen, (M, K), dt, K ** -0.5), rnd(gen, (M, K), dt, K ** -0.5)
