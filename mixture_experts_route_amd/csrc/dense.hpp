@@ -224,12 +224,13 @@ struct TileArgs {
   const void* b[2];
   int64_t lda[2], ldb[2];
   int32_t M, N, R;         // outputs i, j; reduction per segment
-  int32_t len_a;           // readable elements of A's rows (kRows): R, or more where what follows is zeros
+  int32_t len_a, len_b;    // readable elements of A's and B's rows (kRows): R, or more where what follows is zeros
   int32_t nseg, nbatch;    // 1 or 2 each
   int32_t tiles_i, tiles_j;
   int32_t splits;          // workgroups sharing a tile's reduction
   float* part;
   size_t part_bytes;
+  uint16_t *pack_a, *pack_b[2];  // workspace for copies of the operands with whole 16-byte rows (NULL: none)
   DenseEpi epi;
 };
 // moe_debug_force_dense_plan: the tile kernel (MOE_DENSE_AUTO: chosen by size) and the splits (0: chosen by size).
@@ -278,6 +279,17 @@ struct GradArgs {
 // dense_tile_*.hip, dense_grad.hip (dtype: MOE_BF16 or MOE_F16)
 hipError_t launch_tile(int dtype, const TileArgs& a, int order_a, int order_b, int epi_kind, hipStream_t st);
 hipError_t launch_rows(int dtype, const TileArgs& a, int epi_kind, hipStream_t st);  // dense_rows.hip: M <= MOE_DENSE_ROW_TOKENS
+// Copies of up to three matrices with rows of whole 16-byte chunks, zeros past a row's end (dense_grad.hip).
+struct PackArgs {
+  struct {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t ld, dst_ld, lines;
+    int32_t len;
+  } m[3];
+  int32_t count;
+};
+hipError_t launch_pack(const PackArgs& p, hipStream_t st);
 hipError_t launch_finish(int dtype, const TileArgs& a, int epi_kind, hipStream_t st);  // dense_grad.hip
 hipError_t launch_grad_in(int dtype, const GradArgs& a, bool gated, hipStream_t st);
 hipError_t launch_bias_sum(int dtype, const float* part, int runs, int mats, int N, void* db0, void* db1, hipStream_t st);

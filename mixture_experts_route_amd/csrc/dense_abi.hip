@@ -9,7 +9,7 @@ DensePlan g_dense_plan = {MOE_DENSE_AUTO, 0};
 // Workspace: control words, the sums of split reductions, then for a backward pass dz (gated: dg, du) in the operands' type with rows
 // padded to whole 16-byte chunks, and the bias gradients' partial sums.
 struct DenseWs {
-  size_t part, dz0, dz1, bias_part, total;
+  size_t part, x, w[2], dz0, dz1, bias_part, total;
   int64_t ldz;
 };
 
@@ -31,6 +31,17 @@ static DenseWs dense_ws(const moe_dense_dims* d, int64_t T, bool backward) {
   DenseWs L{};
   L.part = kCtrlBytes;
   size_t off = dense_align(L.part + part_bytes(d, T, backward));
+  // copies of operands without whole 16-byte rows: x always (its stride is the caller's), the weights when n_in says so
+  const int64_t ld_in = ((int64_t)d->n_in + 7) / 8 * 8;
+  if (T > MOE_DENSE_ROW_TOKENS || backward) {
+    L.x = off;
+    off = dense_align(off + 2 * (size_t)(T * ld_in));
+    if (d->n_in % 8)
+      for (int m = 0; m < 2; ++m) {
+        L.w[m] = off;
+        off = dense_align(off + 2 * (size_t)(d->n_out * ld_in));
+      }
+  }
   if (backward) {
     const int64_t runs = (T + kGradRows - 1) / kGradRows;
     L.ldz = ((int64_t)d->n_out + 7) / 8 * 8;
@@ -87,9 +98,14 @@ static int dense_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EH
 static bool vec8(const void* p, int64_t ld, int elem = 2) { return !p || ((uintptr_t)p % 16 == 0 && ld * elem % 16 == 0); }
 
 static TileArgs tile_args(const moe_dense_dims* d, int64_t T, bool backward, void* ws) {
+  const DenseWs L = dense_ws(d, T, backward);
+  auto at = [&](size_t off) { return off ? (uint16_t*)((uint8_t*)ws + off) : nullptr; };
   TileArgs a{};
-  a.part = (float*)((uint8_t*)ws + kCtrlBytes);
+  a.part = (float*)at(L.part);
   a.part_bytes = part_bytes(d, T, backward);
+  a.pack_a = at(L.x);  // the forward's A is x, its B the weights
+  a.pack_b[0] = at(L.w[0]);
+  a.pack_b[1] = at(L.w[1]);
   return a;
 }
 
@@ -112,6 +128,7 @@ static int run_products(const moe_dense_dims* d, int mats, const void* x, int64_
     a.N = d->n_in;
     a.R = d->n_out;
     a.len_a = len_dz;
+    a.pack_a = nullptr;
     a.nseg = mats;
     a.nbatch = 1;
     a.epi.y[0] = dx;
@@ -125,6 +142,8 @@ static int run_products(const moe_dense_dims* d, int mats, const void* x, int64_
   a.N = d->n_in;
   a.R = T;
   a.nseg = 1;
+  a.pack_b[0] = a.pack_a;  // here B is x, once for both batches
+  a.pack_a = nullptr;
   a.b[0] = a.b[1] = x;
   a.ldb[0] = a.ldb[1] = ldx;
   a.epi.vec = 1;
@@ -159,7 +178,7 @@ MOE_API size_t moe_dense_workspace_bytes(const moe_dense_dims* dims, int32_t max
 }
 
 MOE_API int moe_debug_force_dense_plan(int32_t kernel, int32_t splits) {
-  if (kernel < MOE_DENSE_AUTO || kernel > MOE_DENSE_TILE_ANY || splits < 0 || splits > kMaxSplits) return MOE_EINVAL;
+  if (kernel < MOE_DENSE_AUTO || kernel > MOE_DENSE_ANY128 || splits < 0 || splits > kMaxSplits) return MOE_EINVAL;
   g_dense_plan = {kernel, splits};
   return MOE_OK;
 }
@@ -188,7 +207,7 @@ MOE_API int moe_linear_forward(const moe_dense_dims* dims, const void* x, int64_
   a.ldb[0] = ldw;
   a.M = n_tokens;
   a.N = dims->n_out;
-  a.R = a.len_a = dims->n_in;
+  a.R = a.len_a = a.len_b = dims->n_in;
   a.nseg = a.nbatch = 1;
   a.epi.y[0] = y;
   a.epi.ldy[0] = ldy;
@@ -234,7 +253,7 @@ MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t
   a.ldb[1] = ld_wu;
   a.M = n_tokens;
   a.N = dims->n_out;
-  a.R = a.len_a = dims->n_in;
+  a.R = a.len_a = a.len_b = dims->n_in;
   a.nseg = a.nbatch = 1;
   a.epi.y[0] = h;
   a.epi.ldy[0] = ldh;

@@ -114,6 +114,34 @@ __global__ __launch_bounds__(256) void k_bias_sum(const float* part, int runs, i
   db[c < N ? c : c - N] = (T)s;
 }
 
+// A chunk of 8 elements per thread and pass; blockIdx.y is the matrix.
+__global__ __launch_bounds__(256) void k_pack(PackArgs p) {
+  const auto& m = p.m[blockIdx.y];
+  const int64_t chunks = m.dst_ld / 8, total = m.lines * chunks;
+  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+    const int64_t line = id / chunks, e = id % chunks * 8;
+    const uint16_t* src = m.src + line * m.ld + e;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (e + 8 <= m.len) {
+      typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+      v = *(const u32x4_any*)src;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (e + i < m.len) v[i >> 1] |= (uint32_t)src[i] << (16 * (i & 1));
+    }
+    *(u32x4*)(m.dst + line * m.dst_ld + e) = v;
+  }
+}
+
+hipError_t launch_pack(const PackArgs& p, hipStream_t st) {
+  int64_t most = 0;
+  for (int i = 0; i < p.count; ++i) most = p.m[i].lines * (p.m[i].dst_ld / 8) > most ? p.m[i].lines * (p.m[i].dst_ld / 8) : most;
+  const int64_t blocks = (most + 255) / 256;
+  k_pack<<<dim3((uint32_t)(blocks < 4096 ? blocks : 4096), p.count), 256, 0, st>>>(p);
+  return hipGetLastError();
+}
+
 // Adds the sums of a split reduction in split order and applies the epilogue: 8 outputs per thread.
 template <typename T, int KIND>
 __global__ __launch_bounds__(256) void k_finish(TileArgs a) {

@@ -142,91 +142,169 @@ MOE_DEV u32x4 load8_any(const uint16_t* base, int64_t ld, int64_t line, int64_t 
   return v;
 }
 
-// 128 x 128 tile, 4 waves of 64 x 64; operands pass through registers (a step ahead) on their way to LDS,
-// so any address, stride and length works.
-template <typename T, int OA, int OB, int KIND>
+// One operand's 16-byte chunks of a step, COUNT per thread, loaded at any alignment.  A step that is not the matrix's last is
+// loaded without checks: lines past the outputs repeat the last one, chunks past them (kCols) the first, and a chunk that
+// straddles the end of a kCols line runs into the next line, which exists; all of that reaches only sums that are not stored.
+template <int ORDER, int H, int COUNT>
+struct AnyLoad {
+  const uint16_t* p[COUNT];
+  int64_t advance;
+  const uint16_t* base;
+  int64_t ld, o0;
+  int O, R;
+  bool careful;
+
+  MOE_DEV void init(const void* m, int64_t ld_, int64_t o0_, int O_, int R_, int step, int tid) {
+    base = (const uint16_t*)m;
+    ld = ld_;
+    o0 = o0_;
+    O = O_;
+    R = R_;
+    careful = ORDER == kCols && ld < 8;
+    advance = ORDER == kRows ? kStepR : kStepR * ld;
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) {
+      const int q = tid + 256 * n;
+      if constexpr (ORDER == kRows) {
+        const int64_t i = o0 + (q >> 3);
+        p[n] = base + (i < O ? i : O - 1) * ld + (q & 7) * 8 + step * advance;
+      } else {
+        const int64_t c = o0 + q % (H / 8) * 8;
+        p[n] = base + (c < O ? c : 0) + (q / (H / 8)) * ld + step * advance;
+      }
+    }
+  }
+  // step: of this matrix; last: its last one
+  MOE_DEV void load(u32x4 (&reg)[COUNT], int step, bool last, int tid) {
+    if (last || careful) {
+#pragma unroll
+      for (int n = 0; n < COUNT; ++n) {
+        const int q = tid + 256 * n;
+        if constexpr (ORDER == kRows)
+          reg[n] = load8_any(base, ld, o0 + (q >> 3), O, (int64_t)step * kStepR + (q & 7) * 8, R);
+        else
+          reg[n] = load8_any(base, ld, (int64_t)step * kStepR + q / (H / 8), R, o0 + q % (H / 8) * 8, O);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < COUNT; ++n) reg[n] = *(const u32x4_u*)p[n];
+    }
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) p[n] += advance;
+  }
+  MOE_DEV static void park(const u32x4 (&reg)[COUNT], uint16_t* half, int tid) {
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) {
+      const int q = tid + 256 * n;
+      if constexpr (ORDER == kRows) *(u32x4*)(half + chunk_pos<kRows, H>(q >> 3, q & 7)) = reg[n];
+      else *(u32x4*)(half + chunk_pos<kCols, H>(q / (H / 8), q % (H / 8))) = reg[n];
+    }
+  }
+};
+
+// (64 F) x (64 F) tile, 4 waves of (32 F) x (32 F); operands pass through registers, two steps ahead, into two LDS
+// buffers, so that any address, stride and length works.
+template <typename T, int OA, int OB, int KIND, int F>
 __global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
-  constexpr int H = 64;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[4 * H * kStepR];
+  constexpr int H = 32 * F, kBuf = 4 * H * kStepR;  // elements: A0 A1 B0 B1
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[2 * kBuf];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wi = wave >> 1, wj = wave & 1;
-  const TileIndex x = tile_index(a, blockIdx.x, (int64_t)a.tiles_i * a.tiles_j * a.nbatch * a.splits);
+  const TileIndex x = tile_index(a, blockIdx.x, gridDim.x);
   constexpr int JT = KIND == kEpiGated ? H : 2 * H;  // output columns per tile
   const int64_t i0 = (int64_t)x.ti * 2 * H, j0 = (int64_t)x.tj * JT;
-
   const int steps = (a.R + kStepR - 1) / kStepR;
-  const int total = steps * a.nseg;
+  const int s_begin = (int)((int64_t)steps * a.nseg * x.split / a.splits);
+  const int s_end = (int)((int64_t)steps * a.nseg * (x.split + 1) / a.splits);
+  constexpr bool kSegs = OA == kRows && OB == kCols, kBatches = OA == kCols;
 
-  u32x4 reg[8];
-  auto fetch = [&](int s) {
-    const int seg = s >= steps ? 1 : 0;
-    const int64_t r0 = (int64_t)(s - seg * steps) * kStepR;
-    const uint16_t* pa = (const uint16_t*)a.a[a.nbatch > 1 ? x.batch : seg];
-    const int64_t lda = a.lda[a.nbatch > 1 ? x.batch : seg];
+  AnyLoad<OA, H, F> la[2];
+  AnyLoad<OB, H, F> lb[2];
+  auto point = [&](int s) __attribute__((always_inline)) {  // at step s
+    const bool seg = kSegs && s >= steps, second_a = kBatches ? x.batch : seg;
+    const int step = seg ? s - steps : s;
+    const void *a0 = a.a[0], *a1 = a.a[1], *b0 = a.b[0], *b1 = a.b[1];
+    const int64_t ldb0 = a.ldb[0], ldb1 = a.ldb[1];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      const bool second_b = KIND == kEpiGated ? h == 1 : seg;
+      la[h].init(second_a ? a1 : a0, a.lda[0], i0 + h * H, a.M, a.R, step, tid);
+      lb[h].init(second_b ? b1 : b0, second_b ? ldb1 : ldb0, j0 + (KIND == kEpiGated ? 0 : h * H), a.N, a.R, step, tid);
+    }
+  };
+  u32x4 ra[2][2][F], rb[2][2][F];  // [set][half][chunk]
+  auto fetch = [&](auto S, int s) __attribute__((always_inline)) {
+    constexpr int set = decltype(S)::value;
+    if (s >= s_end) return;
+    if (kSegs && s == steps && s != s_begin) point(s);
+    const int step = kSegs && s >= steps ? s - steps : s;
+    const bool last = step == steps - 1;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int q = tid + 256 * n, m = q >> 3, c = q & 7;
-        if constexpr (OA == kRows)
-          reg[2 * h + n] = load8_any(pa, lda, i0 + h * H + m, a.M, r0 + c * 8, a.R);
-        else
-          reg[2 * h + n] = load8_any(pa, lda, r0 + m, a.R, i0 + h * H + c * 8, a.M);
-        const int sb = KIND == kEpiGated ? h : seg;
-        const int64_t j = j0 + (KIND == kEpiGated ? 0 : h * H);
-        const uint16_t* pb = (const uint16_t*)a.b[sb];
-        if constexpr (OB == kRows)
-          reg[4 + 2 * h + n] = load8_any(pb, a.ldb[sb], j + m, a.N, r0 + c * 8, a.R);
-        else
-          reg[4 + 2 * h + n] = load8_any(pb, a.ldb[sb], r0 + m, a.R, j + c * 8, a.N);
-      }
+    for (int h = 0; h < 2; ++h) {
+      la[h].load(ra[set][h], step, last, tid);
+      lb[h].load(rb[set][h], step, last, tid);
+    }
+  };
+  auto park = [&](auto S, int buf) __attribute__((always_inline)) {
+    constexpr int set = decltype(S)::value;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      la[h].park(ra[set][h], lds + buf * kBuf + h * H * kStepR, tid);
+      lb[h].park(rb[set][h], lds + buf * kBuf + (2 + h) * H * kStepR, tid);
+    }
   };
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds;
-  const uint32_t addr_a = frag_addr<OA, H>(lds0, wi * 32, lane), addr_b = frag_addr<OB, H>(lds0, wj * 32, lane);
+  const uint32_t addr_a = frag_addr<OA, H>(lds0, wi * 16 * F, lane), addr_b = frag_addr<OB, H>(lds0, wj * 16 * F, lane);
   constexpr int kHalf = H * kStepR * 2;  // bytes
-  float4v acc[2][2][2][2] = {};  // [i half][j half][i fragment][j fragment]
-  fetch(0);
-  for (int s = 0; s < total; ++s) {
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int q = tid + 256 * n, m = q >> 3, c = q & 7;
-        *(u32x4*)(lds + h * H * kStepR + chunk_pos<OA, H>(m, c)) = reg[2 * h + n];
-        *(u32x4*)(lds + (2 + h) * H * kStepR + chunk_pos<OB, H>(m, c)) = reg[4 + 2 * h + n];
-      }
-    __syncthreads();
-    if (s + 1 < total) fetch(s + 1);
+  float4v acc[2][2][F][F] = {};          // [i half][j half]
+  auto multiply = [&](int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      typename Operand<T>::v8 fb[2][2];
+      typename Operand<T>::v8 fb[2][F];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
-          fb[h][g] = read_frag<T, OB, H>(addr_b, g, kk, (2 + h) * kHalf);
+        for (int g = 0; g < F; ++g) fb[h][g] = read_frag<T, OB, H>(addr_b + buf * kBuf * 2, g, kk, (2 + h) * kHalf);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const auto fa = read_frag<T, OA, H>(addr_a, f, kk, h * kHalf);
+        for (int f = 0; f < F; ++f) {
+          const auto fa = read_frag<T, OA, H>(addr_a + buf * kBuf * 2, f, kk, h * kHalf);
 #pragma unroll
           for (int hj = 0; hj < 2; ++hj)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) acc[h][hj][f][g] = Operand<T>::mma(fb[hj][g], fa, acc[h][hj][f][g]);
+            for (int g = 0; g < F; ++g) acc[h][hj][f][g] = Operand<T>::mma(fb[hj][g], fa, acc[h][hj][f][g]);
         }
     }
+  };
+  auto step = [&](int s, auto S) __attribute__((always_inline)) {  // step s, parked in buffer S; the next one is in register set 1 - S
+    constexpr int set = decltype(S)::value;
+    __syncthreads();
+    fetch(S, s + 2);
+    multiply(set);
+    if (s + 1 < s_end) park(std::integral_constant<int, 1 - set>{}, 1 - set);
+  };
+  constexpr std::integral_constant<int, 0> zero{};
+  constexpr std::integral_constant<int, 1> one{};
+  point(s_begin);
+  fetch(zero, s_begin);
+  fetch(one, s_begin + 1);
+  park(zero, 0);
+  int s = s_begin;
+  for (; s + 1 < s_end; s += 2) {
+    step(s, zero);
+    step(s + 1, one);
   }
+  if (s < s_end) step(s, zero);
 
   __syncthreads();
-  float* own = (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * 32 * 32;
+  float* own = (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * F * F * 256;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int hj = 0; hj < (KIND == kEpiGated ? 1 : 2); ++hj)
-      finish_fragments<T, KIND, 2, 2>(a, x, i0 + h * H + wi * 32, j0 + hj * H + wj * 32, acc[h][hj], acc[h][1], own,
+      finish_fragments<T, KIND, F, F>(a, x, i0 + h * H + wi * 16 * F, j0 + hj * H + wj * 16 * F, acc[h][hj], acc[h][1], own,
                                       lane);
 }
 
@@ -289,7 +367,8 @@ struct HalfStream {
     const int64_t first = 2 * (ORDER == kRows ? o0 * ld : o0);
     stride = ORDER == kRows ? 2 * kStepR : 2 * kStepR * (uint64_t)ld;
     const int n = O - o0 < H ? (int)(O - o0) : H;
-    bytes = n <= 0 ? 0 : ORDER == kRows ? 2 * ((n - 1) * (int32_t)ld + kStepR) : 2 * ((kStepR - 1) * (int32_t)ld + n);
+    // (an odd row's last element shares its 4-byte word with what follows; a word is read whole or not at all)
+    bytes = n <= 0 ? 0 : ORDER == kRows ? 2 * ((n - 1) * (int32_t)ld + kStepR) : 2 * ((kStepR - 1) * (int32_t)ld + n + (n & 1));
     const int tail = R - (steps - 1) * kStepR;
     cut = n <= 0 ? 0 : 2 * (kStepR - tail) * (ORDER == kRows ? 1 : (int32_t)ld);
     const int in0 = begin >= steps ? 0 : (begin + count < steps ? count : steps - begin);
@@ -372,7 +451,8 @@ __global__ __launch_bounds__(256, 2) void k_tile_deep(TileArgs a) {
   for (int h = 0; h < 2; ++h) {
     constexpr bool g = KIND == kEpiGated;
     cb[h].init(a.ldb[g ? h : 0], wave, lane);
-    sb[h].init(a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], j0 + (g ? 0 : h * HJ), a.N, a.R, steps, s_begin, count);
+    sb[h].init(a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], j0 + (g ? 0 : h * HJ), a.N, OB == kRows ? a.len_b : a.R, steps, s_begin,
+               count);
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds;
   auto copy = [&](uint32_t to) {  // the next step into the stage at `to`
@@ -479,7 +559,8 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
     sa[h].init(kBatches && x.batch ? a.a[1] : a.a[0], a.a[1], a.lda[0], i0 + h * HI, a.M, OA == kRows ? a.len_a : a.R, steps,
                s_begin, count);
     cb[h].init(a.ldb[g ? h : 0], wave, lane);
-    sb[h].init(a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], j0 + (g ? 0 : h * HJ), a.N, a.R, steps, s_begin, count);
+    sb[h].init(a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], j0 + (g ? 0 : h * HJ), a.N, OB == kRows ? a.len_b : a.R, steps, s_begin,
+               count);
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds;
   const uint32_t mine = lds0 + wave * 1024;
@@ -580,9 +661,10 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
                                         acc[h][1], own, lane);
 }
 
-// Row lengths, strides and addresses of both operands are whole 16-byte chunks.
-inline bool whole_chunks(const void* p, int64_t ld, int64_t len) {
-  return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && len % 8 == 0;
+// A line's chunks lie on 16-byte addresses.  kRows: and end with the reduction (or with zeros past it: len counts them).  kCols:
+// a last chunk that is partly past the outputs only reaches sums that are not stored.
+inline bool whole_chunks(int order, const void* p, int64_t ld, int64_t len) {
+  return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && (order == kCols || len % 8 == 0);
 }
 
 // The plan with the least estimated time, in microseconds.  Measured at bf16 and 64 reduction elements per step: a CU draws
@@ -590,27 +672,35 @@ inline bool whole_chunks(const void* p, int64_t ld, int64_t len) {
 // with a 64 x 64 tile (16 KB), 0.63 us with 128 x 128, 1.5 us with 256 x 256; two workgroups side by side (which the two
 // smaller tiles allow) take 0.52 and 0.92 us for a step of each.  Per round of tiles the prologue and epilogue add
 // 1, 2 and 5 us; a split reduction adds a launch and the traffic of its fp32 sums.
+struct TileCost {
+  int kernel, tile;
+  double lone, pair, round;
+};
+constexpr TileCost kWholeCosts[] = {{MOE_DENSE_TILE64, 64, 0.36, 0.52, 1.0},
+                                    {MOE_DENSE_TILE128, 128, 0.63, 0.92, 2.0},
+                                    {MOE_DENSE_TILE256, 256, 1.55, 3.1, 5.0}};
+constexpr TileCost kAnyCosts[] = {{MOE_DENSE_ANY64, 64, 0.9, 1.1, 1.0}, {MOE_DENSE_ANY128, 128, 1.5, 2.2, 2.0}};
+
 template <int OA, int KIND>
-DensePlan plan_tile(const TileArgs& a) {
+DensePlan plan_tile(const TileArgs& a, bool whole, double* us) {
   const int64_t steps = (int64_t)((a.R + kStepR - 1) / kStepR) * a.nseg;
   const int mats = KIND == kEpiGated ? 2 : a.nbatch;
-  DensePlan best = {MOE_DENSE_TILE256, 1};
-  double least = 1e30;
-  for (int kernel : {MOE_DENSE_TILE64, MOE_DENSE_TILE128, MOE_DENSE_TILE256}) {
-    const int ti = kernel == MOE_DENSE_TILE64 ? 64 : kernel == MOE_DENSE_TILE128 ? 128 : 256, tj = KIND == kEpiGated ? ti / 2 : ti;
+  DensePlan best = {0, 1};
+  double& least = *us = 1e300;
+  const TileCost* costs = whole ? kWholeCosts : kAnyCosts;
+  for (int c = 0; c < (whole ? 3 : 2); ++c) {
+    const TileCost& k = costs[c];
+    const int ti = k.tile, tj = KIND == kEpiGated ? ti / 2 : ti;
     const int64_t tiles = (((int64_t)a.M + ti - 1) / ti) * (((int64_t)a.N + tj - 1) / tj) * a.nbatch;
-    const double lone = kernel == MOE_DENSE_TILE64 ? 0.36 : kernel == MOE_DENSE_TILE128 ? 0.63 : 1.55;
-    const double pair = kernel == MOE_DENSE_TILE64 ? 0.52 : kernel == MOE_DENSE_TILE128 ? 0.92 : 3.1;
-    const double round = kernel == MOE_DENSE_TILE64 ? 1 : kernel == MOE_DENSE_TILE128 ? 2 : 5;
     for (int splits = 1; splits <= kMaxSplits; ++splits) {
       const size_t part = split_bytes(splits, mats, a.M, a.N);
       if (splits > 1 && (part > a.part_bytes || tiles * splits > 512 || steps / splits < 4)) break;
       const int64_t per_cu = (tiles * splits + 255) / 256;
-      double t = 3.0 + (per_cu / 2 * pair + per_cu % 2 * lone) * ((steps + splits - 1) / splits) + (per_cu + 1) / 2 * round;
+      double t = 3.0 + (per_cu / 2 * k.pair + per_cu % 2 * k.lone) * ((steps + splits - 1) / splits) + (per_cu + 1) / 2 * k.round;
       if (splits > 1) t += 2.5 + 2.0 * part / 4e6;
       if (t < least) {
         least = t;
-        best = {kernel, splits};
+        best = {k.kernel, splits};
       }
     }
   }
@@ -645,25 +735,74 @@ hipError_t start_plan(TileArgs a, int kernel, hipStream_t st) {
       return hipGetLastError();
     case MOE_DENSE_TILE128: return start_tile<T, OA, OB, KIND, 2, 2, 2, 2>(a, st);
     case MOE_DENSE_TILE256: return start_tile<T, OA, OB, KIND, 2, 4, 4, 2>(a, st);
+    case MOE_DENSE_ANY64:
+      if (!set_tiles<64, KIND == kEpiGated ? 32 : 64, 256>(a, &count)) return hipErrorInvalidConfiguration;
+      k_tile_any<T, OA, OB, KIND, 1><<<dim3((uint32_t)count), dim3(256), 0, st>>>(a);
+      return hipGetLastError();
     default:
       if (!set_tiles<128, KIND == kEpiGated ? 64 : 128, 256>(a, &count)) return hipErrorInvalidConfiguration;
-      k_tile_any<T, OA, OB, KIND><<<dim3((uint32_t)count), dim3(256), 0, st>>>(a);
+      k_tile_any<T, OA, OB, KIND, 2><<<dim3((uint32_t)count), dim3(256), 0, st>>>(a);
       return hipGetLastError();
   }
+}
+
+// Gives the operands that lack them whole 16-byte chunks, by copies in the workspace, when that pays: the copy costs a launch
+// and the operand's bytes twice, the other kernels run at about half the rate (4096 x 4096 tokens and outputs of 4095
+// inputs: 258 us without copies).
+template <int OA, int OB, int KIND>
+bool pack_operands(TileArgs& a, bool whole_a, const bool (&whole_b)[2], hipStream_t st, hipError_t* err) {
+  const int na = a.nseg > 1 || a.nbatch > 1 ? 2 : 1, nb = KIND == kEpiGated || a.nseg > 1 ? 2 : 1;
+  PackArgs p{};
+  double bytes = 0;
+  auto add = [&](const void*& src, int64_t& ld, uint16_t* to, int64_t lines, int len) {
+    if (!to || p.count == 3) return false;
+    const int64_t to_ld = ((int64_t)len + 7) / 8 * 8;
+    p.m[p.count++] = {(const uint16_t*)src, to, ld, to_ld, lines, len};
+    bytes += 4.0 * lines * to_ld;
+    src = to;
+    ld = to_ld;
+    return true;
+  };
+  TileArgs b = a;
+  if (!whole_a) {
+    if (na > 1 || !add(b.a[0], b.lda[0], a.pack_a, OA == kRows ? a.M : a.R, OA == kRows ? a.R : a.M)) return false;
+    b.len_a = (a.R + 7) / 8 * 8;
+  }
+  b.len_b = OB == kRows && !(whole_b[0] && whole_b[1]) ? (a.R + 7) / 8 * 8 : a.R;
+  for (int m = 0; m < nb; ++m) {
+    const bool needs = nb == 2 ? !(whole_b[0] && whole_b[1]) : !whole_b[0];  // both, for equal strides
+    if (needs && !add(b.b[m], b.ldb[m], a.pack_b[m], OB == kRows ? a.N : a.R, OB == kRows ? a.R : a.N)) return false;
+  }
+  if (a.nbatch > 1) b.b[1] = b.b[0], b.ldb[1] = b.ldb[0];
+  double direct, packed;
+  plan_tile<OA, KIND>(a, false, &direct);
+  plan_tile<OA, KIND>(b, true, &packed);
+  if (packed + 2.5 + bytes / 4e6 >= direct) return false;
+  a = b;
+  *err = launch_pack(p, st);
+  return true;
 }
 
 template <typename T, int OA, int OB, int KIND>
 hipError_t launch_tile_k(const TileArgs& args, hipStream_t st) {
   TileArgs a = args;
-  bool whole = true;
+  bool whole_a = true, whole_b[2] = {true, true};
   for (int m = 0; m < (a.nseg > 1 || a.nbatch > 1 ? 2 : 1); ++m)
-    whole = whole && whole_chunks(a.a[m], a.lda[m], OA == kRows ? a.len_a : a.M);
+    whole_a = whole_a && whole_chunks(OA, a.a[m], a.lda[m], a.len_a);
   for (int m = 0; m < (KIND == kEpiGated || a.nseg > 1 ? 2 : 1); ++m)
-    whole = whole && whole_chunks(a.b[m], a.ldb[m], OB == kRows ? a.R : a.N);
-  if (a.nseg > 1) whole = whole && a.ldb[0] == a.ldb[1];
-  DensePlan plan = whole ? plan_tile<OA, KIND>(a) : DensePlan{MOE_DENSE_TILE_ANY, 1};
-  if (whole && g_dense_plan.kernel != MOE_DENSE_AUTO) plan = {g_dense_plan.kernel, 1};
-  if (g_dense_plan.splits && plan.kernel != MOE_DENSE_TILE_ANY) {
+    whole_b[m] = whole_chunks(OB, a.b[m], a.ldb[m], a.R);
+  if (a.nseg > 1 && a.ldb[0] != a.ldb[1]) whole_b[1] = false;
+  bool whole = whole_a && whole_b[0] && whole_b[1];
+  if (!whole && g_dense_plan.kernel < MOE_DENSE_ANY64) {
+    hipError_t err = hipSuccess;
+    whole = pack_operands<OA, OB, KIND>(a, whole_a, whole_b, st, &err);
+    if (err != hipSuccess) return err;
+  }
+  double us;
+  DensePlan plan = plan_tile<OA, KIND>(a, whole, &us);
+  if (g_dense_plan.kernel != MOE_DENSE_AUTO && (whole || g_dense_plan.kernel >= MOE_DENSE_ANY64))
+    plan = {g_dense_plan.kernel, 1};
+  if (g_dense_plan.splits) {
     plan.splits = g_dense_plan.splits;
     while (plan.splits > 1 && split_bytes(plan.splits, KIND == kEpiGated ? 2 : a.nbatch, a.M, a.N) > a.part_bytes)
       --plan.splits;

@@ -290,7 +290,8 @@ def moe_dense_workspace_bytes(d: moe_dense_dims, max_tokens: int, backward: bool
     return _lib.moe_dense_workspace_bytes(ctypes.byref(d), max_tokens, int(backward))
 
 
-MOE_DENSE_AUTO, MOE_DENSE_TILE64, MOE_DENSE_TILE128, MOE_DENSE_TILE256, MOE_DENSE_TILE_ANY = range(5)
+(MOE_DENSE_AUTO, MOE_DENSE_TILE64, MOE_DENSE_TILE128, MOE_DENSE_TILE256, MOE_DENSE_ANY64,
+ MOE_DENSE_ANY128) = range(6)
 
 
 def moe_debug_force_dense_plan(kernel: int = MOE_DENSE_AUTO, splits: int = 0):

@@ -130,7 +130,7 @@ def test_optional_arguments_refused(N):
 
 def test_forced_plan_refused(N):
     f = N.raw("moe_debug_force_dense_plan")
-    for kernel, splits in ((-1, 0), (5, 0), (0, -1), (0, 9)):
+    for kernel, splits in ((-1, 0), (6, 0), (0, -1), (0, 9)):
         assert f(kernel, splits) == N.MOE_EINVAL
 
 

@@ -231,7 +231,7 @@ def test_large(N, shape):
 
 
 @pytest.mark.parametrize("splits", [1, 2, 3, 8])
-@pytest.mark.parametrize("kernel", [1, 2, 3, 4], ids=["tile64", "tile128", "tile256", "any"])
+@pytest.mark.parametrize("kernel", [1, 2, 3, 4, 5], ids=["tile64", "tile128", "tile256", "any64", "any128"])
 def test_every_kernel_and_split(N, kernel, splits):
     """Each tile kernel at sizes inside, at and past its tile, with the reduction in one piece and in parts (fewer steps
     than parts among them), and the few-token kernel in as many parts."""
