@@ -262,8 +262,7 @@ MOE_DEV void finish_or_park(const TileArgs& a, int split, int batch, int64_t i, 
 
 // dz of a backward pass: dz0 = dy * act'(pre0) (dy itself without an activation), or gated dz0 = dh * u * act'(g),
 // dz1 = dh * act(g) with pre0 = g, pre1 = u; rows of ldz elements, zero from N to ldz.  Column sums of the
-// unrounded values over runs of kGradRows rows go to `part` [run][mats][N] when wanted.
-constexpr int kGradRows = 64;
+// unrounded values over runs of `rows` rows go to `part` [run][mats][N] when wanted.
 struct GradArgs {
   const void* dy;
   const void* pre0;
@@ -274,7 +273,14 @@ struct GradArgs {
   float* part;  // NULL: no sums
   int32_t T, N;
   int32_t act;
+  int32_t rows;
 };
+// Runs of rows: about 1024 workgroups (with 512 columns each), at least 4 rows (one per wave).
+inline int64_t grad_runs_most(int64_t N) { return (1024 + (N + 511) / 512 - 1) / ((N + 511) / 512); }
+inline int grad_rows(int64_t T, int64_t N) {
+  const int64_t rows = (T + grad_runs_most(N) - 1) / grad_runs_most(N);
+  return (int)((rows + 3) / 4 * 4);
+}
 
 // dense_tile_*.hip, dense_grad.hip (dtype: MOE_BF16 or MOE_F16)
 hipError_t launch_tile(int dtype, const TileArgs& a, int order_a, int order_b, int epi_kind, hipStream_t st);

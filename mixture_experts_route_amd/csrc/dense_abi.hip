@@ -43,7 +43,7 @@ static DenseWs dense_ws(const moe_dense_dims* d, int64_t T, bool backward) {
       }
   }
   if (backward) {
-    const int64_t runs = (T + kGradRows - 1) / kGradRows;
+    const int64_t most = grad_runs_most(d->n_out), runs = (T + 3) / 4 < most ? (T + 3) / 4 : most;
     L.ldz = ((int64_t)d->n_out + 7) / 8 * 8;
     L.dz0 = off;
     off = dense_align(off + 2 * (size_t)(T * L.ldz));
@@ -307,9 +307,10 @@ MOE_API int moe_linear_backward(const moe_dense_dims* dims, const void* x, int64
     g.T = n_tokens;
     g.N = dims->n_out;
     g.act = dims->act;
+    g.rows = grad_rows(n_tokens, dims->n_out);
     if ((rc = dense_status(launch_grad_in(dims->dtype, g, false, st)))) return rc;
     if (dbias_or_null &&
-        (rc = dense_status(launch_bias_sum(dims->dtype, g.part, (n_tokens + kGradRows - 1) / kGradRows, 1, dims->n_out,
+        (rc = dense_status(launch_bias_sum(dims->dtype, g.part, (n_tokens + g.rows - 1) / g.rows, 1, dims->n_out,
                                            dbias_or_null, nullptr, st))))
       return rc;
   }
@@ -360,8 +361,9 @@ MOE_API int moe_gated_backward(const moe_dense_dims* dims, const void* x, int64_
   g.T = n_tokens;
   g.N = dims->n_out;
   g.act = dims->act;
+  g.rows = grad_rows(n_tokens, dims->n_out);
   if ((rc = dense_status(launch_grad_in(dims->dtype, g, true, st)))) return rc;
-  if (sums && (rc = dense_status(launch_bias_sum(dims->dtype, g.part, (n_tokens + kGradRows - 1) / kGradRows, 2,
+  if (sums && (rc = dense_status(launch_bias_sum(dims->dtype, g.part, (n_tokens + g.rows - 1) / g.rows, 2,
                                                  dims->n_out, dbias_gate_or_null, dbias_up_or_null, st))))
     return rc;
   const void* w[2] = {w_gate, w_up};

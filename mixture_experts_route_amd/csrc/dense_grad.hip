@@ -20,16 +20,16 @@ MOE_DEV void load8f(const void* base, int64_t off, int e, int N, float v[8]) {
   }
 }
 
-// Memory-bound: reads dy and the saved values once, writes dz once.  A workgroup takes 512 columns (8 per
-// lane, 16 bytes a load) x kGradRows rows; its 4 waves take every fourth row and keep the column sums of
-// their rows in registers, added over the waves in LDS in wave order.
+// Memory-bound: reads dy and the saved values once, writes dz once.  A workgroup takes 512 columns (8 per lane, 16 bytes a
+// load) of a run of rows; its 4 waves take every fourth row and keep the column sums of their rows in registers, added
+// over the waves in LDS in wave order.
 template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void k_grad_in(GradArgs a) {
   __shared__ float red[3][2][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = blockIdx.y * 512 + lane * 8;
-  const int t0 = blockIdx.x * kGradRows;
-  const int t1 = a.T - t0 < kGradRows ? a.T : t0 + kGradRows;
+  const int t0 = blockIdx.x * a.rows;
+  const int t1 = a.T - t0 < a.rows ? a.T : t0 + a.rows;
   float sum0[8] = {}, sum1[8] = {};
   if (e < a.ldz) {
     for (int t = t0 + wave; t < t1; t += 4) {
@@ -102,16 +102,27 @@ __global__ __launch_bounds__(256) void k_grad_in(GradArgs a) {
   }
 }
 
-// db[m][n] = sum over runs of part[run][m][n], in run order.
+// db[m][n] = sum over runs of part[run][m][n]: 32 columns per workgroup, 8 threads per column take contiguous shares of
+// the runs, added in LDS in order.  (One thread per column took 31 us for 128 runs of 2048 columns: a chain of loads on 8 CUs.)
 template <typename T>
 __global__ __launch_bounds__(256) void k_bias_sum(const float* part, int runs, int mats, int N, T* db0, T* db1) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= mats * N) return;
-  T* db = c < N ? db0 : db1;
-  if (!db) return;
+  __shared__ float sums[8][33];
+  const int64_t width = (int64_t)mats * N;
+  const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+  const int g = threadIdx.x >> 5;
   float s = 0.0f;
-  for (int r = 0; r < runs; ++r) s += part[(int64_t)r * mats * N + c];
-  db[c < N ? c : c - N] = (T)s;
+  if (c < width) {
+    const int end = (int)((int64_t)runs * (g + 1) / 8);
+#pragma unroll 8
+    for (int r = (int)((int64_t)runs * g / 8); r < end; ++r) s += part[r * width + c];
+  }
+  sums[g][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (g || c >= width) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += sums[i][threadIdx.x];
+  T* db = c < N ? db0 : db1;
+  if (db) db[c < N ? c : c - N] = (T)s;
 }
 
 // A chunk of 8 elements per thread and pass; blockIdx.y is the matrix.
@@ -182,7 +193,7 @@ hipError_t launch_finish(int dtype, const TileArgs& a, int kind, hipStream_t st)
 }
 
 hipError_t launch_grad_in(int dtype, const GradArgs& a, bool gated, hipStream_t st) {
-  const dim3 grid((uint32_t)((a.T + kGradRows - 1) / kGradRows), (uint32_t)((a.ldz + 511) / 512));
+  const dim3 grid((uint32_t)((a.T + a.rows - 1) / a.rows), (uint32_t)((a.ldz + 511) / 512));
   if (dtype == MOE_BF16) {
     if (gated) k_grad_in<__bf16, true><<<grid, 256, 0, st>>>(a);
     else k_grad_in<__bf16, false><<<grid, 256, 0, st>>>(a);
@@ -194,7 +205,7 @@ hipError_t launch_grad_in(int dtype, const GradArgs& a, bool gated, hipStream_t 
 }
 
 hipError_t launch_bias_sum(int dtype, const float* part, int runs, int mats, int N, void* db0, void* db1, hipStream_t st) {
-  const uint32_t grid = (uint32_t)((mats * (int64_t)N + 255) / 256);
+  const uint32_t grid = (uint32_t)((mats * (int64_t)N + 31) / 32);
   if (dtype == MOE_BF16) k_bias_sum<__bf16><<<grid, 256, 0, st>>>(part, runs, mats, N, (__bf16*)db0, (__bf16*)db1);
   else k_bias_sum<_Float16><<<grid, 256, 0, st>>>(part, runs, mats, N, (_Float16*)db0, (_Float16*)db1);
   return hipGetLastError();
