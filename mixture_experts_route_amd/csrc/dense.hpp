@@ -127,6 +127,8 @@ struct DenseEpi {
   int32_t y_f32;       // linear: y and res are fp32
   int32_t act;
   int32_t vec;         // every matrix above may be moved 8 elements at a time (16-byte aligned rows)
+  int32_t stream;      // outputs larger than the L2s: stored with the non-temporal hint (launch_tile), so that they leave
+                       // the operands in the caches (4096 tokens and outputs: 512 inputs 28.6 -> 24.9 us, 4096 inputs 110.8 -> 106.3 us)
 };
 
 // 8 consecutive elements of a row as fp32, or the first n of them.
@@ -145,7 +147,7 @@ MOE_DEV void load8(const void* base, int64_t off, int n, bool vec, float (&v)[8]
   }
 }
 template <typename T>
-MOE_DEV void store8(void* base, int64_t off, int n, bool vec, const float (&v)[8]) {
+MOE_DEV void store8(void* base, int64_t off, int n, bool vec, const float (&v)[8], bool stream = false) {
   T* p = (T*)base + off;
   if (vec && n == 8) {
     typedef T v8 __attribute__((ext_vector_type(8)));
@@ -153,7 +155,8 @@ MOE_DEV void store8(void* base, int64_t off, int n, bool vec, const float (&v)[8
     v8 t;
 #pragma unroll
     for (int c = 0; c < 8; ++c) t[c] = (T)v[c];
-    *(v8_16*)p = t;
+    if (stream) __builtin_nontemporal_store(t, (v8_16*)p);
+    else *(v8_16*)p = t;
   } else {
 #pragma unroll
     for (int c = 0; c < 8; ++c)
@@ -164,9 +167,9 @@ MOE_DEV void store8(void* base, int64_t off, int n, bool vec, const float (&v)[8
 // Outputs (i, j .. j + n - 1), n = 1..8, j a multiple of 8: s0 = the fp32 sums (gated: the gate's), s1 = the up's.
 template <typename T, int KIND>
 MOE_DEV void finish8(const DenseEpi& e, int batch, int64_t i, int j, int n, float (&s0)[8], float (&s1)[8]) {
-  const bool vec = e.vec;
+  const bool vec = e.vec, stream = e.stream;
   if constexpr (KIND == kEpiStore) {
-    store8<T>(batch ? e.y[1] : e.y[0], i * (batch ? e.ldy[1] : e.ldy[0]) + j, n, vec, s0);
+    store8<T>(batch ? e.y[1] : e.y[0], i * (batch ? e.ldy[1] : e.ldy[0]) + j, n, vec, s0, stream);
     return;
   }
   float t[8];
@@ -183,14 +186,14 @@ MOE_DEV void finish8(const DenseEpi& e, int batch, int64_t i, int j, int n, floa
     }
   }
   if (e.pre[0]) {
-    store8<T>(e.pre[0], i * e.ldp[0] + j, n, vec, s0);
-    if constexpr (KIND == kEpiGated) store8<T>(e.pre[1], i * e.ldp[1] + j, n, vec, s1);
+    store8<T>(e.pre[0], i * e.ldp[0] + j, n, vec, s0, stream);
+    if constexpr (KIND == kEpiGated) store8<T>(e.pre[1], i * e.ldp[1] + j, n, vec, s1, stream);
   }
   act_values(e.act, s0);
   if constexpr (KIND == kEpiGated) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) s0[c] *= s1[c];
-    store8<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
+    store8<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0, stream);
   } else {
     if (e.res) {
       if (e.y_f32)
@@ -201,9 +204,9 @@ MOE_DEV void finish8(const DenseEpi& e, int batch, int64_t i, int j, int n, floa
       for (int c = 0; c < 8; ++c) s0[c] += t[c];
     }
     if (e.y_f32)
-      store8<float>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
+      store8<float>(e.y[0], i * e.ldy[0] + j, n, vec, s0, stream);
     else
-      store8<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0);
+      store8<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0, stream);
   }
 }
 

@@ -808,6 +808,7 @@ hipError_t launch_tile_k(const TileArgs& args, hipStream_t st) {
       --plan.splits;
   }
   a.splits = plan.splits;
+  a.epi.stream = 2.0 * a.M * a.N * a.nbatch >= 16e6;
   const hipError_t e = start_plan<T, OA, OB, KIND>(a, plan.kernel, st);
   return e != hipSuccess || a.splits == 1 ? e : launch_finish(__is_same(T, __bf16) ? MOE_BF16 : MOE_F16, a, KIND, st);
 }
