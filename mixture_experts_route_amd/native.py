@@ -303,24 +303,21 @@ _DENSE_TYPES = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int1
                 MOE_F16: (torch.float16,)}
 
 
-# The device's current stream as an address, without the stream object that torch.cuda.current_stream builds
-# (2.9 against 0.1 us of host time per call, measured, where a one-token kernel takes 4 us).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _dense_fail(where: str):
-    raise MoeError(MOE_EINVAL, where)
+# The current device and its current stream as an address, without the stream object that torch.cuda.current_stream
+# builds (2.9 against 0.1 us of host time per call, measured, where a one-token kernel takes 4 us).
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _mat(t, rows: int, cols: int, types, device, where: str):
     """(address, row stride) of a row-major [rows][cols] tensor.  The C interface sees addresses only: a tensor's
     type, sizes, strides and device are checked here."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype not in types or t.device != device:
-        _dense_fail(where)
-    if stride[1] != 1 and cols > 1:
-        _dense_fail(where)
-    return t.data_ptr(), (stride[0] if rows > 1 else cols)
+        raise MoeError(MOE_EINVAL, where)
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise MoeError(MOE_EINVAL, where)
+    return t.data_ptr(), ld if rows > 1 else cols
 
 
 def _opt_mat(t, rows: int, cols: int, types, device, where: str):
@@ -331,70 +328,74 @@ def _opt_vec(t, n: int, types, device, where: str):
     if t is None:
         return None
     if t.dim() != 1 or t.shape[0] != n or t.dtype not in types or t.device != device or (n > 1 and t.stride(0) != 1):
-        _dense_fail(where)
+        raise MoeError(MOE_EINVAL, where)
     return t.data_ptr()
 
 
-def _dense_call(name: str, d: moe_dense_dims, device, ws, stream, args):
+def _dense_call(f, where: str, d: moe_dense_dims, device, ws, stream, args):
     """The C call on the tensors' device, on ``stream`` or that device's current one."""
     if device.type != "cuda" or ws.device != device or not ws.is_contiguous():
-        _dense_fail(f"{name}, device or ws")
-    f, index = getattr(_lib, name), device.index
+        raise MoeError(MOE_EINVAL, where + ", device or ws")
+    index = device.index
     st = _raw_stream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         rc = f(ctypes.byref(d), *args, ws.data_ptr(), ws.nbytes, st)
     else:
         with torch.cuda.device(index):
             rc = f(ctypes.byref(d), *args, ws.data_ptr(), ws.nbytes, st)
     if rc != MOE_OK:
-        raise MoeError(rc, name)
+        raise MoeError(rc, where)
 
 
 def moe_linear_forward(d: moe_dense_dims, x, n_tokens: int, w, y, ws, bias=None, residual=None, pre=None, stream=None):
     """``y = act(x w^T + bias) + residual``; y and residual in the operands' type or float32."""
-    K, N, T, dev, ty, at = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_linear_forward, "
-    yd = dtype_code(y)
+    K, N, T, dev, ty, yd = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), dtype_code(y)
     yt = _DENSE_TYPES[yd]
-    _dense_call("moe_linear_forward", d, dev, ws, stream, (
-        *_mat(x, T, K, ty, dev, at + "x"), T, *_mat(w, N, K, ty, dev, at + "w"), _opt_vec(bias, N, ty, dev, at + "bias"),
-        *_opt_mat(residual, T, N, yt, dev, at + "residual"), *_mat(y, T, N, yt, dev, at + "y"), yd,
-        *_opt_mat(pre, T, N, ty, dev, at + "pre")))
+    _dense_call(_lib.moe_linear_forward, "moe_linear_forward", d, dev, ws, stream, (
+        *_mat(x, T, K, ty, dev, "moe_linear_forward, x"), T, *_mat(w, N, K, ty, dev, "moe_linear_forward, w"),
+        _opt_vec(bias, N, ty, dev, "moe_linear_forward, bias"),
+        *_opt_mat(residual, T, N, yt, dev, "moe_linear_forward, residual"),
+        *_mat(y, T, N, yt, dev, "moe_linear_forward, y"), yd,
+        *_opt_mat(pre, T, N, ty, dev, "moe_linear_forward, pre")))
 
 
 def moe_linear_backward(d: moe_dense_dims, x, n_tokens: int, w, dy, ws, pre=None, dx=None, dw=None, dbias=None,
                         stream=None):
     """Gradients of ``act(x w^T + bias)`` from ``dy`` and the saved ``pre``; outputs that are None are not computed."""
-    K, N, T, dev, ty, at = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_linear_backward, "
-    _dense_call("moe_linear_backward", d, dev, ws, stream, (
-        *_mat(x, T, K, ty, dev, at + "x"), T, *_mat(w, N, K, ty, dev, at + "w"),
-        *_opt_mat(pre, T, N, ty, dev, at + "pre"), *_mat(dy, T, N, ty, dev, at + "dy"),
-        *_opt_mat(dx, T, K, ty, dev, at + "dx"), *_opt_mat(dw, N, K, ty, dev, at + "dw"),
-        _opt_vec(dbias, N, ty, dev, at + "dbias")))
+    K, N, T, dev, ty = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ())
+    _dense_call(_lib.moe_linear_backward, "moe_linear_backward", d, dev, ws, stream, (
+        *_mat(x, T, K, ty, dev, "moe_linear_backward, x"), T, *_mat(w, N, K, ty, dev, "moe_linear_backward, w"),
+        *_opt_mat(pre, T, N, ty, dev, "moe_linear_backward, pre"), *_mat(dy, T, N, ty, dev, "moe_linear_backward, dy"),
+        *_opt_mat(dx, T, K, ty, dev, "moe_linear_backward, dx"), *_opt_mat(dw, N, K, ty, dev, "moe_linear_backward, dw"),
+        _opt_vec(dbias, N, ty, dev, "moe_linear_backward, dbias")))
 
 
 def moe_gated_forward(d: moe_dense_dims, x, n_tokens: int, w_gate, w_up, h, ws, gate_bias=None, up_bias=None, gate=None,
                       up=None, stream=None):
     """``h = act(x w_gate^T + gate_bias) * (x w_up^T + up_bias)``; ``gate`` and ``up`` receive the two factors'
     pre-activations for the backward pass."""
-    K, N, T, dev, ty, at = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_gated_forward, "
-    _dense_call("moe_gated_forward", d, dev, ws, stream, (
-        *_mat(x, T, K, ty, dev, at + "x"), T, *_mat(w_gate, N, K, ty, dev, at + "w_gate"),
-        *_mat(w_up, N, K, ty, dev, at + "w_up"), _opt_vec(gate_bias, N, ty, dev, at + "gate_bias"),
-        _opt_vec(up_bias, N, ty, dev, at + "up_bias"), *_mat(h, T, N, ty, dev, at + "h"),
-        *_opt_mat(gate, T, N, ty, dev, at + "gate"), *_opt_mat(up, T, N, ty, dev, at + "up")))
+    K, N, T, dev, ty = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ())
+    _dense_call(_lib.moe_gated_forward, "moe_gated_forward", d, dev, ws, stream, (
+        *_mat(x, T, K, ty, dev, "moe_gated_forward, x"), T, *_mat(w_gate, N, K, ty, dev, "moe_gated_forward, w_gate"),
+        *_mat(w_up, N, K, ty, dev, "moe_gated_forward, w_up"),
+        _opt_vec(gate_bias, N, ty, dev, "moe_gated_forward, gate_bias"),
+        _opt_vec(up_bias, N, ty, dev, "moe_gated_forward, up_bias"), *_mat(h, T, N, ty, dev, "moe_gated_forward, h"),
+        *_opt_mat(gate, T, N, ty, dev, "moe_gated_forward, gate"), *_opt_mat(up, T, N, ty, dev, "moe_gated_forward, up")))
 
 
 def moe_gated_backward(d: moe_dense_dims, x, n_tokens: int, w_gate, w_up, gate, up, dh, ws, dx=None, dw_gate=None,
                        dw_up=None, dgate_bias=None, dup_bias=None, stream=None):
     """Gradients of moe_gated_forward from ``dh`` and the saved ``gate`` and ``up``; None: not computed."""
-    K, N, T, dev, ty, at = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_gated_backward, "
-    _dense_call("moe_gated_backward", d, dev, ws, stream, (
-        *_mat(x, T, K, ty, dev, at + "x"), T, *_mat(w_gate, N, K, ty, dev, at + "w_gate"),
-        *_mat(w_up, N, K, ty, dev, at + "w_up"), *_mat(gate, T, N, ty, dev, at + "gate"),
-        *_mat(up, T, N, ty, dev, at + "up"), *_mat(dh, T, N, ty, dev, at + "dh"),
-        *_opt_mat(dx, T, K, ty, dev, at + "dx"), *_opt_mat(dw_gate, N, K, ty, dev, at + "dw_gate"),
-        *_opt_mat(dw_up, N, K, ty, dev, at + "dw_up"), _opt_vec(dgate_bias, N, ty, dev, at + "dgate_bias"),
-        _opt_vec(dup_bias, N, ty, dev, at + "dup_bias")))
+    K, N, T, dev, ty = d.n_in, d.n_out, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ())
+    _dense_call(_lib.moe_gated_backward, "moe_gated_backward", d, dev, ws, stream, (
+        *_mat(x, T, K, ty, dev, "moe_gated_backward, x"), T, *_mat(w_gate, N, K, ty, dev, "moe_gated_backward, w_gate"),
+        *_mat(w_up, N, K, ty, dev, "moe_gated_backward, w_up"), *_mat(gate, T, N, ty, dev, "moe_gated_backward, gate"),
+        *_mat(up, T, N, ty, dev, "moe_gated_backward, up"), *_mat(dh, T, N, ty, dev, "moe_gated_backward, dh"),
+        *_opt_mat(dx, T, K, ty, dev, "moe_gated_backward, dx"),
+        *_opt_mat(dw_gate, N, K, ty, dev, "moe_gated_backward, dw_gate"),
+        *_opt_mat(dw_up, N, K, ty, dev, "moe_gated_backward, dw_up"),
+        _opt_vec(dgate_bias, N, ty, dev, "moe_gated_backward, dgate_bias"),
+        _opt_vec(dup_bias, N, ty, dev, "moe_gated_backward, dup_bias")))
 
 
 def raw(name: str):

@@ -447,6 +447,33 @@ def test_dense_shared_expert_on_the_routed_layer(N):
             R.check("logits", logits, R.linear_forward(0, yb, head, None, None, F32)["y"])
 
 
+def test_binding_refuses_mismatched_tensors(N):
+    """Tensors whose shape, type, stride or device does not fit never reach the library, and outputs stay as they are."""
+    T, K, M = 4, 64, 32
+    x, w = torch.zeros(T, K, dtype=BF16, device="cuda"), torch.zeros(M, K, dtype=BF16, device="cuda")
+    y = torch.full((T, M), 7.0, dtype=BF16, device="cuda")
+    d = N.dense_dims(K, M, N.MOE_BF16, N.MOE_ACT_SILU)
+    ws, _ = workspace(N, d, T, True)
+    for bad in (dict(x=x[:3]), dict(x=x.half()), dict(x=x.cpu()), dict(x=torch.zeros(K, T, dtype=BF16, device="cuda").t()),
+                dict(w=w[:, :40]), dict(w=w.float()), dict(w=w.cpu()), dict(y=y[:, :31]), dict(y=y.cpu()),
+                dict(y=y.half()), dict(ws=ws.cpu()), dict(ws=ws[::2]), dict(ws=ws[:64]), dict(bias=w[0, :31]),
+                dict(bias=w[:, 0]), dict(residual=y.float()), dict(pre=y.float()), dict(x=x[:1].expand(T, K))):
+        a = dict(x=x, w=w, y=y, ws=ws, bias=None, residual=None, pre=None)
+        a.update(bad)
+        with pytest.raises(N.MoeError) as e:
+            N.moe_linear_forward(d, a["x"], T, a["w"], a["y"], a["ws"], bias=a["bias"], residual=a["residual"], pre=a["pre"])
+        assert e.value.code in (N.MOE_EINVAL, N.MOE_EWORKSPACE, N.MOE_EUNSUPPORTED), bad
+    for call in (lambda: N.moe_gated_forward(d, x, T, w, w[:16], y, ws),
+                 lambda: N.moe_gated_forward(d, x, T, w, w, y, ws, gate=y),
+                 lambda: N.moe_linear_backward(d, x, T, w, y, ws, dx=x),
+                 lambda: N.moe_linear_backward(d, x, T, w, y, ws, pre=y),
+                 lambda: N.moe_gated_backward(d, x, T, w, w, y, y, y[:2], ws, dx=x)):
+        with pytest.raises(N.MoeError):
+            call()
+    torch.cuda.synchronize()
+    assert (y == 7.0).all()
+
+
 def test_more_than_2_31_elements(N):
     """Outputs, inputs and reductions whose element offsets pass 32 bits: sampled rows and columns."""
     T, K, M = 34000, 64, 65536
