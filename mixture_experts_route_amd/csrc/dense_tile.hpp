@@ -70,21 +70,25 @@ MOE_DEV typename Operand<T>::v8 read_frag(uint32_t addr, int n, int kk, int offs
 struct TileIndex {
   int batch, ti, tj, split;
 };
-MOE_DEV TileIndex tile_index(const TileArgs& a, int64_t id, int64_t count) {
-  const int64_t q = count / 8, rem = count % 8;
-  const int64_t xcd = id % 8, k = id / 8;
-  int64_t t = xcd * q + (xcd < rem ? xcd : rem) + k;
-  TileIndex x;
-  x.split = (int)(t % a.splits);
-  t /= a.splits;
-  const int64_t per_batch = (int64_t)a.tiles_i * a.tiles_j;
-  x.batch = (int)(t / per_batch);
-  t -= x.batch * per_batch;
-  const int64_t group = t / (8 * (int64_t)a.tiles_j);
-  const int64_t in_group = t - group * 8 * a.tiles_j;
-  const int rows = a.tiles_i - (int)group * 8 < 8 ? a.tiles_i - (int)group * 8 : 8;
-  x.ti = (int)group * 8 + (int)(in_group % rows);
-  x.tj = (int)(in_group / rows);
+MOE_DEV TileIndex tile_index(const TileArgs& a, uint32_t id, uint32_t count) {
+  const uint32_t q = count / 8, rem = count % 8, xcd = id % 8;
+  uint32_t t = xcd * q + (xcd < rem ? xcd : rem) + id / 8;
+  TileIndex x = {0, 0, 0, 0};
+  if (a.splits > 1) {
+    x.split = (int)(t % a.splits);
+    t /= a.splits;
+  }
+  const uint32_t per_batch = (uint32_t)a.tiles_i * a.tiles_j;
+  if (a.nbatch > 1 && t >= per_batch) {
+    x.batch = 1;
+    t -= per_batch;
+  }
+  const uint32_t in_full = 8u * a.tiles_j;
+  const uint32_t group = t / in_full, in_group = t - group * in_full;
+  const uint32_t left = a.tiles_i - group * 8;
+  const uint32_t rows = left < 8 ? left : 8;
+  x.tj = (int)(rows == 8 ? in_group >> 3 : in_group / rows);
+  x.ti = (int)(group * 8 + in_group - x.tj * rows);
   return x;
 }
 

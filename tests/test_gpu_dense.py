@@ -329,6 +329,20 @@ def test_infinities_and_nans_stay_in_their_rows(N, T):
     assert torch.isinf(y[0]).all() and (y[1] == 65504).all() and (y[2:] == 0).all()
 
 
+@pytest.mark.parametrize("T", [3, 100])
+def test_subnormal_operands_count(N, T):
+    """fp16 values below 2^-14 enter the sums and results exactly."""
+    x = torch.zeros(T, 64, dtype=F16, device="cuda")
+    x[:, 5], x[:, 40] = 3 * 2.0 ** -24, 2.0 ** -20
+    w = torch.ones(32, 64, dtype=F16, device="cuda")
+    d = N.dense_dims(64, 32, N.MOE_F16, 0)
+    ws, _ = workspace(N, d, T, False)
+    y, y16 = torch.empty(T, 32, device="cuda"), torch.empty(T, 32, dtype=F16, device="cuda")
+    N.moe_linear_forward(d, x, T, w, y, ws)
+    N.moe_linear_forward(d, x, T, w, y16, ws)
+    assert (y == 19 * 2.0 ** -24).all() and (y16.double() == 19 * 2.0 ** -24).all()
+
+
 def test_gradients_match_differences(N):
     """The GPU's gradients against central differences of the float64 forward pass along random directions."""
     T, K, M = 37, 72, 56
