@@ -93,9 +93,11 @@ MOE_DEV TileIndex tile_index(const TileArgs& a, uint32_t id, uint32_t count) {
 }
 
 // ---- epilogue -------------------------------------------------------------------------------------
-// One wave's FI x FJ fragments of outputs (i0.., j0..) (gated: the gate's and the up's) through the wave's own LDS
-// (16-byte chunks swizzled by row), so that a lane finishes 8 consecutive elements and the code of an
-// activation exists once per kernel.
+// A wave's FI x FJ fragments of outputs (i0.., j0..): lane l holds rows f 16 + l % 16, columns g 16 + 4 (l / 16) ..+3.  They pass
+// through the wave's own LDS (16-byte chunks swizzled by row) so that a lane stores 8 consecutive elements.  Plain results are
+// rounded to 16 bits first, half the LDS bytes (4096 x 4096 outputs of 512 terms 27.2 -> 23.5 us, 8192 x 8192 of 2048 251 -> 244 us);
+// with a bias, activation or residual the fp32 sums pass, in a loop, so that the code of an activation exists once per
+// kernel and no registers spill.
 template <typename T, int KIND, int FI, int FJ>
 MOE_DEV void finish_fragments(const TileArgs& a, const TileIndex& x, int64_t i0, int64_t j0, const float4v (&s0)[FI][FJ],
                               const float4v (&s1)[FI][FJ], float* lds, int lane) {
@@ -122,9 +124,94 @@ MOE_DEV void finish_fragments(const TileArgs& a, const TileIndex& x, int64_t i0,
       *(float4v*)v1 = *(const float4v*)(lds + R * C + pos(r, j / 4));
       *(float4v*)(v1 + 4) = *(const float4v*)(lds + R * C + pos(r, j / 4 + 1));
     }
-    if (i0 + r < a.M && n > 0) finish_or_park<T, KIND>(a, x.split, x.batch, i0 + r, (int)(j0 + j), n, v0, v1);
+    if (i0 + r < a.M && n > 0) finish8<T, KIND>(a.epi, x.batch, i0 + r, (int)(j0 + j), n, v0, v1);
   }
   __builtin_amdgcn_wave_barrier();
+}
+
+template <typename T, int FI, int FJ>
+MOE_DEV void store_block(void* y, int64_t ldy, int64_t i0, int64_t j0, int M, int N, bool vec, bool stream,
+                         const float4v (&s)[FI][FJ], uint16_t* lds, int lane) {
+  typedef typename Operand<T>::v8 v8;
+  typedef T v4 __attribute__((ext_vector_type(4)));
+  constexpr int R = FI * 16, C = FJ * 16, kLanes = C / 8, kRowsPer = 64 / kLanes;  // lanes per row, rows per pass
+  auto pos = [](int r, int chunk) { return r * C + ((chunk ^ ((r >> (FJ == 1 ? 3 : 2)) & (kLanes - 1))) << 3); };
+#pragma unroll
+  for (int f = 0; f < FI; ++f)
+#pragma unroll
+    for (int g = 0; g < FJ; ++g) {
+      v4 t;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) t[c] = (T)s[f][g][c];
+      const int chunk = g * 2 + (lane >> 5);
+      *(v4*)(lds + pos(f * 16 + (lane & 15), chunk) + ((lane >> 4) & 1) * 4) = t;
+    }
+  __builtin_amdgcn_wave_barrier();  // one wave: its LDS operations take effect in issue order
+  const int r0 = lane / kLanes, j = (lane % kLanes) * 8;
+  const int64_t cols = N - (j0 + j);
+  T* p = (T*)y + (i0 + r0) * ldy + j0 + j;
+  const int64_t rows = M - i0;
+  if (vec && N - j0 >= C) {
+#pragma unroll
+    for (int r = 0; r < R; r += kRowsPer) {
+      const v8 t = *(const v8*)(lds + pos(r0 + r, lane % kLanes));
+      if (r0 + r < rows && r0 + r < R) {
+        typedef v8 v8_16 __attribute__((aligned(16)));
+        if (stream) __builtin_nontemporal_store(t, (v8_16*)(p + r * ldy));
+        else *(v8_16*)(p + r * ldy) = t;
+      }
+    }
+  } else {
+#pragma clang loop unroll(disable)
+    for (int r = r0; r < R; r += kRowsPer) {
+      const v8 t = *(const v8*)(lds + pos(r, lane % kLanes));
+      if (r < rows)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < cols) p[(r - r0) * ldy + c] = t[c];
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Parked sums leave from the registers, 16 bytes per lane and 64 per row and fragment; N a multiple of 4.
+template <int FI, int FJ>
+MOE_DEV void store_block_f32(float* y, int64_t ldy, int64_t i0, int64_t j0, int64_t M, int64_t N, const float4v (&s)[FI][FJ],
+                             int lane) {
+#pragma unroll
+  for (int f = 0; f < FI; ++f) {
+    const int64_t i = i0 + f * 16 + (lane & 15);
+#pragma unroll
+    for (int g = 0; g < FJ; ++g) {
+      const int64_t j = j0 + g * 16 + 4 * (lane >> 4);
+      if (i < M && j < N) *(float4v*)(y + i * ldy + j) = s[f][g];
+    }
+  }
+}
+
+// All of a wave's sums: NI x 2 blocks, block (h, hj) at rows i0 + h di, columns j0 + hj dj (gated: hj = 0 the gate's, 1 the
+// up's sums of the same outputs).
+template <typename T, int KIND, int NI, int FI, int FJ>
+MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, int64_t di, int64_t j0, int64_t dj,
+                           const float4v (&s)[NI][2][FI][FJ], float* lds, int lane) {
+  const DenseEpi& e = a.epi;
+  constexpr bool kGated = KIND == kEpiGated;
+  const bool plain = KIND == kEpiStore || (KIND == kEpiLinear && !e.bias[0] && !e.pre[0] && !e.res && !e.y_f32 && e.act == MOE_ACT_NONE);
+#pragma unroll
+  for (int h = 0; h < NI; ++h)
+#pragma unroll
+    for (int hj = 0; hj < 2; ++hj) {
+      const int64_t i = i0 + h * di, j = j0 + (kGated ? 0 : hj * dj);
+      if (a.splits > 1) {  // parked for the second launch; rows padded to 8 floats, so a last fragment's spare columns have room
+        const int mat = kGated ? hj : x.batch, mats = kGated ? 2 : a.nbatch;
+        store_block_f32<FI, FJ>(part_at(a, x.split, mats, mat, 0, 0), (a.N + 7) / 8 * 8, i, j, a.M, (a.N + 7) / 8 * 8, s[h][hj], lane);
+      } else if (!kGated && plain) {
+        store_block<T, FI, FJ>(x.batch ? e.y[1] : e.y[0], x.batch ? e.ldy[1] : e.ldy[0], i, j, a.M, a.N, e.vec, e.stream, s[h][hj],
+                               (uint16_t*)lds, lane);
+      } else if (KIND != kEpiStore && !(kGated && hj)) {
+        finish_fragments<T, KIND, FI, FJ>(a, x, i, j, s[h][hj], s[h][1], lds, lane);
+      }
+    }
 }
 
 // ---- any alignment --------------------------------------------------------------------------------
@@ -303,13 +390,8 @@ __global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
   if (s < s_end) step(s, zero);
 
   __syncthreads();
-  float* own = (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * F * F * 256;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int hj = 0; hj < (KIND == kEpiGated ? 1 : 2); ++hj)
-      finish_fragments<T, KIND, F, F>(a, x, i0 + h * H + wi * 16 * F, j0 + hj * H + wj * 16 * F, acc[h][hj], acc[h][1], own,
-                                      lane);
+  finish_blocks<T, KIND>(a, x, i0 + wi * 16 * F, H, j0 + wj * 16 * F, H, acc,
+                         (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * F * F * 256, lane);
 }
 
 // ---- 16-byte aligned operands ------------------------------------------------------------------------
@@ -509,15 +591,12 @@ __global__ __launch_bounds__(256, 2) void k_tile_deep(TileArgs a) {
   if (k < count) step(std::integral_constant<int, 0>{});
   copies_barrier<0>();  // no copy may land after the workgroup has given its LDS back
 
-  float* own = (float*)lds + wave * 2 * 512;
-  float4v s[2][2][1];
+  float4v s[1][2][2][1];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int n = 0; n < 2; ++n) s[h][n][0] = acc[h][n];
-#pragma unroll
-  for (int h = 0; h < (KIND == kEpiGated ? 1 : 2); ++h)
-    finish_fragments<T, KIND, 2, 1>(a, x, i0 + wi * 32, j0 + h * HJ + wj * 16, s[h], s[1], own, lane);
+    for (int n = 0; n < 2; ++n) s[0][h][n][0] = acc[h][n];
+  finish_blocks<T, KIND>(a, x, i0 + wi * 32, 0, j0 + wj * 16, HJ, s, (float*)lds + wave * 1024, lane);
 }
 
 // (2 WI FI 16) x (2 WJ FJ 16) tile, WI x WJ waves; a wave's quarter in (i half, j half) is FI x FJ fragments.
@@ -656,13 +735,8 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   if (k < count) step(std::integral_constant<int, 0>{});
   copies_barrier<0>();  // no copy may land after the workgroup has given its LDS back
 
-  float* own = (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * FI * FJ * 256;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int hj = 0; hj < (KIND == kEpiGated ? 1 : 2); ++hj)
-      finish_fragments<T, KIND, FI, FJ>(a, x, i0 + h * HI + wi * FI * 16, j0 + hj * HJ + wj * FJ * 16, acc[h][hj],
-                                        acc[h][1], own, lane);
+  finish_blocks<T, KIND>(a, x, i0 + wi * FI * 16, HI, j0 + wj * FJ * 16, HJ, acc,
+                         (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * FI * FJ * 256, lane);
 }
 
 // A line's chunks lie on 16-byte addresses.  kRows: and end with the reduction (or with zeros past it: len counts them).  kCols:
