@@ -189,6 +189,19 @@ MOE_DEV void store_block_f32(float* y, int64_t ldy, int64_t i0, int64_t j0, int6
   }
 }
 
+// act(g) * u of one block, in registers.
+template <int ACT, int FI, int FJ>
+MOE_DEV void gate_block(const float4v (&g)[FI][FJ], const float4v (&u)[FI][FJ], float4v (&h)[FI][FJ]) {
+#pragma unroll
+  for (int f = 0; f < FI; ++f)
+#pragma unroll
+    for (int n = 0; n < FJ; ++n) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) h[f][n][c] = act_value(ACT, g[f][n][c]) * u[f][n][c];
+      __builtin_amdgcn_sched_barrier(0);  // a fragment at a time: the registers are full of sums
+    }
+}
+
 // All of a wave's sums: NI x 2 blocks, block (h, hj) at rows i0 + h di, columns j0 + hj dj (gated: hj = 0 the gate's, 1 the
 // up's sums of the same outputs).
 template <typename T, int KIND, int NI, int FI, int FJ>
@@ -196,6 +209,24 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
                            const float4v (&s)[NI][2][FI][FJ], float* lds, int lane) {
   const DenseEpi& e = a.epi;
   constexpr bool kGated = KIND == kEpiGated;
+  if constexpr (kGated) {
+    if (a.splits == 1 && !e.bias[0] && !e.bias[1] && !e.pre[0]) {
+#pragma unroll
+      for (int h = 0; h < NI; ++h) {
+        float4v v[FI][FJ];
+        switch (e.act) {
+          case MOE_ACT_SILU: gate_block<MOE_ACT_SILU>(s[h][0], s[h][1], v); break;
+          case MOE_ACT_GELU: gate_block<MOE_ACT_GELU>(s[h][0], s[h][1], v); break;
+          case MOE_ACT_GELU_TANH: gate_block<MOE_ACT_GELU_TANH>(s[h][0], s[h][1], v); break;
+          case MOE_ACT_RELU: gate_block<MOE_ACT_RELU>(s[h][0], s[h][1], v); break;
+          case MOE_ACT_SIGMOID: gate_block<MOE_ACT_SIGMOID>(s[h][0], s[h][1], v); break;
+          default: gate_block<MOE_ACT_NONE>(s[h][0], s[h][1], v);
+        }
+        store_block<T, FI, FJ>(e.y[0], e.ldy[0], i0 + h * di, j0, a.M, a.N, e.vec, e.stream, v, (uint16_t*)lds, lane);
+      }
+      return;
+    }
+  }
   const bool plain = KIND == kEpiStore || (KIND == kEpiLinear && !e.bias[0] && !e.pre[0] && !e.res && !e.y_f32 && e.act == MOE_ACT_NONE);
 #pragma unroll
   for (int h = 0; h < NI; ++h)
