@@ -285,10 +285,42 @@ inline int grad_rows(int64_t T, int64_t N) {
   return (int)((rows + 3) / 4 * 4);
 }
 
-// dense_tile_*.hip, dense_grad.hip (dtype: MOE_BF16 or MOE_F16)
-hipError_t launch_tile(int dtype, const TileArgs& a, int order_a, int order_b, int epi_kind, hipStream_t st);
-hipError_t launch_rows(int dtype, const TileArgs& a, int epi_kind, hipStream_t st);  // dense_rows.hip: M <= MOE_DENSE_ROW_TOKENS
-// Copies of up to three matrices with rows of whole 16-byte chunks, zeros past a row's end (dense_grad.hip).
+// The bias gradients from such sums: db[m][n] = sum over runs of part[run][m][n], in run order.
+struct BiasSumArgs {
+  const float* part;
+  void* db[2];  // NULL: not wanted
+  int32_t runs, mats, N;
+};
+// 32 columns per workgroup of 256, 8 threads per column take contiguous shares of the runs, added in LDS in order.  (One
+// thread per column took 31 us for 128 runs of 2048 columns: a chain of loads on 8 CUs; this 4 us.)
+template <typename T>
+MOE_DEV void bias_sum_block(const BiasSumArgs& a, uint32_t block, float* sums) {
+  const int64_t width = (int64_t)a.mats * a.N;
+  const int64_t c = (int64_t)block * 32 + (threadIdx.x & 31);
+  const int g = threadIdx.x >> 5;
+  float s = 0.0f;
+  if (c < width) {
+    const int end = (int)((int64_t)a.runs * (g + 1) / 8);
+#pragma unroll 8
+    for (int r = (int)((int64_t)a.runs * g / 8); r < end; ++r) s += a.part[r * width + c];
+  }
+  sums[g * 33 + (threadIdx.x & 31)] = s;
+  __syncthreads();
+  if (g || c >= width) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += sums[i * 33 + threadIdx.x];
+  T* db = (T*)(c < a.N ? a.db[0] : a.db[1]);
+  if (db) db[c < a.N ? c : c - a.N] = (T)s;
+}
+
+// dense_tile_bf16.hip, dense_tile_f16.hip
+hipError_t launch_forward_bf16(const TileArgs& a, int epi_kind, hipStream_t st);
+hipError_t launch_forward_f16(const TileArgs& a, int epi_kind, hipStream_t st);
+hipError_t launch_backward_bf16(const TileArgs& dx, const TileArgs& dw, const BiasSumArgs& db, hipStream_t st);
+hipError_t launch_backward_f16(const TileArgs& dx, const TileArgs& dw, const BiasSumArgs& db, hipStream_t st);
+// dense_rows.hip: up to MOE_DENSE_ROW_TOKENS tokens
+hipError_t launch_rows(int dtype, const TileArgs& a, int epi_kind, hipStream_t st);
+// dense_grad.hip.  PackArgs: copies of up to three matrices with rows of whole 16-byte chunks, zeros past a row's end.
 struct PackArgs {
   struct {
     const uint16_t* src;
@@ -299,8 +331,8 @@ struct PackArgs {
   int32_t count;
 };
 hipError_t launch_pack(const PackArgs& p, hipStream_t st);
-hipError_t launch_finish(int dtype, const TileArgs& a, int epi_kind, hipStream_t st);  // dense_grad.hip
+hipError_t launch_finish(int dtype, const TileArgs& a, int epi_kind, hipStream_t st);
 hipError_t launch_grad_in(int dtype, const GradArgs& a, bool gated, hipStream_t st);
-hipError_t launch_bias_sum(int dtype, const float* part, int runs, int mats, int N, void* db0, void* db1, hipStream_t st);
+hipError_t launch_bias_sum(int dtype, const BiasSumArgs& a, hipStream_t st);
 
 }  // namespace moe

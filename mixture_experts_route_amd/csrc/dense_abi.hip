@@ -111,59 +111,53 @@ static TileArgs tile_args(const moe_dense_dims* d, int64_t T, bool backward, voi
 
 static uint8_t* ws_at(void* ws, size_t off) { return (uint8_t*)ws + off; }
 
-// dx = sum over mats of dz[m] W[m], then dW[m] = dz[m]^T x.
+// dx = sum over mats of dz[m] W[m], dW[m] = dz[m]^T x, and the bias gradients (db.runs 0: none).
 static int run_products(const moe_dense_dims* d, int mats, const void* x, int64_t ldx, int32_t T, const void* const* w,
-                        const int64_t* ldw, const void* const* dz, int64_t ldz, int32_t len_dz,
-                        void* dx, int64_t ld_dx, void* const* dw,
-                        const int64_t* ld_dw, void* ws, hipStream_t st) {
+                        const int64_t* ldw, const void* const* dz, int64_t ldz, int32_t len_dz, void* dx, int64_t ld_dx,
+                        void* const* dw, const int64_t* ld_dw, const BiasSumArgs& db, void* ws, hipStream_t st) {
+  TileArgs ax = tile_args(d, T, true, ws), aw = tile_args(d, T, true, ws);
   if (dx) {
-    TileArgs a = tile_args(d, T, true, ws);
     for (int m = 0; m < mats; ++m) {
-      a.a[m] = dz[m];
-      a.lda[m] = ldz;
-      a.b[m] = w[m];
-      a.ldb[m] = ldw[m];
+      ax.a[m] = dz[m];
+      ax.lda[m] = ldz;
+      ax.b[m] = w[m];
+      ax.ldb[m] = ldw[m];
     }
-    a.M = T;
-    a.N = d->n_in;
-    a.R = d->n_out;
-    a.len_a = len_dz;
-    a.pack_a = nullptr;
-    a.nseg = mats;
-    a.nbatch = 1;
-    a.epi.y[0] = dx;
-    a.epi.ldy[0] = ld_dx;
-    a.epi.vec = vec8(dx, ld_dx);
-    const int rc = dense_status(launch_tile(d->dtype, a, kRows, kCols, kEpiStore, st));
-    if (rc) return rc;
+    ax.M = T;
+    ax.N = d->n_in;
+    ax.R = d->n_out;
+    ax.len_a = len_dz;
+    ax.pack_a = nullptr;
+    ax.nseg = mats;
+    ax.nbatch = 1;
+    ax.epi.y[0] = dx;
+    ax.epi.ldy[0] = ld_dx;
+    ax.epi.vec = vec8(dx, ld_dx);
   }
-  TileArgs a = tile_args(d, T, true, ws);
-  a.M = d->n_out;
-  a.N = d->n_in;
-  a.R = T;
-  a.nseg = 1;
-  a.pack_b[0] = a.pack_a;  // here B is x, once for both batches
-  a.pack_a = nullptr;
-  a.b[0] = a.b[1] = x;
-  a.ldb[0] = a.ldb[1] = ldx;
-  a.epi.vec = 1;
+  aw.M = d->n_out;
+  aw.N = d->n_in;
+  aw.R = T;
+  aw.nseg = 1;
+  aw.pack_b[0] = aw.pack_a;  // here B is x, once for both batches
+  aw.pack_a = nullptr;
+  aw.b[0] = aw.b[1] = x;
+  aw.ldb[0] = aw.ldb[1] = ldx;
+  aw.epi.vec = 1;
   for (int m = 0; m < mats; ++m) {
     if (!dw[m]) continue;
-    a.a[a.nbatch] = dz[m];
-    a.lda[a.nbatch] = ldz;
-    a.epi.y[a.nbatch] = dw[m];
-    a.epi.ldy[a.nbatch] = ld_dw[m];
-    a.epi.vec = a.epi.vec && vec8(dw[m], ld_dw[m]);
-    ++a.nbatch;
+    aw.a[aw.nbatch] = dz[m];
+    aw.lda[aw.nbatch] = ldz;
+    aw.epi.y[aw.nbatch] = dw[m];
+    aw.epi.ldy[aw.nbatch] = ld_dw[m];
+    aw.epi.vec = aw.epi.vec && vec8(dw[m], ld_dw[m]);
+    ++aw.nbatch;
   }
-  return a.nbatch ? dense_status(launch_tile(d->dtype, a, kCols, kCols, kEpiStore, st)) : MOE_OK;
+  return dense_status(d->dtype == MOE_BF16 ? launch_backward_bf16(ax, aw, db, st) : launch_backward_f16(ax, aw, db, st));
 }
 
-hipError_t launch_tile_bf16(const TileArgs& a, int oa, int ob, int kind, hipStream_t st);
-hipError_t launch_tile_f16(const TileArgs& a, int oa, int ob, int kind, hipStream_t st);
-
-hipError_t launch_tile(int dtype, const TileArgs& a, int oa, int ob, int kind, hipStream_t st) {
-  return dtype == MOE_BF16 ? launch_tile_bf16(a, oa, ob, kind, st) : launch_tile_f16(a, oa, ob, kind, st);
+static int run_forward(const moe_dense_dims* d, const TileArgs& a, int kind, hipStream_t st) {
+  if (a.M <= MOE_DENSE_ROW_TOKENS) return dense_status(launch_rows(d->dtype, a, kind, st));
+  return dense_status(d->dtype == MOE_BF16 ? launch_forward_bf16(a, kind, st) : launch_forward_f16(a, kind, st));
 }
 
 }  // namespace moe
@@ -220,9 +214,7 @@ MOE_API int moe_linear_forward(const moe_dense_dims* dims, const void* x, int64_
   a.epi.act = dims->act;
   a.epi.vec = vec8(y, ldy, ye) && vec8(residual_or_null, ld_residual, ye) &&
               vec8(pre_or_null, ld_pre) && vec8(bias_or_null, 0);
-  hipStream_t st = (hipStream_t)stream;
-  return dense_status(n_tokens <= MOE_DENSE_ROW_TOKENS ? launch_rows(dims->dtype, a, kEpiLinear, st)
-                                                       : launch_tile(dims->dtype, a, kRows, kRows, kEpiLinear, st));
+  return run_forward(dims, a, kEpiLinear, (hipStream_t)stream);
 }
 
 MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens,
@@ -266,9 +258,7 @@ MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t
   a.epi.act = dims->act;
   a.epi.vec = vec8(h, ldh) && vec8(gate_or_null, ld_gate) && vec8(up_or_null, ld_up) &&
               vec8(bias_gate_or_null, 0) && vec8(bias_up_or_null, 0);
-  hipStream_t st = (hipStream_t)stream;
-  return dense_status(n_tokens <= MOE_DENSE_ROW_TOKENS ? launch_rows(dims->dtype, a, kEpiGated, st)
-                                                       : launch_tile(dims->dtype, a, kRows, kRows, kEpiGated, st));
+  return run_forward(dims, a, kEpiGated, (hipStream_t)stream);
 }
 
 MOE_API int moe_linear_backward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
@@ -295,6 +285,7 @@ MOE_API int moe_linear_backward(const moe_dense_dims* dims, const void* x, int64
   const bool products = dx_or_null || dw_or_null;
   const bool whole = (uintptr_t)dy % 16 == 0 && ld_dy % 8 == 0 && dims->n_out % 8 == 0;
   const bool make = products && (act || !whole);
+  BiasSumArgs db{};
   if (make || dbias_or_null) {
     GradArgs g{};
     g.dy = dy;
@@ -309,15 +300,11 @@ MOE_API int moe_linear_backward(const moe_dense_dims* dims, const void* x, int64
     g.act = dims->act;
     g.rows = grad_rows(n_tokens, dims->n_out);
     if ((rc = dense_status(launch_grad_in(dims->dtype, g, false, st)))) return rc;
-    if (dbias_or_null &&
-        (rc = dense_status(launch_bias_sum(dims->dtype, g.part, (n_tokens + g.rows - 1) / g.rows, 1, dims->n_out,
-                                           dbias_or_null, nullptr, st))))
-      return rc;
+    if (dbias_or_null) db = {g.part, {dbias_or_null, nullptr}, (n_tokens + g.rows - 1) / g.rows, 1, dims->n_out};
   }
   const void* dz = make ? ws_at(ws, L.dz0) : dy;
   return run_products(dims, 1, x, ldx, n_tokens, &w, &ldw, &dz, make ? L.ldz : ld_dy,
-                      make ? (int32_t)L.ldz : dims->n_out, dx_or_null, ld_dx, &dw_or_null,
-                      &ld_dw, ws, st);
+                      make ? (int32_t)L.ldz : dims->n_out, dx_or_null, ld_dx, &dw_or_null, &ld_dw, db, ws, st);
 }
 
 MOE_API int moe_gated_backward(const moe_dense_dims* dims, const void* x, int64_t ldx, int32_t n_tokens,
@@ -363,15 +350,14 @@ MOE_API int moe_gated_backward(const moe_dense_dims* dims, const void* x, int64_
   g.act = dims->act;
   g.rows = grad_rows(n_tokens, dims->n_out);
   if ((rc = dense_status(launch_grad_in(dims->dtype, g, true, st)))) return rc;
-  if (sums && (rc = dense_status(launch_bias_sum(dims->dtype, g.part, (n_tokens + g.rows - 1) / g.rows, 2,
-                                                 dims->n_out, dbias_gate_or_null, dbias_up_or_null, st))))
-    return rc;
+  BiasSumArgs db{};
+  if (sums) db = {g.part, {dbias_gate_or_null, dbias_up_or_null}, (n_tokens + g.rows - 1) / g.rows, 2, dims->n_out};
   const void* w[2] = {w_gate, w_up};
   const int64_t ldw[2] = {ld_wg, ld_wu};
   const void* dz[2] = {g.dz0, g.dz1};
   void* dw[2] = {dw_gate_or_null, dw_up_or_null};
   const int64_t ld_dw[2] = {ld_dwg, ld_dwu};
-  return products ? run_products(dims, 2, x, ldx, n_tokens, w, ldw, dz, L.ldz, (int32_t)L.ldz, dx_or_null, ld_dx, dw, ld_dw, ws, st) : MOE_OK;
+  return run_products(dims, 2, x, ldx, n_tokens, w, ldw, dz, L.ldz, (int32_t)L.ldz, dx_or_null, ld_dx, dw, ld_dw, db, ws, st);
 }
 
 }  // extern "C"

@@ -102,27 +102,10 @@ __global__ __launch_bounds__(256) void k_grad_in(GradArgs a) {
   }
 }
 
-// db[m][n] = sum over runs of part[run][m][n]: 32 columns per workgroup, 8 threads per column take contiguous shares of
-// the runs, added in LDS in order.  (One thread per column took 31 us for 128 runs of 2048 columns: a chain of loads on 8 CUs.)
 template <typename T>
-__global__ __launch_bounds__(256) void k_bias_sum(const float* part, int runs, int mats, int N, T* db0, T* db1) {
-  __shared__ float sums[8][33];
-  const int64_t width = (int64_t)mats * N;
-  const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-  const int g = threadIdx.x >> 5;
-  float s = 0.0f;
-  if (c < width) {
-    const int end = (int)((int64_t)runs * (g + 1) / 8);
-#pragma unroll 8
-    for (int r = (int)((int64_t)runs * g / 8); r < end; ++r) s += part[r * width + c];
-  }
-  sums[g][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (g || c >= width) return;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) s += sums[i][threadIdx.x];
-  T* db = c < N ? db0 : db1;
-  if (db) db[c < N ? c : c - N] = (T)s;
+__global__ __launch_bounds__(256) void k_bias_sum(BiasSumArgs a) {
+  __shared__ float sums[8 * 33];
+  bias_sum_block<T>(a, blockIdx.x, sums);
 }
 
 // A chunk of 8 elements per thread and pass; blockIdx.y is the matrix.
@@ -204,10 +187,10 @@ hipError_t launch_grad_in(int dtype, const GradArgs& a, bool gated, hipStream_t 
   return hipGetLastError();
 }
 
-hipError_t launch_bias_sum(int dtype, const float* part, int runs, int mats, int N, void* db0, void* db1, hipStream_t st) {
-  const uint32_t grid = (uint32_t)((mats * (int64_t)N + 31) / 32);
-  if (dtype == MOE_BF16) k_bias_sum<__bf16><<<grid, 256, 0, st>>>(part, runs, mats, N, (__bf16*)db0, (__bf16*)db1);
-  else k_bias_sum<_Float16><<<grid, 256, 0, st>>>(part, runs, mats, N, (_Float16*)db0, (_Float16*)db1);
+hipError_t launch_bias_sum(int dtype, const BiasSumArgs& a, hipStream_t st) {
+  const uint32_t grid = (uint32_t)((a.mats * (int64_t)a.N + 31) / 32);
+  if (dtype == MOE_BF16) k_bias_sum<__bf16><<<grid, 256, 0, st>>>(a);
+  else k_bias_sum<_Float16><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

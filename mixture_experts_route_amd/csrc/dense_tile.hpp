@@ -536,20 +536,20 @@ struct HalfStream {
 };
 
 // 64 x 64 tile (gated: 64 x 32 outputs), 4 waves of 32 x 2 x 16, for products with too few large tiles to fill the chip: there
-// a step's arithmetic is short and the time is the copies' latency, so STAGES LDS buffers of one step (64 reduction elements,
-// 16 KB) keep STAGES - 1 steps in flight.  While a step's MFMAs run from registers the next step's fragments are read.
-template <typename T, int OA, int OB, int KIND, int STAGES>
-__global__ __launch_bounds__(256, 2) void k_tile_deep(TileArgs a) {
-  constexpr int W = 4, HI = 64, HJ = 32;
-  constexpr int kBytes = (HI + 2 * HJ) * kStepR * 2;  // of one stage: A, B0, B1
+// a step's arithmetic is short and the time is the copies' latency, so five LDS buffers of one step (64 reduction elements,
+// 16 KB) keep four steps in flight.  While a step's MFMAs run from registers the next step's fragments are read.
+constexpr int kDeepStages = 5, kDeepStageBytes = (64 + 2 * 32) * kStepR * 2;
+template <typename T, int OA, int OB, int KIND>
+MOE_DEV void deep_tile(const TileArgs& a, uint32_t id, uint32_t ids, uint16_t* lds) {
+  constexpr int STAGES = kDeepStages, W = 4, HI = 64, HJ = 32;
+  constexpr int kBytes = kDeepStageBytes;  // A, B0, B1
   typedef typename Operand<T>::v8 v8;
   constexpr int kCopies = OperandCopy<OA, HI, W>::kCopies + 2 * OperandCopy<OB, HJ, W>::kCopies;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES * kBytes / 2];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave >> 1, wj = wave & 1;
-  const TileIndex x = tile_index(a, blockIdx.x, gridDim.x);
+  const TileIndex x = tile_index(a, id, ids);
   constexpr int JT = KIND == kEpiGated ? HJ : 2 * HJ;
   const int64_t i0 = (int64_t)x.ti * HI, j0 = (int64_t)x.tj * JT;
 
@@ -628,6 +628,30 @@ __global__ __launch_bounds__(256, 2) void k_tile_deep(TileArgs a) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) s[0][h][n][0] = acc[h][n];
   finish_blocks<T, KIND>(a, x, i0 + wi * 32, 0, j0 + wj * 16, HJ, s, (float*)lds + wave * 1024, lane);
+}
+
+template <typename T, int OA, int OB, int KIND>
+__global__ __launch_bounds__(256, 2) void k_tile_deep(TileArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[kDeepStages * kDeepStageBytes / 2];
+  deep_tile<T, OA, OB, KIND>(a, blockIdx.x, gridDim.x, lds);
+}
+
+// A small backward pass in one launch: dx's tiles, dW's tiles, then the bias gradients' columns.  Alone each of the two
+// products leaves CUs idle, and a launch costs two to three microseconds (333 tokens, 1000 x 1357: 27.8 us as separate launches).
+template <typename T>
+__global__ __launch_bounds__(256, 2) void k_backward_small(TileArgs dx, TileArgs dw, BiasSumArgs db, uint32_t n_dx, uint32_t n_dw) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[kDeepStages * kDeepStageBytes / 2];
+  uint32_t id = blockIdx.x;
+  if (id < n_dx) {
+    deep_tile<T, kRows, kCols, kEpiStore>(dx, id, n_dx, lds);
+    return;
+  }
+  id -= n_dx;
+  if (id < n_dw) {
+    deep_tile<T, kCols, kCols, kEpiStore>(dw, id, n_dw, lds);
+    return;
+  }
+  bias_sum_block<T>(db, id - n_dw, (float*)lds);
 }
 
 // (2 WI FI 16) x (2 WJ FJ 16) tile, WI x WJ waves; a wave's quarter in (i half, j half) is FI x FJ fragments.
@@ -840,7 +864,7 @@ hipError_t start_plan(TileArgs a, int kernel, hipStream_t st) {
   switch (kernel) {
     case MOE_DENSE_TILE64:
       if (!set_tiles<64, KIND == kEpiGated ? 32 : 64, 256>(a, &count)) return hipErrorInvalidConfiguration;
-      k_tile_deep<T, OA, OB, KIND, 5><<<dim3((uint32_t)count), dim3(256), 0, st>>>(a);
+      k_tile_deep<T, OA, OB, KIND><<<dim3((uint32_t)count), dim3(256), 0, st>>>(a);
       return hipGetLastError();
     case MOE_DENSE_TILE128: return start_tile<T, OA, OB, KIND, 2, 2, 2, 2>(a, st);
     case MOE_DENSE_TILE256: return start_tile<T, OA, OB, KIND, 2, 4, 4, 2>(a, st);
@@ -892,9 +916,9 @@ bool pack_operands(TileArgs& a, bool whole_a, const bool (&whole_b)[2], hipStrea
   return true;
 }
 
-template <typename T, int OA, int OB, int KIND>
-hipError_t launch_tile_k(const TileArgs& args, hipStream_t st) {
-  TileArgs a = args;
+// The operands as the kernels will read them (copied where that pays), and the plan with its estimate.
+template <int OA, int OB, int KIND>
+hipError_t prepare_tile(TileArgs& a, DensePlan& plan, double& us, hipStream_t st) {
   bool whole_a = true, whole_b[2] = {true, true};
   for (int m = 0; m < (a.nseg > 1 || a.nbatch > 1 ? 2 : 1); ++m)
     whole_a = whole_a && whole_chunks(OA, a.a[m], a.lda[m], a.len_a);
@@ -907,8 +931,7 @@ hipError_t launch_tile_k(const TileArgs& args, hipStream_t st) {
     whole = pack_operands<OA, OB, KIND>(a, whole_a, whole_b, st, &err);
     if (err != hipSuccess) return err;
   }
-  double us;
-  DensePlan plan = plan_tile<OA, KIND>(a, whole, &us);
+  plan = plan_tile<OA, KIND>(a, whole, &us);
   if (g_dense_plan.kernel != MOE_DENSE_AUTO && (whole || g_dense_plan.kernel >= MOE_DENSE_ANY64))
     plan = {g_dense_plan.kernel, 1};
   if (g_dense_plan.splits) {
@@ -918,20 +941,60 @@ hipError_t launch_tile_k(const TileArgs& args, hipStream_t st) {
   }
   a.splits = plan.splits;
   a.epi.stream = 2.0 * a.M * a.N * a.nbatch >= 16e6;
+  return hipSuccess;
+}
+
+template <typename T, int OA, int OB, int KIND>
+hipError_t run_tile(const TileArgs& a, const DensePlan& plan, hipStream_t st) {
   const hipError_t e = start_plan<T, OA, OB, KIND>(a, plan.kernel, st);
   return e != hipSuccess || a.splits == 1 ? e : launch_finish(__is_same(T, __bf16) ? MOE_BF16 : MOE_F16, a, KIND, st);
 }
 
-template <typename T>
-hipError_t launch_tile_t(const TileArgs& a, int oa, int ob, int kind, hipStream_t st) {
-  if (oa == kRows && ob == kRows && kind == kEpiLinear) return launch_tile_k<T, kRows, kRows, kEpiLinear>(a, st);
-  if (oa == kRows && ob == kRows && kind == kEpiGated) return launch_tile_k<T, kRows, kRows, kEpiGated>(a, st);
-  if (oa == kRows && ob == kCols && kind == kEpiStore) return launch_tile_k<T, kRows, kCols, kEpiStore>(a, st);
-  if (oa == kCols && ob == kCols && kind == kEpiStore) return launch_tile_k<T, kCols, kCols, kEpiStore>(a, st);
-  return hipErrorInvalidValue;
+template <typename T, int OA, int OB, int KIND>
+hipError_t launch_tile_k(const TileArgs& args, hipStream_t st) {
+  TileArgs a = args;
+  DensePlan plan;
+  double us;
+  const hipError_t e = prepare_tile<OA, OB, KIND>(a, plan, us, st);
+  return e != hipSuccess ? e : run_tile<T, OA, OB, KIND>(a, plan, st);
 }
 
-hipError_t launch_tile_bf16(const TileArgs& a, int oa, int ob, int kind, hipStream_t st);
-hipError_t launch_tile_f16(const TileArgs& a, int oa, int ob, int kind, hipStream_t st);
+// The products (and bias sums) of a backward pass; dx.nseg, dw.nbatch or db.runs 0: not wanted.
+template <typename T>
+hipError_t launch_backward_t(const TileArgs& dx_args, const TileArgs& dw_args, const BiasSumArgs& db, hipStream_t st) {
+  TileArgs dx = dx_args, dw = dw_args;
+  DensePlan px, pw;
+  double ux = 0, uw = 0;
+  hipError_t e;
+  if (dx.nseg && (e = prepare_tile<kRows, kCols, kEpiStore>(dx, px, ux, st)) != hipSuccess) return e;
+  if (dw.nbatch && (e = prepare_tile<kCols, kCols, kEpiStore>(dw, pw, uw, st)) != hipSuccess) return e;
+  const bool small = [&] {  // both on 64 x 64 tiles by choice, and faster together unsplit
+    if (!dx.nseg || !dw.nbatch || px.kernel != MOE_DENSE_TILE64 || pw.kernel != MOE_DENSE_TILE64) return false;
+    if (g_dense_plan.splits > 1) return false;
+    const TileCost& k = kWholeCosts[0];
+    const int64_t nx = (int64_t)((dx.M + 63) / 64) * ((dx.N + 63) / 64), nw = (int64_t)((dw.M + 63) / 64) * ((dw.N + 63) / 64) * dw.nbatch;
+    const int64_t sx = (int64_t)((dx.R + kStepR - 1) / kStepR) * dx.nseg, sw = (dw.R + kStepR - 1) / kStepR;
+    const int64_t per_cu = (nx + nw + 255) / 256;
+    const double each = per_cu > 1 ? k.pair / 2 : k.lone, mean = (double)(nx * sx + nw * sw) / 256 * each;
+    const double longest = (sx > sw ? sx : sw) * k.lone;
+    return 3.0 + (mean > longest ? mean : longest) + k.round * per_cu < ux + uw;
+  }();
+  if (small) {
+    int64_t nx, nw;
+    dx.splits = dw.splits = 1;
+    if (!set_tiles<64, 64, 256>(dx, &nx) || !set_tiles<64, 64, 256>(dw, &nw)) return hipErrorInvalidConfiguration;
+    const int64_t nb = db.runs ? ((int64_t)db.mats * db.N + 31) / 32 : 0;
+    k_backward_small<T><<<dim3((uint32_t)(nx + nw + nb)), dim3(256), 0, st>>>(dx, dw, db, (uint32_t)nx, (uint32_t)nw);
+    return hipGetLastError();
+  }
+  if (db.runs && (e = launch_bias_sum(__is_same(T, __bf16) ? MOE_BF16 : MOE_F16, db, st)) != hipSuccess) return e;
+  if (dx.nseg && (e = run_tile<T, kRows, kCols, kEpiStore>(dx, px, st)) != hipSuccess) return e;
+  return dw.nbatch ? run_tile<T, kCols, kCols, kEpiStore>(dw, pw, st) : hipSuccess;
+}
+
+template <typename T>
+hipError_t launch_forward_t(const TileArgs& a, int kind, hipStream_t st) {
+  return kind == kEpiGated ? launch_tile_k<T, kRows, kRows, kEpiGated>(a, st) : launch_tile_k<T, kRows, kRows, kEpiLinear>(a, st);
+}
 
 }  // namespace moe
