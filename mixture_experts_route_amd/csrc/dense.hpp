@@ -126,19 +126,19 @@ struct DenseEpi {
   int64_t ldp[2];
   int32_t y_f32;       // linear: y and res are fp32
   int32_t act;
-  int32_t vec;         // every matrix above may be moved 8 elements at a time (16-byte aligned rows)
   int32_t stream;      // outputs larger than the L2s: stored with the non-temporal hint (launch_tile), so that they leave
                        // the operands in the caches (4096 tokens and outputs: 512 inputs 28.6 -> 24.9 us, 4096 inputs 110.8 -> 106.3 us)
 };
 
-// 8 consecutive elements of a row as fp32, or the first n of them.
+// 8 consecutive elements of a row as fp32, or the first n of them.  Global accesses of 16 bytes need only the element's
+// alignment here, so rows of any address and stride move 8 elements at a time.
 template <typename T>
-MOE_DEV void load8(const void* base, int64_t off, int n, bool vec, float (&v)[8]) {
+MOE_DEV void load8(const void* base, int64_t off, int n, float (&v)[8]) {
   const T* p = (const T*)base + off;
-  if (vec && n == 8) {
+  if (n == 8) {
     typedef T v8 __attribute__((ext_vector_type(8)));
-    typedef v8 v8_16 __attribute__((aligned(16)));
-    const v8 t = *(const v8_16*)p;
+    typedef v8 v8_any __attribute__((aligned(sizeof(T))));
+    const v8 t = *(const v8_any*)p;
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] = (float)t[c];
   } else {
@@ -147,16 +147,16 @@ MOE_DEV void load8(const void* base, int64_t off, int n, bool vec, float (&v)[8]
   }
 }
 template <typename T>
-MOE_DEV void store8(void* base, int64_t off, int n, bool vec, const float (&v)[8], bool stream = false) {
+MOE_DEV void store8(void* base, int64_t off, int n, const float (&v)[8], bool stream = false) {
   T* p = (T*)base + off;
-  if (vec && n == 8) {
+  if (n == 8) {
     typedef T v8 __attribute__((ext_vector_type(8)));
-    typedef v8 v8_16 __attribute__((aligned(16)));
+    typedef v8 v8_any __attribute__((aligned(sizeof(T))));
     v8 t;
 #pragma unroll
     for (int c = 0; c < 8; ++c) t[c] = (T)v[c];
-    if (stream) __builtin_nontemporal_store(t, (v8_16*)p);
-    else *(v8_16*)p = t;
+    if (stream) __builtin_nontemporal_store(t, (v8_any*)p);
+    else *(v8_any*)p = t;
   } else {
 #pragma unroll
     for (int c = 0; c < 8; ++c)
@@ -167,46 +167,46 @@ MOE_DEV void store8(void* base, int64_t off, int n, bool vec, const float (&v)[8
 // Outputs (i, j .. j + n - 1), n = 1..8, j a multiple of 8: s0 = the fp32 sums (gated: the gate's), s1 = the up's.
 template <typename T, int KIND>
 MOE_DEV void finish8(const DenseEpi& e, int batch, int64_t i, int j, int n, float (&s0)[8], float (&s1)[8]) {
-  const bool vec = e.vec, stream = e.stream;
+  const bool stream = e.stream;
   if constexpr (KIND == kEpiStore) {
-    store8<T>(batch ? e.y[1] : e.y[0], i * (batch ? e.ldy[1] : e.ldy[0]) + j, n, vec, s0, stream);
+    store8<T>(batch ? e.y[1] : e.y[0], i * (batch ? e.ldy[1] : e.ldy[0]) + j, n, s0, stream);
     return;
   }
   float t[8];
   if (e.bias[0]) {
-    load8<T>(e.bias[0], j, n, vec, t);
+    load8<T>(e.bias[0], j, n, t);
 #pragma unroll
     for (int c = 0; c < 8; ++c) s0[c] += t[c];
   }
   if constexpr (KIND == kEpiGated) {
     if (e.bias[1]) {
-      load8<T>(e.bias[1], j, n, vec, t);
+      load8<T>(e.bias[1], j, n, t);
 #pragma unroll
       for (int c = 0; c < 8; ++c) s1[c] += t[c];
     }
   }
   if (e.pre[0]) {
-    store8<T>(e.pre[0], i * e.ldp[0] + j, n, vec, s0, stream);
-    if constexpr (KIND == kEpiGated) store8<T>(e.pre[1], i * e.ldp[1] + j, n, vec, s1, stream);
+    store8<T>(e.pre[0], i * e.ldp[0] + j, n, s0, stream);
+    if constexpr (KIND == kEpiGated) store8<T>(e.pre[1], i * e.ldp[1] + j, n, s1, stream);
   }
   act_values(e.act, s0);
   if constexpr (KIND == kEpiGated) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) s0[c] *= s1[c];
-    store8<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0, stream);
+    store8<T>(e.y[0], i * e.ldy[0] + j, n, s0, stream);
   } else {
     if (e.res) {
       if (e.y_f32)
-        load8<float>(e.res, i * e.ldr + j, n, vec, t);
+        load8<float>(e.res, i * e.ldr + j, n, t);
       else
-        load8<T>(e.res, i * e.ldr + j, n, vec, t);
+        load8<T>(e.res, i * e.ldr + j, n, t);
 #pragma unroll
       for (int c = 0; c < 8; ++c) s0[c] += t[c];
     }
     if (e.y_f32)
-      store8<float>(e.y[0], i * e.ldy[0] + j, n, vec, s0, stream);
+      store8<float>(e.y[0], i * e.ldy[0] + j, n, s0, stream);
     else
-      store8<T>(e.y[0], i * e.ldy[0] + j, n, vec, s0, stream);
+      store8<T>(e.y[0], i * e.ldy[0] + j, n, s0, stream);
   }
 }
 
@@ -256,10 +256,10 @@ MOE_DEV void finish_or_park(const TileArgs& a, int split, int batch, int64_t i, 
   if (a.splits == 1) {
     finish8<T, KIND>(a.epi, batch, i, j, n, s0, s1);
   } else if constexpr (KIND == kEpiGated) {
-    store8<float>(part_at(a, split, 2, 0, i, j), 0, 8, true, s0);
-    store8<float>(part_at(a, split, 2, 1, i, j), 0, 8, true, s1);
+    store8<float>(part_at(a, split, 2, 0, i, j), 0, 8, s0);
+    store8<float>(part_at(a, split, 2, 1, i, j), 0, 8, s1);
   } else {
-    store8<float>(part_at(a, split, a.nbatch, batch, i, j), 0, 8, true, s0);
+    store8<float>(part_at(a, split, a.nbatch, batch, i, j), 0, 8, s0);
   }
 }
 

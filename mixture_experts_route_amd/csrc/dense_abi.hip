@@ -94,9 +94,6 @@ static int check_dense_ws(const moe_dense_dims* d, int32_t T, bool backward, con
 
 static int dense_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
-// 8-element accesses at multiples of 8: rows start and stay 16-byte aligned.
-static bool vec8(const void* p, int64_t ld, int elem = 2) { return !p || ((uintptr_t)p % 16 == 0 && ld * elem % 16 == 0); }
-
 static TileArgs tile_args(const moe_dense_dims* d, int64_t T, bool backward, void* ws) {
   const DenseWs L = dense_ws(d, T, backward);
   auto at = [&](size_t off) { return off ? (uint16_t*)((uint8_t*)ws + off) : nullptr; };
@@ -132,7 +129,6 @@ static int run_products(const moe_dense_dims* d, int mats, const void* x, int64_
     ax.nbatch = 1;
     ax.epi.y[0] = dx;
     ax.epi.ldy[0] = ld_dx;
-    ax.epi.vec = vec8(dx, ld_dx);
   }
   aw.M = d->n_out;
   aw.N = d->n_in;
@@ -142,14 +138,12 @@ static int run_products(const moe_dense_dims* d, int mats, const void* x, int64_
   aw.pack_a = nullptr;
   aw.b[0] = aw.b[1] = x;
   aw.ldb[0] = aw.ldb[1] = ldx;
-  aw.epi.vec = 1;
   for (int m = 0; m < mats; ++m) {
     if (!dw[m]) continue;
     aw.a[aw.nbatch] = dz[m];
     aw.lda[aw.nbatch] = ldz;
     aw.epi.y[aw.nbatch] = dw[m];
     aw.epi.ldy[aw.nbatch] = ld_dw[m];
-    aw.epi.vec = aw.epi.vec && vec8(dw[m], ld_dw[m]);
     ++aw.nbatch;
   }
   return dense_status(d->dtype == MOE_BF16 ? launch_backward_bf16(ax, aw, db, st) : launch_backward_f16(ax, aw, db, st));
@@ -212,8 +206,6 @@ MOE_API int moe_linear_forward(const moe_dense_dims* dims, const void* x, int64_
   a.epi.pre[0] = pre_or_null;
   a.epi.ldp[0] = ld_pre;
   a.epi.act = dims->act;
-  a.epi.vec = vec8(y, ldy, ye) && vec8(residual_or_null, ld_residual, ye) &&
-              vec8(pre_or_null, ld_pre) && vec8(bias_or_null, 0);
   return run_forward(dims, a, kEpiLinear, (hipStream_t)stream);
 }
 
@@ -256,8 +248,6 @@ MOE_API int moe_gated_forward(const moe_dense_dims* dims, const void* x, int64_t
   a.epi.ldp[0] = ld_gate;
   a.epi.ldp[1] = ld_up;
   a.epi.act = dims->act;
-  a.epi.vec = vec8(h, ldh) && vec8(gate_or_null, ld_gate) && vec8(up_or_null, ld_up) &&
-              vec8(bias_gate_or_null, 0) && vec8(bias_up_or_null, 0);
   return run_forward(dims, a, kEpiGated, (hipStream_t)stream);
 }
 

@@ -153,7 +153,7 @@ __global__ __launch_bounds__(256) void k_finish(TileArgs a) {
 #pragma unroll
     for (int m = 0; m < kMats; ++m) {
       float t[8];
-      load8<float>(part_at(a, p, mats, KIND == kEpiGated ? m : batch, i, j), 0, 8, true, t);
+      load8<float>(part_at(a, p, mats, KIND == kEpiGated ? m : batch, i, j), 0, 8, t);
 #pragma unroll
       for (int c = 0; c < 8; ++c) s[m][c] += t[c];
     }

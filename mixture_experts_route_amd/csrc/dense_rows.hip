@@ -1,7 +1,5 @@
 // The dense operators' forward pass for up to MOE_DENSE_ROW_TOKENS tokens: the weights streamed once, every
 // token at a time on the matrix cores.
-#include <algorithm>
-
 #include "dense.hpp"
 
 namespace moe {
@@ -137,27 +135,46 @@ static hipError_t start_rows(const TileArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// How many weight rows a workgroup takes and how many workgroups share them, by the outputs and inputs alone.  The time is
+// the most loaded CU's: whole workgroups per CU times their rows (and the activations beside them, as 6 rows' worth); what its
+// waves have in flight at once costs one latency, about 2 us, the rest comes at about 17 KB per microsecond.  A shared
+// reduction adds a launch, 2.5 us, and the traffic of its sums (16 tokens').  Measured, 16 tokens: 8192 inputs and outputs
+// 40.0 us with one fragment, 34.7 with two; 8192 inputs, 2048 outputs 19.8 us alone, 14.6 shared by four; 4096 inputs, 1024
+// outputs 11.1 us, 8.0 by four.  One token: 2048 inputs, 768 gated outputs 5.6 us, 6.4 by two; 6912 inputs, 2304 gated
+// outputs (288 workgroups for 256 CUs) 24.8 us, 19.2 by eight.
+struct RowPlan {
+  int frags, splits;
+};
+static RowPlan plan_rows(int64_t groups, int64_t R, int64_t sums) {
+  RowPlan best = {1, 1};
+  double least = 1e300;
+  for (int f = 1; f <= 2; ++f)
+    for (int s = 1; s <= kMaxSplits && (s == 1 || R / s >= 512); ++s) {
+      const int64_t per_cu = ((groups + f - 1) / f * s + 255) / 256;
+      const double late = (double)per_cu / s * (16 * f + 6) * R * 2 - 88e3;
+      const double us = 2.0 + (late > 0 ? late / 17e3 : 0.0) + (s > 1 ? 2.5 + 16.0 * sums * s * 8 / 4e6 : 0.0);
+      if (us < least) {
+        least = us;
+        best = {f, s};
+      }
+    }
+  return best;
+}
+
 template <typename T, int KIND>
 static hipError_t launch_rows_k(const TileArgs& args, hipStream_t st) {
   TileArgs a = args;
   auto whole_rows = [](const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
   bool whole = a.R % 8 == 0 && whole_rows(a.a[0], a.lda[0]) && whole_rows(a.b[0], a.ldb[0]);
   if (KIND == kEpiGated) whole = whole && whole_rows(a.b[1], a.ldb[1]);
-  // With few workgroups and long rows several share an output's rows: a CU draws about 17 KB per microsecond from memory, so
-  // the rows are spread over all 256; the second launch costs 2.5 us (8192 inputs, 2048 outputs: 19.8 us as 128 workgroups,
-  // 16.4 us as 256; 4096 inputs, 1024 outputs: 11.1 and 8.0 us; 2048 inputs, 768 gated outputs: 5.6 and 6.4 us).
-  const int outs = KIND == kEpiGated ? 8 : 16;
-  const int groups = (a.N + outs - 1) / outs;
-  a.splits = 1;
-  if (a.R >= 4096) a.splits = std::max(1, std::min(std::min(256 / groups, a.R / 1024), kMaxSplits));
-  if (g_dense_plan.splits) a.splits = g_dense_plan.splits;
+  constexpr int outs = KIND == kEpiGated ? 8 : 16;
+  RowPlan plan = plan_rows((a.N + outs - 1) / outs, a.R, (int64_t)a.N * (KIND == kEpiGated ? 2 : 1));
+  if (g_dense_plan.splits) plan.splits = g_dense_plan.splits;
+  a.splits = plan.splits;
   while (a.splits > 1 && split_bytes(a.splits, KIND == kEpiGated ? 2 : 1, a.M, a.N) > a.part_bytes) --a.splits;
   hipError_t e;
-  if (!whole) e = start_rows<T, KIND, 1, false>(a, st);
-  // Twice the outputs per workgroup once that leaves one per CU: every weight load then shares its activation load with
-  // another (16 tokens, 8192 inputs and outputs: 40.0 -> 34.7 us).
-  else if (groups >= 512) e = start_rows<T, KIND, 2, true>(a, st);
-  else e = start_rows<T, KIND, 1, true>(a, st);
+  if (plan.frags == 1) e = whole ? start_rows<T, KIND, 1, true>(a, st) : start_rows<T, KIND, 1, false>(a, st);
+  else e = whole ? start_rows<T, KIND, 2, true>(a, st) : start_rows<T, KIND, 2, false>(a, st);
   return e != hipSuccess || a.splits == 1 ? e : launch_finish(__is_same(T, __bf16) ? MOE_BF16 : MOE_F16, a, KIND, st);
 }
 

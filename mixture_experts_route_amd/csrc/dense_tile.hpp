@@ -130,7 +130,7 @@ MOE_DEV void finish_fragments(const TileArgs& a, const TileIndex& x, int64_t i0,
 }
 
 template <typename T, int FI, int FJ>
-MOE_DEV void store_block(void* y, int64_t ldy, int64_t i0, int64_t j0, int M, int N, bool vec, bool stream,
+MOE_DEV void store_block(void* y, int64_t ldy, int64_t i0, int64_t j0, int M, int N, bool stream,
                          const float4v (&s)[FI][FJ], uint16_t* lds, int lane) {
   typedef typename Operand<T>::v8 v8;
   typedef T v4 __attribute__((ext_vector_type(4)));
@@ -151,24 +151,28 @@ MOE_DEV void store_block(void* y, int64_t ldy, int64_t i0, int64_t j0, int M, in
   const int64_t cols = N - (j0 + j);
   T* p = (T*)y + (i0 + r0) * ldy + j0 + j;
   const int64_t rows = M - i0;
-  if (vec && N - j0 >= C) {
+  typedef v8 v8_any __attribute__((aligned(2)));
+  if (N - j0 >= C) {
 #pragma unroll
     for (int r = 0; r < R; r += kRowsPer) {
       const v8 t = *(const v8*)(lds + pos(r0 + r, lane % kLanes));
       if (r0 + r < rows && r0 + r < R) {
-        typedef v8 v8_16 __attribute__((aligned(16)));
-        if (stream) __builtin_nontemporal_store(t, (v8_16*)(p + r * ldy));
-        else *(v8_16*)(p + r * ldy) = t;
+        if (stream) __builtin_nontemporal_store(t, (v8_any*)(p + r * ldy));
+        else *(v8_any*)(p + r * ldy) = t;
       }
     }
   } else {
 #pragma clang loop unroll(disable)
     for (int r = r0; r < R; r += kRowsPer) {
       const v8 t = *(const v8*)(lds + pos(r, lane % kLanes));
-      if (r < rows)
+      if (r >= rows) continue;
+      if (cols >= 8) {
+        *(v8_any*)(p + (r - r0) * ldy) = t;
+      } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           if (c < cols) p[(r - r0) * ldy + c] = t[c];
+      }
     }
   }
   __builtin_amdgcn_wave_barrier();
@@ -222,7 +226,7 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
           case MOE_ACT_SIGMOID: gate_block<MOE_ACT_SIGMOID>(s[h][0], s[h][1], v); break;
           default: gate_block<MOE_ACT_NONE>(s[h][0], s[h][1], v);
         }
-        store_block<T, FI, FJ>(e.y[0], e.ldy[0], i0 + h * di, j0, a.M, a.N, e.vec, e.stream, v, (uint16_t*)lds, lane);
+        store_block<T, FI, FJ>(e.y[0], e.ldy[0], i0 + h * di, j0, a.M, a.N, e.stream, v, (uint16_t*)lds, lane);
       }
       return;
     }
@@ -237,7 +241,7 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
         const int mat = kGated ? hj : x.batch, mats = kGated ? 2 : a.nbatch;
         store_block_f32<FI, FJ>(part_at(a, x.split, mats, mat, 0, 0), (a.N + 7) / 8 * 8, i, j, a.M, (a.N + 7) / 8 * 8, s[h][hj], lane);
       } else if (!kGated && plain) {
-        store_block<T, FI, FJ>(x.batch ? e.y[1] : e.y[0], x.batch ? e.ldy[1] : e.ldy[0], i, j, a.M, a.N, e.vec, e.stream, s[h][hj],
+        store_block<T, FI, FJ>(x.batch ? e.y[1] : e.y[0], x.batch ? e.ldy[1] : e.ldy[0], i, j, a.M, a.N, e.stream, s[h][hj],
                                (uint16_t*)lds, lane);
       } else if (KIND != kEpiStore && !(kGated && hj)) {
         finish_fragments<T, KIND, FI, FJ>(a, x, i, j, s[h][hj], s[h][1], lds, lane);
