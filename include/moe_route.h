@@ -472,21 +472,23 @@ MOE_API int moe_pool_debug_fail_copies(moe_pool* pool, int32_t after_n);
  * A gated block whose h goes through a linear (W [hidden][F], r = the routed layer's fp32 y) adds a
  * dense shared expert to moe_layer_forward's output.
  *
- * Conventions, beyond those at the top of this file:
+ * Conventions, beyond those at the top of this file (whose 16-byte rule for x and y does not hold here):
  *   - dims->dtype is the type of x, every weight, bias, saved pre-activation, h, incoming gradient
  *     and result of a backward pass: MOE_BF16 or MOE_F16 (anything else: MOE_EUNSUPPORTED).  y and r of the
  *     linear share y_dtype: dims->dtype or MOE_F32.
  *   - ld* is a matrix's row stride in elements, at least its row length and at most MOE_DENSE_MAX_LD;
- *     rows may start at any element-aligned address (a slice of a wider tensor, an odd width).  Rows
- *     of 16-byte aligned addresses, strides and lengths run the asynchronous-copy kernels, others a
- *     slower variant of them.  A misaligned element (odd address) is MOE_EINVAL.
+ *     rows may start at any element-aligned address (a slice of a wider tensor, an odd width; an odd
+ *     address is MOE_EINVAL).  Operands on 16-byte addresses with strides (and n_in) a multiple of 8 run the
+ *     asynchronous-copy kernels; others are first copied into the workspace or run slower kernels.
  *   - 1 <= n_in, n_out <= MOE_DENSE_MAX_WIDTH; 1 <= n_tokens <= MOE_DENSE_MAX_TOKENS (beyond:
  *     MOE_EUNSUPPORTED).
  *   - Sums are fp32 in a fixed order, so equal calls give equal bits.  Up to
  *     MOE_DENSE_ROW_TOKENS tokens a forward pass gives a token the same bits alone and in any batch.
- *     Results are rounded to their type once (to nearest even); a value beyond fp16's range becomes infinite, as the
- *     type has it.  The backward passes round dz (dg, du) to dims->dtype before the matrix products;
- *     the bias gradients sum it unrounded.
+ *     Results are rounded to their type once (to nearest even); a value beyond fp16's range becomes
+ *     infinite, as the type has it.  The backward passes round dz (dg, du) to dims->dtype before the
+ *     matrix products; the bias gradients sum it unrounded.
+ *   - A NaN or an infinity stays in the rows and columns that its definition reaches; nothing between the
+ *     rows of a matrix (ld > row length) is used, nor written.
  *   - Outputs must not overlap inputs or each other, except y on r exactly (same address and
  *     stride).  A NULL output of a backward pass is not computed; at least one must be given.
  *   - `ws` as everywhere: moe_dense_workspace_bytes(dims, n_tokens, backward) bytes, cleared once
