@@ -148,15 +148,20 @@ __global__ __launch_bounds__(256) void k_finish(TileArgs a) {
   const int64_t row = id / chunks;
   const int batch = row >= a.M;
   const int64_t i = row - (int64_t)batch * a.M;
-  float s[2][8] = {};
-  for (int p = 0; p < a.splits; ++p)
+  // every load goes out before the first sum
+  float t[kMaxSplits][kMats][8], s[2][8] = {};
 #pragma unroll
-    for (int m = 0; m < kMats; ++m) {
-      float t[8];
-      load8<float>(part_at(a, p, mats, KIND == kEpiGated ? m : batch, i, j), 0, 8, t);
+  for (int p = 0; p < kMaxSplits; ++p)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) s[m][c] += t[c];
-    }
+    for (int m = 0; m < kMats; ++m)
+      if (p < a.splits) load8<float>(part_at(a, p, mats, KIND == kEpiGated ? m : batch, i, j), 0, 8, t[p][m]);
+#pragma unroll
+  for (int p = 0; p < kMaxSplits; ++p)
+    if (p < a.splits)
+#pragma unroll
+      for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s[m][c] += t[p][m][c];
   finish8<T, KIND>(a.epi, batch, i, j, a.N - j < 8 ? a.N - j : 8, s[0], s[1]);
 }
 
