@@ -127,11 +127,12 @@ struct DenseEpi {
   int32_t y_f32;       // linear: y and res are fp32
   int32_t act;
   int32_t stream;      // outputs larger than the L2s: stored with the non-temporal hint (launch_tile), so that they leave
-                       // the operands in the caches (4096 tokens and outputs: 512 inputs 28.6 -> 24.9 us, 4096 inputs 110.8 -> 106.3 us)
+                       // the operands in the caches (4096 tokens and outputs: 512 inputs 28.6 -> 24.9 us, 4096
+                       // inputs 110.8 -> 106.3 us)
 };
 
-// 8 consecutive elements of a row as fp32, or the first n of them.  Global accesses of 16 bytes need only the element's
-// alignment here, so rows of any address and stride move 8 elements at a time.
+// 8 consecutive elements of a row as fp32, or the first n of them. Global accesses of 16 bytes need only the
+// element's alignment here, so rows of any address and stride move 8 elements at a time.
 template <typename T>
 MOE_DEV void load8(const void* base, int64_t off, int n, float (&v)[8]) {
   const T* p = (const T*)base + off;
@@ -217,8 +218,9 @@ MOE_DEV void finish8(const DenseEpi& e, int batch, int64_t i, int j, int n, floa
 //   dx          A = dz  kRows, B = W   kCols   (gated: two segments, dg Wg then du Wu, in one sum)
 //   dW          A = dz  kCols, B = x   kCols   (gated: two batches, dg and du)
 enum OperandOrder { kRows = 0, kCols = 1 };
-// Where workgroups share a tile's reduction they leave their fp32 sums in the workspace, and a second launch adds them in
-// split order and applies the epilogue: [split][mat][i][part_ld], mat = the batch (gated: gate, up).
+// Where workgroups share a tile's reduction they leave their fp32 sums in the workspace, and a second launch
+// adds them in split order and applies the epilogue: [split][mat][i][part_ld], mat = the batch (gated: gate,
+// up).
 constexpr size_t kDensePartBytes = 32u << 20;
 constexpr int kMaxSplits = 8;
 
@@ -291,8 +293,8 @@ struct BiasSumArgs {
   void* db[2];  // NULL: not wanted
   int32_t runs, mats, N;
 };
-// 32 columns per workgroup of 256, 8 threads per column take contiguous shares of the runs, added in LDS in order.  (One
-// thread per column took 31 us for 128 runs of 2048 columns: a chain of loads on 8 CUs; this 4 us.)
+// 32 columns per workgroup of 256, 8 threads per column take contiguous shares of the runs, added in LDS in
+// order. (One thread per column took 31 us for 128 runs of 2048 columns: a chain of loads on 8 CUs; this 4 us.)
 template <typename T>
 MOE_DEV void bias_sum_block(const BiasSumArgs& a, uint32_t block, float* sums) {
   const int64_t width = (int64_t)a.mats * a.N;
@@ -320,7 +322,8 @@ hipError_t launch_backward_bf16(const TileArgs& dx, const TileArgs& dw, const Bi
 hipError_t launch_backward_f16(const TileArgs& dx, const TileArgs& dw, const BiasSumArgs& db, hipStream_t st);
 // dense_rows.hip: up to MOE_DENSE_ROW_TOKENS tokens
 hipError_t launch_rows(int dtype, const TileArgs& a, int epi_kind, hipStream_t st);
-// dense_grad.hip.  PackArgs: copies of up to three matrices with rows of whole 16-byte chunks, zeros past a row's end.
+// dense_grad.hip. PackArgs: copies of up to three matrices with rows of whole 16-byte chunks, zeros past a
+// row's end.
 struct PackArgs {
   struct {
     const uint16_t* src;

@@ -6,8 +6,8 @@ namespace moe {
 
 DensePlan g_dense_plan = {MOE_DENSE_AUTO, 0};
 
-// Workspace: control words, the sums of split reductions, then for a backward pass dz (gated: dg, du) in the operands' type with rows
-// padded to whole 16-byte chunks, and the bias gradients' partial sums.
+// Workspace: control words, the sums of split reductions, then for a backward pass dz (gated: dg, du) in the
+// operands' type with rows padded to whole 16-byte chunks, and the bias gradients' partial sums.
 struct DenseWs {
   size_t part, x, w[2], dz0, dz1, bias_part, total;
   int64_t ldz;
@@ -31,7 +31,8 @@ static DenseWs dense_ws(const moe_dense_dims* d, int64_t T, bool backward) {
   DenseWs L{};
   L.part = kCtrlBytes;
   size_t off = dense_align(L.part + part_bytes(d, T, backward));
-  // copies of operands without whole 16-byte rows: x always (its stride is the caller's), the weights when n_in says so
+  // copies of operands without whole 16-byte rows: x always (its stride is the caller's), the weights when n_in
+  // says so
   const int64_t ld_in = ((int64_t)d->n_in + 7) / 8 * 8;
   if (T > MOE_DENSE_ROW_TOKENS || backward) {
     L.x = off;

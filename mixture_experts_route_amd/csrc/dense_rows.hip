@@ -4,13 +4,13 @@
 
 namespace moe {
 
-// Bound by the weights' bytes.  One v_mfma_f32_16x16x32 takes 16 weight rows (one row per lane index l % 16, 16 bytes of
-// it per lane) and all tokens as its 16 columns; a column depends on its own token only, so absent tokens repeat the last
-// one and are dropped, and a token's result is the same in any batch.  A workgroup owns FRAGS x 16 weight rows: as many
-// outputs (linear), or half as many outputs' rows of Wg and of Wu (FRAGS = 1: 8 rows of each in one fragment).  Its 8
-// waves take the blocks of 64 elements of its share of the reduction in turn, each from global memory straight into
-// registers (four blocks in flight per wave), and their sums meet in LDS in wave order.  Nothing in that order, nor in
-// the choice of FRAGS and splits, depends on the tokens.
+// Bound by the weights' bytes. One v_mfma_f32_16x16x32 takes 16 weight rows (one row per lane index l % 16, 16
+// bytes of it per lane) and all tokens as its 16 columns; a column depends on its own token only, so absent
+// tokens repeat the last one and are dropped, and a token's result is the same in any batch. A workgroup owns
+// FRAGS x 16 weight rows: as many outputs (linear), or half as many outputs' rows of Wg and of Wu (FRAGS = 1: 8
+// rows of each in one fragment). Its 8 waves take the blocks of 64 elements of its share of the reduction in
+// turn, each from global memory straight into registers (four blocks in flight per wave), and their sums meet
+// in LDS in wave order. Nothing in that order, nor in the choice of FRAGS and splits, depends on the tokens.
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
 constexpr int kRowWaves = 8, kRowAhead = 4;
@@ -135,13 +135,14 @@ static hipError_t start_rows(const TileArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// How many weight rows a workgroup takes and how many workgroups share them, by the outputs and inputs alone.  The time is
-// the most loaded CU's: whole workgroups per CU times their rows (and the activations beside them, as 6 rows' worth); what its
-// waves have in flight at once costs one latency, about 2 us, the rest comes at about 17 KB per microsecond.  A shared
-// reduction adds a launch, 2.5 us, and the traffic of its sums (16 tokens').  Measured, 16 tokens: 8192 inputs and outputs
-// 40.0 us with one fragment, 34.7 with two; 8192 inputs, 2048 outputs 19.8 us alone, 14.6 shared by four; 4096 inputs, 1024
-// outputs 11.1 us, 8.0 by four.  One token: 2048 inputs, 768 gated outputs 5.6 us, 6.4 by two; 6912 inputs, 2304 gated
-// outputs (288 workgroups for 256 CUs) 24.8 us, 19.2 by eight.
+// How many weight rows a workgroup takes and how many workgroups share them, by the outputs and inputs alone.
+// The time is the most loaded CU's: whole workgroups per CU times their rows (and the activations beside them,
+// as 6 rows' worth); what its waves have in flight at once costs one latency, about 2 us, the rest comes at
+// about 17 KB per microsecond. A shared reduction adds a launch, 2.5 us, and the traffic of its sums (16
+// tokens'). Measured, 16 tokens: 8192 inputs and outputs 40.0 us with one fragment, 34.7 with two; 8192 inputs,
+// 2048 outputs 19.8 us alone, 14.6 shared by four; 4096 inputs, 1024 outputs 11.1 us, 8.0 by four. One token:
+// 2048 inputs, 768 gated outputs 5.6 us, 6.4 by two; 6912 inputs, 2304 gated outputs (288 workgroups for 256
+// CUs) 24.8 us, 19.2 by eight.
 struct RowPlan {
   int frags, splits;
 };

@@ -29,16 +29,18 @@ MOE_DEV int col_mix(int r) {
   return (r >> 3) & 1;
 }
 
-// Element offset in a half tile of the 16-byte chunk `c` of line `m` (kRows: line = output, kCols: line = reduction row).
+// Element offset in a half tile of the 16-byte chunk `c` of line `m` (kRows: line = output, kCols: line =
+// reduction row).
 template <int ORDER, int H>
 MOE_DEV int chunk_pos(int m, int c) {
   if constexpr (ORDER == kRows) return m * kStepR + ((c ^ (m & 7)) << 3);
   return m * H + (((c >> 1) ^ col_mix<H>(m)) << 4) + ((c & 1) << 3);
 }
 
-// A lane's LDS byte address for the fragment of outputs o .. o+15 (o a multiple of 16), reduction elements 0..31, of the half
-// tile at byte address `half`.  Fragments of a wave start at o = FR * 16 * (wave's index), FR a power of two, so fragment
-// n's pair index is o / 16 ^ n and every further address differs by a constant or one exclusive or.
+// A lane's LDS byte address for the fragment of outputs o .. o+15 (o a multiple of 16), reduction elements
+// 0..31, of the half tile at byte address `half`. Fragments of a wave start at o = FR * 16 * (wave's index), FR
+// a power of two, so fragment n's pair index is o / 16 ^ n and every further address differs by a constant or
+// one exclusive or.
 template <int ORDER, int H>
 MOE_DEV uint32_t frag_addr(uint32_t half, int o, int lane) {
   if constexpr (ORDER == kRows) return half + 2 * chunk_pos<kRows, H>(o + (lane & 15), lane >> 4);
@@ -93,11 +95,11 @@ MOE_DEV TileIndex tile_index(const TileArgs& a, uint32_t id, uint32_t count) {
 }
 
 // ---- epilogue -------------------------------------------------------------------------------------
-// A wave's FI x FJ fragments of outputs (i0.., j0..): lane l holds rows f 16 + l % 16, columns g 16 + 4 (l / 16) ..+3.  They pass
-// through the wave's own LDS (16-byte chunks swizzled by row) so that a lane stores 8 consecutive elements.  Plain results are
-// rounded to 16 bits first, half the LDS bytes (4096 x 4096 outputs of 512 terms 27.2 -> 23.5 us, 8192 x 8192 of 2048 251 -> 244 us);
-// with a bias, activation or residual the fp32 sums pass, in a loop, so that the code of an activation exists once per
-// kernel and no registers spill.
+// A wave's FI x FJ fragments of outputs (i0.., j0..): lane l holds rows f 16 + l % 16, columns g 16 + 4 (l /
+// 16) ..+3. They pass through the wave's own LDS (16-byte chunks swizzled by row) so that a lane stores 8
+// consecutive elements. Plain results are rounded to 16 bits first, half the LDS bytes (4096 x 4096 outputs of
+// 512 terms 27.2 -> 23.5 us, 8192 x 8192 of 2048 251 -> 244 us); with a bias, activation or residual the fp32
+// sums pass, in a loop, so that the code of an activation exists once per kernel and no registers spill.
 template <typename T, int KIND, int FI, int FJ>
 MOE_DEV void finish_fragments(const TileArgs& a, const TileIndex& x, int64_t i0, int64_t j0, const float4v (&s0)[FI][FJ],
                               const float4v (&s1)[FI][FJ], float* lds, int lane) {
@@ -206,8 +208,8 @@ MOE_DEV void gate_block(const float4v (&g)[FI][FJ], const float4v (&u)[FI][FJ], 
     }
 }
 
-// All of a wave's sums: NI x 2 blocks, block (h, hj) at rows i0 + h di, columns j0 + hj dj (gated: hj = 0 the gate's, 1 the
-// up's sums of the same outputs).
+// All of a wave's sums: NI x 2 blocks, block (h, hj) at rows i0 + h di, columns j0 + hj dj (gated: hj = 0 the
+// gate's, 1 the up's sums of the same outputs).
 template <typename T, int KIND, int NI, int FI, int FJ>
 MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, int64_t di, int64_t j0, int64_t dj,
                            const float4v (&s)[NI][2][FI][FJ], float* lds, int lane) {
@@ -268,9 +270,10 @@ MOE_DEV u32x4 load8_any(const uint16_t* base, int64_t ld, int64_t line, int64_t 
   return v;
 }
 
-// One operand's 16-byte chunks of a step, COUNT per thread, loaded at any alignment.  A step that is not the matrix's last is
-// loaded without checks: lines past the outputs repeat the last one, chunks past them (kCols) the first, and a chunk that
-// straddles the end of a kCols line runs into the next line, which exists; all of that reaches only sums that are not stored.
+// One operand's 16-byte chunks of a step, COUNT per thread, loaded at any alignment. A step that is not the
+// matrix's last is loaded without checks: lines past the outputs repeat the last one, chunks past them (kCols)
+// the first, and a chunk that straddles the end of a kCols line runs into the next line, which exists; all of
+// that reaches only sums that are not stored.
 template <int ORDER, int H, int COUNT>
 struct AnyLoad {
   const uint16_t* p[COUNT];
@@ -328,8 +331,10 @@ struct AnyLoad {
   }
 };
 
-// (64 F) x (64 F) tile, 4 waves of (32 F) x (32 F); operands pass through registers, two steps ahead, into two LDS
-// buffers, so that any address, stride and length works.
+// (64 F) x (64 F) tile, 4 waves of (32 F) x (32 F); operands pass through registers, two steps ahead, into two
+// LDS buffers, so that any address, stride and length works. Bound by the latency and rate of unaligned loads:
+// 0.9 us a step with 64-square tiles, 1.5 with 128 (4096 x 4095 outputs of 4095 terms 257 us; through copies
+// with whole rows 171 us).
 template <typename T, int OA, int OB, int KIND, int F>
 __global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
   constexpr int H = 32 * F, kBuf = 4 * H * kStepR;  // elements: A0 A1 B0 B1
@@ -448,7 +453,8 @@ MOE_DEV void copies_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
-// Copies of one operand: WAVES waves, half tiles of H outputs; each wave issues kCopies copies per half tile and step.
+// Copies of one operand: WAVES waves, half tiles of H outputs; each wave issues kCopies copies per half tile
+// and step.
 template <int ORDER, int H, int WAVES>
 struct OperandCopy {
   static constexpr int kCopies = H / 8 / WAVES;  // H * 128 bytes in 1-KiB copies
@@ -469,9 +475,9 @@ struct OperandCopy {
   }
 };
 
-// The steps of one half tile, in order: a running address and the steps left, so that issuing a step costs few scalar
-// instructions (a wave issues one instruction per four to five cycles: at ~40 per copy the 64 x 64 tile took 0.35 us a
-// step, whatever was in flight).  SEGS: a second matrix of the same stride follows the first.
+// The steps of one half tile, in order: a running address and the steps left, so that issuing a step costs few
+// scalar instructions (a wave issues one instruction per four to five cycles: at ~40 per copy the 64 x 64 tile
+// took 0.35 us a step, whatever was in flight). SEGS: a second matrix of the same stride follows the first.
 template <int ORDER, int H, int WAVES, bool SEGS>
 struct HalfStream {
   typedef OperandCopy<ORDER, H, WAVES> Copy;
@@ -482,8 +488,9 @@ struct HalfStream {
   int32_t left, left1;  // steps left in this matrix, the one to be issued included; in the second one
   int32_t end, end1;    // left's value after a matrix's last step if that is partial and this workgroup's, else one it never takes
 
-  // first: the half tile's first element; outs: its outputs that exist; R: reduction length (kRows: readable elements of a
-  // line); the workgroup takes steps begin .. begin + count - 1 of the one or two matrices of `steps` steps each.
+  // first: the half tile's first element; outs: its outputs that exist; R: reduction length (kRows: readable
+  // elements of a line); the workgroup takes steps begin .. begin + count - 1 of the one or two matrices of
+  // `steps` steps each.
   MOE_DEV void init(const void* m0, const void* m1, int64_t ld, int64_t o0, int O, int R, int steps, int begin, int count) {
     const int64_t first = 2 * (ORDER == kRows ? o0 * ld : o0);
     stride = ORDER == kRows ? 2 * kStepR : 2 * kStepR * (uint64_t)ld;
@@ -510,8 +517,8 @@ struct HalfStream {
     end = end1;
     left1 = 0;
   }
-  // Issues this wave's copies of the next step.  With no steps left the same number of copies is issued, all past the
-  // resource's end: nothing is read, zeros are written.
+  // Issues this wave's copies of the next step. With no steps left the same number of copies is issued, all
+  // past the resource's end: nothing is read, zeros are written.
   MOE_DEV void issue(Copy& c, uint32_t lds_addr) {
     u32x4 rsrc;
     rsrc[0] = (uint32_t)p;
@@ -523,7 +530,8 @@ struct HalfStream {
     const bool tail = left == end;
     if (__builtin_expect(tail, 0)) {
       rsrc[2] = bytes - cut;
-      // a kRows line continues past the reduction's end (its next line, or what lies between): those chunks are not read
+      // a kRows line continues past the reduction's end (its next line, or what lies between): those chunks are
+      // not read
       if (ORDER == kRows && c.chunk * 8 >= kStepR - cut / 2)
 #pragma unroll
         for (int d = 0; d < Copy::kCopies; ++d) c.voff[d] |= 0x80000000u;
@@ -539,9 +547,11 @@ struct HalfStream {
   }
 };
 
-// 64 x 64 tile (gated: 64 x 32 outputs), 4 waves of 32 x 2 x 16, for products with too few large tiles to fill the chip: there
-// a step's arithmetic is short and the time is the copies' latency, so five LDS buffers of one step (64 reduction elements,
-// 16 KB) keep four steps in flight.  While a step's MFMAs run from registers the next step's fragments are read.
+// 64 x 64 tile (gated: 64 x 32 outputs), 4 waves of 32 x 2 x 16, for products with too few large tiles to fill
+// the chip: there a step's arithmetic is short and the time is the copies' latency, so five LDS buffers of one
+// step (64 reduction elements, 16 KB) keep four steps in flight (two workgroups of them fill a CU's LDS; eight
+// buffers were no faster): 0.36 us a step alone on a CU, 0.52 for two; 300 x 1000 outputs of 1000 terms 9.5 us,
+// 128-square tiles 15 us. While a step's MFMAs run from registers the next step's fragments are read.
 constexpr int kDeepStages = 5, kDeepStageBytes = (64 + 2 * 32) * kStepR * 2;
 template <typename T, int OA, int OB, int KIND>
 MOE_DEV void deep_tile(const TileArgs& a, uint32_t id, uint32_t ids, uint16_t* lds) {
@@ -640,8 +650,9 @@ __global__ __launch_bounds__(256, 2) void k_tile_deep(TileArgs a) {
   deep_tile<T, OA, OB, KIND>(a, blockIdx.x, gridDim.x, lds);
 }
 
-// A small backward pass in one launch: dx's tiles, dW's tiles, then the bias gradients' columns.  Alone each of the two
-// products leaves CUs idle, and a launch costs two to three microseconds (333 tokens, 1000 x 1357: 27.8 us as separate launches).
+// A small backward pass in one launch: dx's tiles, dW's tiles, then the bias gradients' columns. Alone each of
+// the two products leaves CUs idle, and a launch costs two to three microseconds (333 tokens, 1000 x 1357: 27.8
+// us as separate launches).
 template <typename T>
 __global__ __launch_bounds__(256, 2) void k_backward_small(TileArgs dx, TileArgs dw, BiasSumArgs db, uint32_t n_dx, uint32_t n_dw) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[kDeepStages * kDeepStageBytes / 2];
@@ -660,9 +671,10 @@ __global__ __launch_bounds__(256, 2) void k_backward_small(TileArgs dx, TileArgs
 
 // (2 WI FI 16) x (2 WJ FJ 16) tile, WI x WJ waves; a wave's quarter in (i half, j half) is FI x FJ fragments.
 //
-// Two LDS buffers of one step (64 reduction elements) each.  A step is four phases, one per quarter, in the order
-// (A0,B0) (A0,B1) (A1,B1) (A1,B0); while a phase's MFMAs run from registers, the wave reads the fragments that the
-// next phase adds and issues copies of a later step's half tile into the LDS region that was read out last:
+// Two LDS buffers of one step (64 reduction elements) each. A step is four phases, one per quarter, in the
+// order (A0,B0) (A0,B1) (A1,B1) (A1,B0); while a phase's MFMAs run from registers, the wave reads the fragments
+// that the next phase adds and issues copies of a later step's half tile into the LDS region that was read out
+// last:
 //     phase        MFMA    reads to registers     copies
 //     1 of step k  A0 B0   B1 of k                B0 of k+2
 //     2            A0 B1   A1 of k                B1 of k+2
@@ -670,6 +682,12 @@ __global__ __launch_bounds__(256, 2) void k_backward_small(TileArgs dx, TileArgs
 //     4            A1 B0   B0 of k+1 (over B1)    A0 of k+3
 // A half tile is thus read six to seven phases after its copies were issued, with one barrier per phase that
 // waits only for the copies older than the last six half tiles.
+//
+// Bound by the feed from the L2 (64 KB a step and CU in 256-square tiles; half the barriers or deeper reads
+// ahead changed nothing): 1.47 us a step, matrix cores busy 60 % of the cycles, and about 10 us per round of
+// tiles for the first copies and the stores. 8192^3 bf16: forward 808-910 us (1,210-1,360 TFLOP/s), dx 824, dW
+// 810 us. 128-square tiles, two workgroups per CU, where 256-square ones would leave CUs idle: 4096 x 2048
+// outputs of 8192 terms 134 against 181 us.
 template <typename T, int OA, int OB, int KIND, int WI, int WJ, int FI, int FJ>
 __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   constexpr int W = WI * WJ, HI = WI * FI * 16, HJ = WJ * FJ * 16;
@@ -798,17 +816,18 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
                          (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * FI * FJ * 256, lane);
 }
 
-// A line's chunks lie on 16-byte addresses.  kRows: and end with the reduction (or with zeros past it: len counts them).  kCols:
-// a last chunk that is partly past the outputs only reaches sums that are not stored.
+// A line's chunks lie on 16-byte addresses. kRows: and end with the reduction (or with zeros past it: len
+// counts them). kCols: a last chunk that is partly past the outputs only reaches sums that are not stored.
 inline bool whole_chunks(int order, const void* p, int64_t ld, int64_t len) {
   return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && (order == kCols || len % 8 == 0);
 }
 
-// The plan with the least estimated time, in microseconds.  Measured at bf16 and 64 reduction elements per step: a CU draws
-// 45 to 50 KB per microsecond from the L2 whatever is in flight, so a step of a lone workgroup on its CU takes 0.36 us
-// with a 64 x 64 tile (16 KB), 0.63 us with 128 x 128, 1.5 us with 256 x 256; two workgroups side by side (which the two
-// smaller tiles allow) take 0.52 and 0.92 us for a step of each.  Per round of tiles the prologue and epilogue add
-// 1, 2 and 5 us; a split reduction adds a launch and the traffic of its fp32 sums.
+// The plan with the least estimated time, in microseconds. Measured at bf16 and 64 reduction elements per step:
+// a CU draws 45 to 50 KB per microsecond from the L2 whatever is in flight, so a step of a lone workgroup on
+// its CU takes 0.36 us with a 64 x 64 tile (16 KB), 0.63 us with 128 x 128, 1.5 us with 256 x 256; two
+// workgroups side by side (which the two smaller tiles allow) take 0.52 and 0.92 us for a step of each. Per
+// round of tiles the prologue and epilogue add 1, 2 and 5 us; a split reduction adds a launch and the traffic
+// of its fp32 sums.
 struct TileCost {
   int kernel, tile;
   double lone, pair, round;
@@ -883,9 +902,9 @@ hipError_t start_plan(TileArgs a, int kernel, hipStream_t st) {
   }
 }
 
-// Gives the operands that lack them whole 16-byte chunks, by copies in the workspace, when that pays: the copy costs a launch
-// and the operand's bytes twice, the other kernels run at about half the rate (4096 x 4096 tokens and outputs of 4095
-// inputs: 258 us without copies).
+// Gives the operands that lack them whole 16-byte chunks, by copies in the workspace, when that pays: the copy
+// costs a launch and the operand's bytes twice, the other kernels run at about half the rate (4096 x 4096
+// tokens and outputs of 4095 inputs: 258 us without copies).
 template <int OA, int OB, int KIND>
 bool pack_operands(TileArgs& a, bool whole_a, const bool (&whole_b)[2], hipStream_t st, hipError_t* err) {
   const int na = a.nseg > 1 || a.nbatch > 1 ? 2 : 1, nb = KIND == kEpiGated || a.nseg > 1 ? 2 : 1;
