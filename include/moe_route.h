@@ -515,9 +515,10 @@ typedef struct moe_dense_dims {
  * for up to `max_tokens` tokens; 0 if dims are invalid or max_tokens out of range. */
 MOE_API size_t moe_dense_workspace_bytes(const moe_dense_dims* dims, int32_t max_tokens, int32_t backward);
 
-/* Tuning aid: every dense product of the process runs this tile kernel (MOE_DENSE_AUTO: chosen by size, the default; the
- * MOE_DENSE_TILE ones only where the rows are whole 16-byte chunks), and every dense call this many splits of its reductions (1..8, as far as the workspace holds their sums; 0:
- * chosen by size).  Process-wide, not for concurrent use from several threads. */
+/* Tuning aid: every dense product of the process runs this tile kernel (MOE_DENSE_AUTO: chosen by size, the
+ * default; the MOE_DENSE_TILE ones only where the rows are whole 16-byte chunks), and every dense call this many
+ * splits of its reductions (1..8, as far as the workspace holds their sums; 0: chosen by size).  Process-wide,
+ * not for concurrent use from several threads. */
 enum moe_dense_kernel { MOE_DENSE_AUTO = 0, MOE_DENSE_TILE64 = 1, MOE_DENSE_TILE128 = 2, MOE_DENSE_TILE256 = 3,
                         MOE_DENSE_ANY64 = 4, MOE_DENSE_ANY128 = 5 };
 MOE_API int moe_debug_force_dense_plan(int32_t kernel, int32_t splits);

@@ -65,12 +65,14 @@ MOE_DEV void act_values(int act, float (&v)[8]) {
 #undef MOE_ACT_CASE
 }
 
-// s = sigmoid(z) and c = 1 - s without cancellation (e s, with e = exp(-z) kept finite; NaN passes).
+// s = sigmoid(z) and c = 1 - s without cancellation: e s, with e = exp(-z); 1 where e is too large for its
+// reciprocal to be a normal number (s is 0 there, so a product with s is exactly the derivative's limit, however
+// large z is).  NaN passes.
 MOE_DEV void fast_sigmoid_pair(float z, float& s, float& c) {
-  float e = __builtin_amdgcn_exp2f(z * -1.44269504088896341f);
-  e = e > 1e37f ? 1e37f : e;
-  s = __builtin_amdgcn_rcpf(1.0f + e);
-  c = e * s;
+  const float e = __builtin_amdgcn_exp2f(z * -1.44269504088896341f);
+  const bool large = e > 1e37f;
+  s = large ? 0.0f : __builtin_amdgcn_rcpf(1.0f + e);
+  c = large ? 1.0f : e * s;
 }
 
 // Value and derivative together (the gated block's backward pass needs both).
@@ -80,7 +82,7 @@ MOE_DEV void act_both(int act, float z, float& v, float& d) {
       float s, c;
       fast_sigmoid_pair(z, s, c);
       v = z * s;
-      d = s * (1.0f + z * c);
+      d = s + z * (s * c);
       break;
     }
     case MOE_ACT_GELU: {
@@ -93,7 +95,8 @@ MOE_DEV void act_both(int act, float z, float& v, float& d) {
       float s, c;
       fast_sigmoid_pair(2.0f * kGeluC * z * (1.0f + kGeluK * z * z), s, c);
       v = z * s;
-      d = s + z * s * c * (2.0f * kGeluC * (1.0f + 3.0f * kGeluK * z * z));
+      const float q = z * (s * c);  // before the powers of z: 0 times them where they overflow fp32
+      d = s + 2.0f * kGeluC * (q + 3.0f * kGeluK * (z * (z * q)));
       break;
     }
     case MOE_ACT_RELU:
@@ -126,9 +129,9 @@ struct DenseEpi {
   int64_t ldp[2];
   int32_t y_f32;       // linear: y and res are fp32
   int32_t act;
-  int32_t stream;      // outputs larger than the L2s: stored with the non-temporal hint (launch_tile), so that they leave
-                       // the operands in the caches (4096 tokens and outputs: 512 inputs 28.6 -> 24.9 us, 4096
-                       // inputs 110.8 -> 106.3 us)
+  int32_t stream;      // outputs larger than the L2s: stored with the non-temporal hint (launch_tile), so that
+                       // they leave the operands in the caches (4096 tokens and outputs: 512 inputs 28.6 ->
+                       // 24.9 us, 4096 inputs 110.8 -> 106.3 us)
 };
 
 // 8 consecutive elements of a row as fp32, or the first n of them. Global accesses of 16 bytes need only the

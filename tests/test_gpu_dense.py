@@ -207,6 +207,32 @@ def test_slices_of_wider_rows(N, pad, offset, shape):
     run_gated_backward(N, gen, *shape, BF16, 4, pad=pad, offset=offset)
 
 
+@pytest.mark.parametrize("step", [8, 3])
+@pytest.mark.parametrize("shape", [(5, 128, 64), (90, 200, 136), (300, 520, 264)], ids=str)
+def test_every_matrix_its_own_stride(N, shape, step):
+    """The gated block with a different row stride for every operand and output, whole 16-byte rows or odd."""
+    T, K, M = shape
+    gen = gen_for(21, T, step)
+    pads = iter(range(step, 20 * step, step))
+    x = rnd(gen, (T, K), BF16, pad=next(pads))
+    wg, wu = (rnd(gen, (M, K), BF16, K ** -0.5, pad=next(pads)) for _ in range(2))
+    dh = rnd(gen, (T, M), BF16, pad=next(pads))
+    h, g, u = (Out((T, M), BF16, next(pads)) for _ in range(3))
+    dx, dwg, dwu = Out((T, K), BF16, next(pads)), Out((M, K), BF16, next(pads)), Out((M, K), BF16, next(pads))
+    d = N.dense_dims(K, M, N.MOE_BF16, N.MOE_ACT_SILU)
+    ws, whole = workspace(N, d, T, True)
+    N.moe_gated_forward(d, x, T, wg, wu, h.t, ws, gate=g.t, up=u.t)
+    N.moe_gated_backward(d, x, T, wg, wu, g.t, u.t, dh, ws, dx=dx.t, dw_gate=dwg.t, dw_up=dwu.t)
+    torch.cuda.synchronize()
+    ref = R.gated_forward(N.MOE_ACT_SILU, x, wg, wu, None, None)
+    for k, o in (("h", h), ("gate", g), ("up", u)):
+        R.check(k, o.t, ref[k])
+    ref = R.gated_backward(N.MOE_ACT_SILU, x, wg, wu, g.t, u.t, dh)
+    for k, o in (("dx", dx), ("dw0", dwg), ("dw1", dwu)):
+        R.check(k, o.t, ref[k])
+    assert all(o.untouched() for o in (h, g, u, dx, dwg, dwu)) and guard_ok(whole)
+
+
 @pytest.mark.parametrize("want", [("dx",), ("dw",), ("db",), ("dx", "db"), ("dw", "db")], ids="-".join)
 def test_linear_backward_wanted_outputs(N, want):
     for a in (0, 1):
@@ -327,6 +353,36 @@ def test_infinities_and_nans_stay_in_their_rows(N, T):
     y = torch.empty(T, 8, dtype=F16, device="cuda")
     N.moe_linear_forward(d, x, T, w, y, ws)
     assert torch.isinf(y[0]).all() and (y[1] == 65504).all() and (y[2:] == 0).all()
+
+
+@pytest.mark.parametrize("a", ACTS)
+def test_saved_values_far_out_give_the_derivatives_limits(N, a):
+    """Pre-activations up to bf16's largest: the derivative is its limit there, 0 or 1 (dx of an identity weight
+    is dz itself), and the gated block's factors are the activation's limits.  Beyond |z| = 128 every derivative
+    here differs from its limit by less than exp(-128) 129 < 2^-170, so the results are exact, up to sums of
+    such remainders (below 2^-100, which the rounding to bf16 may keep)."""
+    z = torch.tensor([128.0, 1e3, 1e6, 1e12, 1e15, 1e20, 1e30, 3e38], device="cuda").to(BF16)
+    z = torch.cat([z, -z])
+    M = z.numel()
+    eye = torch.eye(M, device="cuda").to(BF16)
+    x = torch.ones(M, M, dtype=BF16, device="cuda")
+    d = N.dense_dims(M, M, N.MOE_BF16, a)
+    ws, _ = workspace(N, d, M, True)
+    dx, dbg, dbu = torch.empty_like(x), torch.empty_like(z), torch.empty_like(z)
+    pre = z.repeat(M, 1)
+    slope = {0: (1, 1), 5: (0, 0)}.get(a, (1, 0))
+    want = torch.tensor(slope, device="cuda").repeat_interleave(M // 2).double().expand(M, M)
+    N.moe_linear_backward(d, x, M, eye, x, ws, pre=pre, dx=dx)
+    assert ((dx.double() - want).abs() < 2.0 ** -100).all()
+    N.moe_gated_backward(d, x, M, eye, torch.zeros_like(eye), pre, x, x, ws, dx=dx, dgate_bias=dbg)
+    assert ((dx.double() - want).abs() < 2.0 ** -100).all()
+    assert ((dbg.double() - M * want[0]).abs() < 2.0 ** -100).all()
+    # du = dh act(z): z, 1 or 0; a row's 1 / M of it, so that the sum over M equal rows stays in range
+    N.moe_gated_backward(d, x, M, eye, eye, pre, x, x / M, ws, dup_bias=dbu)
+    value = torch.where(z > 0, z.double(), {0: z.double()}.get(a, torch.zeros_like(z).double()))
+    if a == 5:
+        value = (z > 0).double()
+    assert ((dbu.double() - value).abs() <= 2.0 ** -8 * value.abs() + 2.0 ** -100).all()
 
 
 @pytest.mark.parametrize("T", [3, 100])
