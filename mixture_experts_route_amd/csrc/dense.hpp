@@ -222,8 +222,8 @@ MOE_DEV void finish8(const DenseEpi& e, int batch, int64_t i, int j, int n, floa
 //   dW          A = dz  kCols, B = x   kCols   (gated: two batches, dg and du)
 enum OperandOrder { kRows = 0, kCols = 1 };
 // Where workgroups share a tile's reduction they leave their fp32 sums in the workspace, and a second launch
-// adds them in split order and applies the epilogue: [split][mat][i][part_ld], mat = the batch (gated: gate,
-// up).
+// adds them in split order and applies the epilogue: [split][mat][i - head_rows][part_ld], mat = the batch
+// (gated: gate, up).
 constexpr size_t kDensePartBytes = 32u << 20;
 constexpr int kMaxSplits = 8;
 
@@ -235,7 +235,8 @@ struct TileArgs {
   int32_t len_a, len_b;    // readable elements of A's and B's rows (kRows): R, or more where what follows is zeros
   int32_t nseg, nbatch;    // 1 or 2 each
   int32_t tiles_i, tiles_j;
-  int32_t splits;          // workgroups sharing a tile's reduction
+  int32_t splits;          // workgroups sharing a tile's reduction, in rows of tiles from `head` on
+  int32_t head, head_rows; // rows of tiles before them, each tile by one workgroup; their outputs' rows
   float* part;
   size_t part_bytes;
   uint16_t *pack_a, *pack_b[2];  // workspace for copies of the operands with whole 16-byte rows (NULL: none)
@@ -243,7 +244,7 @@ struct TileArgs {
 };
 // moe_debug_force_dense_plan: the tile kernel (MOE_DENSE_AUTO: chosen by size) and the splits (0: chosen by size).
 struct DensePlan {
-  int kernel, splits;
+  int kernel, splits, head;
 };
 extern DensePlan g_dense_plan;
 
@@ -252,7 +253,7 @@ inline size_t split_bytes(int splits, int mats, int64_t M, int64_t N) {
 }
 MOE_DEV float* part_at(const TileArgs& a, int split, int mats, int mat, int64_t i, int j) {
   const int64_t ld = (a.N + 7) / 8 * 8;
-  return a.part + (((int64_t)split * mats + mat) * a.M + i) * ld + j;
+  return a.part + (((int64_t)split * mats + mat) * (a.M - a.head_rows) + i - a.head_rows) * ld + j;
 }
 
 // finish8, or for a split reduction the sums parked for the second launch.

@@ -4,7 +4,7 @@
 
 namespace moe {
 
-DensePlan g_dense_plan = {MOE_DENSE_AUTO, 0};
+DensePlan g_dense_plan = {MOE_DENSE_AUTO, 0, 0};
 
 // Workspace: control words, the sums of split reductions, then for a backward pass dz (gated: dg, du) in the
 // operands' type with rows padded to whole 16-byte chunks, and the bias gradients' partial sums.
@@ -168,7 +168,7 @@ MOE_API size_t moe_dense_workspace_bytes(const moe_dense_dims* dims, int32_t max
 
 MOE_API int moe_debug_force_dense_plan(int32_t kernel, int32_t splits) {
   if (kernel < MOE_DENSE_AUTO || kernel > MOE_DENSE_ANY128 || splits < 0 || splits > kMaxSplits) return MOE_EINVAL;
-  g_dense_plan = {kernel, splits};
+  g_dense_plan = {kernel, splits, 0};
   return MOE_OK;
 }
 

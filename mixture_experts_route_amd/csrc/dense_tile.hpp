@@ -70,15 +70,23 @@ MOE_DEV typename Operand<T>::v8 read_frag(uint32_t addr, int n, int kk, int offs
 // Tile of this workgroup.  Consecutive workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of
 // tiles, walked in groups of 8 tiles along i per column of tiles, so that its L2 keeps a group's A rows.
 struct TileIndex {
-  int batch, ti, tj, split;
+  int batch, ti, tj, split, splits;
 };
+// HEAD: the rows of tiles before a.head and those from there on are numbered each by themselves (else a.head = 0).
+template <bool HEAD>
 MOE_DEV TileIndex tile_index(const TileArgs& a, uint32_t id, uint32_t count) {
+  const uint32_t n_head = HEAD ? (uint32_t)a.head * a.tiles_j : 0;
+  const bool tail = !HEAD || id >= n_head;
+  if (HEAD) {
+    if (tail) id -= n_head;
+    count = tail ? count - n_head : n_head;
+  }
   const uint32_t q = count / 8, rem = count % 8, xcd = id % 8;
   uint32_t t = xcd * q + (xcd < rem ? xcd : rem) + id / 8;
-  TileIndex x = {0, 0, 0, 0};
-  if (a.splits > 1) {
-    x.split = (int)(t % a.splits);
-    t /= a.splits;
+  TileIndex x = {0, 0, 0, 0, tail ? a.splits : 1};
+  if (x.splits > 1) {
+    x.split = (int)(t % x.splits);
+    t /= x.splits;
   }
   const uint32_t per_batch = (uint32_t)a.tiles_i * a.tiles_j;
   if (a.nbatch > 1 && t >= per_batch) {
@@ -87,10 +95,10 @@ MOE_DEV TileIndex tile_index(const TileArgs& a, uint32_t id, uint32_t count) {
   }
   const uint32_t in_full = 8u * a.tiles_j;
   const uint32_t group = t / in_full, in_group = t - group * in_full;
-  const uint32_t left = a.tiles_i - group * 8;
+  const uint32_t left = (!HEAD ? a.tiles_i : tail ? a.tiles_i - a.head : a.head) - group * 8;
   const uint32_t rows = left < 8 ? left : 8;
   x.tj = (int)(rows == 8 ? in_group >> 3 : in_group / rows);
-  x.ti = (int)(group * 8 + in_group - x.tj * rows);
+  x.ti = (int)(group * 8 + in_group - x.tj * rows) + (HEAD && tail ? a.head : 0);
   return x;
 }
 
@@ -216,7 +224,7 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
   const DenseEpi& e = a.epi;
   constexpr bool kGated = KIND == kEpiGated;
   if constexpr (kGated) {
-    if (a.splits == 1 && !e.bias[0] && !e.bias[1] && !e.pre[0]) {
+    if (x.splits == 1 && !e.bias[0] && !e.bias[1] && !e.pre[0]) {
 #pragma unroll
       for (int h = 0; h < NI; ++h) {
         float4v v[FI][FJ];
@@ -239,9 +247,9 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
 #pragma unroll
     for (int hj = 0; hj < 2; ++hj) {
       const int64_t i = i0 + h * di, j = j0 + (kGated ? 0 : hj * dj);
-      if (a.splits > 1) {  // parked for the second launch; rows padded to 8 floats, so a last fragment's spare columns have room
-        const int mat = kGated ? hj : x.batch, mats = kGated ? 2 : a.nbatch;
-        store_block_f32<FI, FJ>(part_at(a, x.split, mats, mat, 0, 0), (a.N + 7) / 8 * 8, i, j, a.M, (a.N + 7) / 8 * 8, s[h][hj], lane);
+      if (x.splits > 1) {  // parked for the second launch; rows padded to 8 floats, with room for spare columns
+        const int mat = kGated ? hj : x.batch, mats = kGated ? 2 : a.nbatch, ld = (a.N + 7) / 8 * 8;
+        store_block_f32<FI, FJ>(part_at(a, x.split, mats, mat, 0, 0), ld, i, j, a.M, ld, s[h][hj], lane);
       } else if (!kGated && plain) {
         store_block<T, FI, FJ>(x.batch ? e.y[1] : e.y[0], x.batch ? e.ldy[1] : e.ldy[0], i, j, a.M, a.N, e.stream, s[h][hj],
                                (uint16_t*)lds, lane);
@@ -341,12 +349,12 @@ __global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[2 * kBuf];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wi = wave >> 1, wj = wave & 1;
-  const TileIndex x = tile_index(a, blockIdx.x, gridDim.x);
+  const TileIndex x = tile_index<false>(a, blockIdx.x, gridDim.x);
   constexpr int JT = KIND == kEpiGated ? H : 2 * H;  // output columns per tile
   const int64_t i0 = (int64_t)x.ti * 2 * H, j0 = (int64_t)x.tj * JT;
   const int steps = (a.R + kStepR - 1) / kStepR;
-  const int s_begin = (int)((int64_t)steps * a.nseg * x.split / a.splits);
-  const int s_end = (int)((int64_t)steps * a.nseg * (x.split + 1) / a.splits);
+  const int s_begin = (int)((int64_t)steps * a.nseg * x.split / x.splits);
+  const int s_end = (int)((int64_t)steps * a.nseg * (x.split + 1) / x.splits);
   constexpr bool kSegs = OA == kRows && OB == kCols, kBatches = OA == kCols;
 
   AnyLoad<OA, H, F> la[2];
@@ -563,13 +571,13 @@ MOE_DEV void deep_tile(const TileArgs& a, uint32_t id, uint32_t ids, uint16_t* l
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave >> 1, wj = wave & 1;
-  const TileIndex x = tile_index(a, id, ids);
+  const TileIndex x = tile_index<false>(a, id, ids);
   constexpr int JT = KIND == kEpiGated ? HJ : 2 * HJ;
   const int64_t i0 = (int64_t)x.ti * HI, j0 = (int64_t)x.tj * JT;
 
   const int steps = (a.R + kStepR - 1) / kStepR, total = steps * a.nseg;
-  const int s_begin = (int)((int64_t)total * x.split / a.splits);
-  const int count = (int)((int64_t)total * (x.split + 1) / a.splits) - s_begin;
+  const int s_begin = (int)((int64_t)total * x.split / x.splits);
+  const int count = (int)((int64_t)total * (x.split + 1) / x.splits) - s_begin;
 
   constexpr bool kSegs = OA == kRows && OB == kCols, kBatches = OA == kCols;
   OperandCopy<OA, HI, W> ca;
@@ -699,13 +707,13 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave / WJ, wj = wave % WJ;
-  const TileIndex x = tile_index(a, blockIdx.x, gridDim.x);
+  const TileIndex x = tile_index<true>(a, blockIdx.x, gridDim.x);
   constexpr int JT = KIND == kEpiGated ? HJ : 2 * HJ;
   const int64_t i0 = (int64_t)x.ti * 2 * HI, j0 = (int64_t)x.tj * JT;
 
   const int steps = (a.R + kStepR - 1) / kStepR, total = steps * a.nseg;
-  const int s_begin = (int)((int64_t)total * x.split / a.splits);
-  const int count = (int)((int64_t)total * (x.split + 1) / a.splits) - s_begin;
+  const int s_begin = (int)((int64_t)total * x.split / x.splits);
+  const int count = (int)((int64_t)total * (x.split + 1) / x.splits) - s_begin;
 
   constexpr bool kSegs = OA == kRows && OB == kCols, kBatches = OA == kCols;  // which products have them
   OperandCopy<OA, HI, W> ca;
@@ -827,7 +835,9 @@ inline bool whole_chunks(int order, const void* p, int64_t ld, int64_t len) {
 // its CU takes 0.36 us with a 64 x 64 tile (16 KB), 0.63 us with 128 x 128, 1.5 us with 256 x 256; two
 // workgroups side by side (which the two smaller tiles allow) take 0.52 and 0.92 us for a step of each. Per
 // round of tiles the prologue and epilogue add 1, 2 and 5 us; a split reduction adds a launch and the traffic
-// of its fp32 sums.
+// of its fp32 sums. A last round that would leave most CUs idle is filled by splitting its tiles' reductions:
+// 2500 x 4096 outputs of 4096 terms 98.5 -> 89.8 us (640 tiles, two of them at a time on a CU: 512 whole, 128 in
+// two parts), gated 2060 x 4096 outputs of 8192 terms 273 -> 224 us (256-square, 256 whole, 32 in eight).
 struct TileCost {
   int kernel, tile;
   double lone, pair, round;
@@ -841,7 +851,7 @@ template <int OA, int KIND>
 DensePlan plan_tile(const TileArgs& a, bool whole, double* us) {
   const int64_t steps = (int64_t)((a.R + kStepR - 1) / kStepR) * a.nseg;
   const int mats = KIND == kEpiGated ? 2 : a.nbatch;
-  DensePlan best = {0, 1};
+  DensePlan best = {0, 1, 0};
   double& least = *us = 1e300;
   const TileCost* costs = whole ? kWholeCosts : kAnyCosts;
   for (int c = 0; c < (whole ? 3 : 2); ++c) {
@@ -856,7 +866,24 @@ DensePlan plan_tile(const TileArgs& a, bool whole, double* us) {
       if (splits > 1) t += 2.5 + 2.0 * part / 4e6;
       if (t < least) {
         least = t;
-        best = {k.kernel, splits};
+        best = {k.kernel, splits, 0};
+      }
+    }
+    // whole rounds of tiles by single workgroups, the rest's reductions split (measured up to 5 us beyond its
+    // parts)
+    if (!whole || k.kernel == MOE_DENSE_TILE64 || a.nbatch > 1 || g_dense_plan.splits) continue;
+    const int64_t row = ((int64_t)a.N + tj - 1) / tj, slots = k.pair < 2 * k.lone ? 512 : 256;
+    const int64_t rounds = tiles / slots, head = rounds * slots / row, tail = tiles - head * row;
+    if (!head || !tail) continue;
+    for (int splits = 2; splits <= kMaxSplits; ++splits) {
+      const size_t part = split_bytes(splits, mats, a.M - head * ti, a.N);
+      if (part > a.part_bytes || tail * splits > slots || steps / splits < 4) break;
+      const double step = slots == 512 ? k.pair : k.lone, tail_step = tail * splits > 256 ? k.pair : k.lone;
+      const double t = 3.0 + rounds * (step * steps + k.round) + tail_step * ((steps + splits - 1) / splits) + k.round +
+                       7.5 + 2.0 * part / 4e6;
+      if (t < least) {
+        least = t;
+        best = {k.kernel, splits, (int)head};
       }
     }
   }
@@ -868,7 +895,7 @@ template <int TI, int TJ, int THREADS>
 bool set_tiles(TileArgs& a, int64_t* count) {
   a.tiles_i = (a.M + TI - 1) / TI;
   a.tiles_j = (a.N + TJ - 1) / TJ;
-  *count = (int64_t)a.tiles_i * a.tiles_j * a.nbatch * a.splits;
+  *count = ((int64_t)(a.tiles_i - a.head) * a.splits + a.head) * a.tiles_j * a.nbatch;
   return *count <= (int64_t)0xFFFFFFFF / THREADS;
 }
 
@@ -956,13 +983,15 @@ hipError_t prepare_tile(TileArgs& a, DensePlan& plan, double& us, hipStream_t st
   }
   plan = plan_tile<OA, KIND>(a, whole, &us);
   if (g_dense_plan.kernel != MOE_DENSE_AUTO && (whole || g_dense_plan.kernel >= MOE_DENSE_ANY64))
-    plan = {g_dense_plan.kernel, 1};
+    plan = {g_dense_plan.kernel, 1, 0};
   if (g_dense_plan.splits) {
     plan.splits = g_dense_plan.splits;
     while (plan.splits > 1 && split_bytes(plan.splits, KIND == kEpiGated ? 2 : a.nbatch, a.M, a.N) > a.part_bytes)
       --plan.splits;
   }
   a.splits = plan.splits;
+  a.head = plan.head;
+  a.head_rows = plan.head * (plan.kernel == MOE_DENSE_TILE256 ? 256 : 128);
   a.epi.stream = 2.0 * a.M * a.N * a.nbatch >= 16e6;
   return hipSuccess;
 }
@@ -976,7 +1005,7 @@ hipError_t run_tile(const TileArgs& a, const DensePlan& plan, hipStream_t st) {
 template <typename T, int OA, int OB, int KIND>
 hipError_t launch_tile_k(const TileArgs& args, hipStream_t st) {
   TileArgs a = args;
-  DensePlan plan;
+  DensePlan plan{};
   double us;
   const hipError_t e = prepare_tile<OA, OB, KIND>(a, plan, us, st);
   return e != hipSuccess ? e : run_tile<T, OA, OB, KIND>(a, plan, st);

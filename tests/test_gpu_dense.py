@@ -256,6 +256,16 @@ def test_large(N, shape):
     run_gated_backward(N, gen, *shape, F16, 1)
 
 
+# a few more tiles than fill the chip: those of the last rows share their reductions (both large tiles, each product)
+@pytest.mark.parametrize("shape", [(2200, 4104, 4050), (4240, 4104, 4010), (4400, 4104, 2050)], ids=str)
+def test_last_tiles_in_parts(N, shape):
+    gen = gen_for(23, *shape)
+    run_linear_forward(N, gen, *shape, BF16, 2, bias=True, res=True, save=True)
+    run_gated_forward(N, gen, *shape, F16, 1, bias=True, save=True)
+    run_linear_backward(N, gen, *shape, F16, 0)
+    run_gated_backward(N, gen, *shape, BF16, 1)
+
+
 @pytest.mark.parametrize("splits", [1, 2, 3, 8])
 @pytest.mark.parametrize("kernel", [1, 2, 3, 4, 5], ids=["tile64", "tile128", "tile256", "any64", "any128"])
 def test_every_kernel_and_split(N, kernel, splits):
