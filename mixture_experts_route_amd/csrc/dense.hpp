@@ -242,7 +242,8 @@ struct TileArgs {
   uint16_t *pack_a, *pack_b[2];  // workspace for copies of the operands with whole 16-byte rows (NULL: none)
   DenseEpi epi;
 };
-// moe_debug_force_dense_plan: the tile kernel (MOE_DENSE_AUTO: chosen by size) and the splits (0: chosen by size).
+// The tile kernel, its splits and head (TileArgs).  g_dense_plan is moe_debug_force_dense_plan's: MOE_DENSE_AUTO and
+// 0 splits: chosen by size.
 struct DensePlan {
   int kernel, splits, head;
 };
