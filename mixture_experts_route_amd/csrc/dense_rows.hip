@@ -146,11 +146,17 @@ static hipError_t start_rows(const TileArgs& a, hipStream_t st) {
 struct RowPlan {
   int frags, splits;
 };
-static RowPlan plan_rows(int64_t groups, int64_t R, int64_t sums) {
+// The workspace must hold the sums of MOE_DENSE_ROW_TOKENS tokens whatever a call's own are, so that a token is
+// summed in the same order in every batch; fewer tokens' sums, and their room, are that much smaller.
+static bool parts_fit(int splits, int mats, int64_t N) {
+  return splits == 1 || split_bytes(splits, mats, MOE_DENSE_ROW_TOKENS, N) <= kDensePartBytes;
+}
+static RowPlan plan_rows(int64_t groups, int64_t R, int mats, int64_t N) {
   RowPlan best = {1, 1};
   double least = 1e300;
+  const int64_t sums = mats * N;
   for (int f = 1; f <= 2; ++f)
-    for (int s = 1; s <= kMaxSplits && (s == 1 || R / s >= 512); ++s) {
+    for (int s = 1; s <= kMaxSplits && (s == 1 || (R / s >= 512 && parts_fit(s, mats, N))); ++s) {
       const int64_t per_cu = ((groups + f - 1) / f * s + 255) / 256;
       const double late = (double)per_cu / s * (16 * f + 6) * R * 2 - 88e3;
       const double us = 2.0 + (late > 0 ? late / 17e3 : 0.0) + (s > 1 ? 2.5 + 16.0 * sums * s * 8 / 4e6 : 0.0);
@@ -168,11 +174,10 @@ static hipError_t launch_rows_k(const TileArgs& args, hipStream_t st) {
   auto whole_rows = [](const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
   bool whole = a.R % 8 == 0 && whole_rows(a.a[0], a.lda[0]) && whole_rows(a.b[0], a.ldb[0]);
   if (KIND == kEpiGated) whole = whole && whole_rows(a.b[1], a.ldb[1]);
-  constexpr int outs = KIND == kEpiGated ? 8 : 16;
-  RowPlan plan = plan_rows((a.N + outs - 1) / outs, a.R, (int64_t)a.N * (KIND == kEpiGated ? 2 : 1));
-  if (g_dense_plan.splits) plan.splits = g_dense_plan.splits;
-  a.splits = plan.splits;
-  while (a.splits > 1 && split_bytes(a.splits, KIND == kEpiGated ? 2 : 1, a.M, a.N) > a.part_bytes) --a.splits;
+  constexpr int outs = KIND == kEpiGated ? 8 : 16, mats = KIND == kEpiGated ? 2 : 1;
+  const RowPlan plan = plan_rows((a.N + outs - 1) / outs, a.R, mats, a.N);
+  a.splits = g_dense_plan.splits ? g_dense_plan.splits : plan.splits;
+  while (!parts_fit(a.splits, mats, a.N)) --a.splits;
   hipError_t e;
   if (plan.frags == 1) e = whole ? start_rows<T, KIND, 1, true>(a, st) : start_rows<T, KIND, 1, false>(a, st);
   else e = whole ? start_rows<T, KIND, 2, true>(a, st) : start_rows<T, KIND, 2, false>(a, st);
