@@ -489,6 +489,8 @@ MOE_API int moe_pool_debug_fail_copies(moe_pool* pool, int32_t after_n);
  *     matrix products; the bias gradients sum it unrounded.
  *   - A NaN or an infinity stays in the rows and columns that its definition reaches; nothing between the
  *     rows of a matrix (ld > row length) is used, nor written.
+ *   - A pre-activation past dims->dtype's range is saved as an infinity.  The backward passes take the limits
+ *     there: act' is 0 or 1, act is 0, 1 or infinite; a zero gradient (or act') times an infinite factor is 0.
  *   - Outputs must not overlap inputs or each other, except y on r exactly (same address and
  *     stride).  A NULL output of a backward pass is not computed; at least one must be given.
  *   - `ws` as everywhere: moe_dense_workspace_bytes(dims, n_tokens, backward) bytes, cleared once

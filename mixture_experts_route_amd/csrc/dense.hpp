@@ -1,6 +1,7 @@
 // The dense operators' types, activations, epilogue and launch arguments (moe_linear_*, moe_gated_*).
 #pragma once
 
+#include <float.h>
 #include <math.h>
 
 #include "kernels.hpp"
@@ -115,6 +116,16 @@ MOE_DEV void act_both(int act, float z, float& v, float& d) {
       d = 1.0f;
   }
 }
+
+// The same where z may be infinite (saved in 16 bits, past their range) and a tail's zero would meet it as NaN: taken as
+// fp32's largest number it gives the limits, and the value stays infinite where the activation has no bound. NaN passes.
+MOE_DEV void act_both_far(int act, float z, float& v, float& d) {
+  act_both(act, z < -FLT_MAX ? -FLT_MAX : (z > FLT_MAX ? FLT_MAX : z), v, d);
+  if (fabsf(v) == FLT_MAX) v = z;
+}
+// p times a saved factor f (u, or act(g)) that may be infinite in the same way: a p of zero gives zero, as it does for
+// every value that f may have had. NaN passes.
+MOE_DEV float times_far(float p, float f) { return p == 0.0f && f == f ? p : p * f; }
 
 // ---- epilogues ------------------------------------------------------------------------------------
 enum DenseEpiKind { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2 };

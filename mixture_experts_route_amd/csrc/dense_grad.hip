@@ -22,7 +22,9 @@ MOE_DEV void load8f(const void* base, int64_t off, int e, int N, float v[8]) {
 
 // Memory-bound: reads dy and the saved values once, writes dz once (gated, 8192 x 8192: 671 MB in 117 us, 5.7
 // TB/s). A workgroup takes 512 columns (8 per lane, 16 bytes a load) of a run of rows; its 4 waves take every
-// fourth row and keep the column sums of their rows in registers, added over the waves in LDS in wave order.
+// fourth row and keep the column sums of their rows in registers, added over the waves in LDS in wave order. Infinite saved
+// values show as NaN in dz, and only a chunk with one is computed again with their limits (checks of every element
+// took the pass from 117 to 130 us).
 template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void k_grad_in(GradArgs a) {
   __shared__ float red[3][2][512];
@@ -39,22 +41,45 @@ __global__ __launch_bounds__(256) void k_grad_in(GradArgs a) {
         float g[8], u[8];
         load8f<T>(a.pre0, (int64_t)t * a.ldp0, e, a.N, g);
         load8f<T>(a.pre1, (int64_t)t * a.ldp1, e, a.N, u);
+        bool nan = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float v, d;
           act_both(a.act, g[i], v, d);
-          z0[i] = dy[i] * u[i] * d;
+          z0[i] = dy[i] * d * u[i];
           z1[i] = dy[i] * v;
+          nan |= __builtin_isunordered(z0[i], z1[i]);
+        }
+        if (nan) {  // from memory again, so that no register is held for this
+          load8f<T>(a.dy, (int64_t)t * a.ld_dy, e, a.N, dy);
+          load8f<T>(a.pre0, (int64_t)t * a.ldp0, e, a.N, g);
+          load8f<T>(a.pre1, (int64_t)t * a.ldp1, e, a.N, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float v, d;
+            act_both_far(a.act, g[i], v, d);
+            z0[i] = times_far(dy[i] * d, u[i]);
+            z1[i] = times_far(dy[i], v);
+          }
         }
       } else if (a.act != MOE_ACT_NONE) {
         float g[8];
         load8f<T>(a.pre0, (int64_t)t * a.ldp0, e, a.N, g);
+        bool nan = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float v, d;
           act_both(a.act, g[i], v, d);
           z0[i] = dy[i] * d;
+          nan |= z0[i] != z0[i];
         }
+        if (nan)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float v, d;
+            act_both_far(a.act, g[i], v, d);
+            z0[i] = dy[i] * d;
+          }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z0[i] = dy[i];

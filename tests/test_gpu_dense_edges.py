@@ -1,9 +1,12 @@
 """The dense operators' rules at their edges."""
 
+import math
+
 import pytest
 import torch
 
-from test_gpu_dense import BF16, F16, F32, gen_for, guard_ok, rnd, workspace
+import dense_reference as R
+from test_gpu_dense import ACTS, BF16, F16, F32, gen_for, guard_ok, rnd, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +51,84 @@ def test_a_token_has_the_same_bits_where_room_for_parts_is_short(N, gated, K, M,
                 assert torch.equal(a, b[rows]), rows
     finally:
         N.moe_debug_force_dense_plan()
+
+
+def limits(N, a):
+    """The activation's value and derivative at -infinity and at +infinity."""
+    inf = math.inf
+    return {N.MOE_ACT_NONE: ((-inf, 1), (inf, 1)), N.MOE_ACT_SIGMOID: ((0, 0), (1, 0))}.get(a, ((0, 0), (inf, 1)))
+
+
+@pytest.mark.parametrize("dt", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("a", ACTS)
+def test_saved_infinities_give_the_limits(N, a, dt):
+    """A pre-activation past the operands' type is saved as an infinity: its derivative is the limit there (0 or 1, and
+    the activation's value 0, 1 or an infinity), exactly; a gradient or a derivative of zero beside an infinite factor
+    gives zero; a NaN stays one."""
+    T, M = 5, 8
+    z = torch.tensor([-math.inf, math.inf] * 4, device="cuda").to(dt)
+    (v0, d0), (v1, d1) = limits(N, a)
+    slope = torch.tensor([d0, d1] * 4, device="cuda").double()
+    value = torch.tensor([v0, v1] * 4, device="cuda").double()
+    eye, ones = torch.eye(M, dtype=dt, device="cuda"), torch.ones(T, M, dtype=dt, device="cuda")
+    pre = z.repeat(T, 1)
+    d = N.dense_dims(M, M, N.dtype_code(ones), a)
+    ws, _ = workspace(N, d, T, True)
+    dx, dw, dw2 = torch.empty_like(ones), torch.empty_like(eye), torch.empty_like(eye)
+    db, db2 = torch.empty_like(z), torch.empty_like(z)
+    # dy = (1, 0, 1, 0, ..) down the tokens: T = 5 has three ones
+    dy = ones.clone()
+    dy[1::2] = 0
+    N.moe_linear_backward(d, ones, T, eye, dy, ws, pre=pre, dx=dx, dw=dw, dbias=db)
+    assert torch.equal(dx.double(), dy.double() * slope)
+    assert torch.equal(dw.double(), (3 * slope)[:, None].expand(M, M)) and torch.equal(db.double(), 3 * slope)
+    N.moe_gated_backward(d, ones, T, eye, eye, pre, ones, dy, ws, dw_gate=dw, dgate_bias=db, dup_bias=db2)
+    assert torch.equal(dw.double(), (3 * slope)[:, None].expand(M, M)) and torch.equal(db.double(), 3 * slope)
+    assert torch.equal(db2.double(), 3 * value)
+    # nothing comes back through either factor where dh is zero
+    N.moe_gated_backward(d, ones, T, eye, eye, pre, pre, torch.zeros_like(dy), ws, dx=dx, dw_gate=dw, dw_up=dw2,
+                         dgate_bias=db, dup_bias=db2)
+    for t in (dx, dw, dw2, db, db2):
+        assert (t == 0).all()
+    # an infinite up factor: dg is infinite, and zero where the derivative is
+    N.moe_gated_backward(d, ones, T, eye, eye, pre, pre, ones, ws, dgate_bias=db)
+    assert torch.equal(db.double(), torch.where(slope == 0, 0.0, z.double()))
+    # NaN
+    bad = torch.full_like(pre, math.nan)
+    if a not in (N.MOE_ACT_NONE, N.MOE_ACT_RELU):
+        N.moe_linear_backward(d, ones, T, eye, ones, ws, pre=bad, dbias=db)
+        assert torch.isnan(db).all()
+    N.moe_gated_backward(d, ones, T, eye, eye, bad, ones, ones, ws, dup_bias=db2)
+    assert torch.isnan(db2).all()
+    N.moe_gated_backward(d, ones, T, eye, eye, ones, bad, ones, ws, dgate_bias=db)
+    assert torch.isnan(db).all()
+
+
+@pytest.mark.parametrize("a", [1, 2, 3, 4], ids=["silu", "gelu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("T", [3, 70])
+def test_a_finite_forward_has_finite_gradients_past_fp16(N, a, T):
+    """z and g of -70000, past fp16: the outputs are finite, and so are the gradients, through the saved -infinity."""
+    K, M = 16, 24
+    gen = gen_for(33, a, T)
+    x, w, w2, dh = rnd(gen, (T, K), F16), rnd(gen, (M, K), F16, 0.25), rnd(gen, (M, K), F16, 0.25), rnd(gen, (T, M), F16)
+    x[1], w[:, 0] = 0, 2.0
+    x[1, 0] = -35000
+    w2[:, 0] = 2.0 ** -8
+    d = N.dense_dims(K, M, N.MOE_F16, a)
+    ws, _ = workspace(N, d, T, True)
+    y = torch.empty(T, M, device="cuda")
+    pre, h, g, u = (torch.empty(T, M, dtype=F16, device="cuda") for _ in range(4))
+    N.moe_linear_forward(d, x, T, w, y, ws, pre=pre)
+    N.moe_gated_forward(d, x, T, w, w2, h, ws, gate=g, up=u)
+    assert torch.isfinite(y).all() and torch.isfinite(h).all() and torch.isfinite(u).all()
+    assert (pre[1] == -math.inf).all() and (g[1] == -math.inf).all()
+    dx, dw, dw2, db, db2 = (torch.empty_like(t) for t in (x, w, w, dh[0], dh[0]))
+    low = torch.full_like(pre, -1000.0)  # where every derivative and value here is zero, too
+    N.moe_linear_backward(d, x, T, w, dh, ws, pre=pre, dx=dx, dw=dw, dbias=db)
+    ref = R.linear_backward(a, x, w, torch.where(torch.isinf(pre), low, pre), dh)
+    for name, t, k in (("dx", dx, "dx"), ("dw", dw, "dw0"), ("db", db, "db0")):
+        R.check(name, t, ref[k])
+    N.moe_gated_backward(d, x, T, w, w2, g, u, dh, ws, dx=dx, dw_gate=dw, dw_up=dw2, dgate_bias=db, dup_bias=db2)
+    ref = R.gated_backward(a, x, w, w2, torch.where(torch.isinf(g), low, g), u, dh)
+    for name, t, k in (("dx", dx, "dx"), ("dwg", dw, "dw0"), ("dwu", dw2, "dw1"), ("dbg", db, "db0"), ("dbu", db2, "db1")):
+        R.check(name, t, ref[k])
