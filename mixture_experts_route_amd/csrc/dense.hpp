@@ -38,10 +38,35 @@ MOE_DEV float fast_sigmoid(float z) {
 constexpr float kGeluC = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kGeluK = 0.044715f;
 
+// Phi(z) and e = exp(-z^2 / 2). For z < 0 Phi(z) = e erfcx(x) / 2, x = |z| / sqrt 2, without the cancellation of
+// (1 + erf) / 2 (5 % off at z = -5, 0 below -5.5); for z > 0 1 - Phi(-z). erfcx(x) / 2 = t P(t) with t = 1 / (1 + 0.45 x) and P
+// of degree 9, fitted over all x >= 0 to a relative 3.2e-8. In fp32 the whole is within (1.5 z^2 + 10) 2^-24 of its value
+// (z^2 / 2 rounded, then exp2; the hardware's exp2 and reciprocal 1 ulp each). No branches: gelu, 4096 x 4096 gated outputs
+// of 2048 terms 127.6 us with erff, 134.3 with erfcf, 121.0 with this.
+MOE_DEV float normal_cdf(float z, float& e) {
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.318198052f * fabsf(z));
+  e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+  float q = -0.0206957665f;
+  q = q * t + 0.0953447786f;
+  q = q * t - 0.15029258f;
+  q = q * t + 0.0712016206f;
+  q = q * t - 0.011179518f;
+  q = q * t + 0.0599753662f;
+  q = q * t + 0.0876260416f;
+  q = q * t + 0.114135822f;
+  q = q * t + 0.126941581f;
+  q = q * t + 0.12694266f;
+  const float tail = e * t * q;
+  return z < 0.0f ? tail : 1.0f - tail;
+}
+
 MOE_DEV float act_value(int act, float z) {
   switch (act) {
     case MOE_ACT_SILU: return z * fast_sigmoid(z);
-    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case MOE_ACT_GELU: {
+      float e;
+      return z * normal_cdf(z, e);
+    }
     case MOE_ACT_GELU_TANH: return z * fast_sigmoid(2.0f * kGeluC * z * (1.0f + kGeluK * z * z));  // (1 + tanh v) / 2 = sigmoid(2 v)
     case MOE_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
     case MOE_ACT_SIGMOID: return fast_sigmoid(z);
@@ -87,9 +112,10 @@ MOE_DEV void act_both(int act, float z, float& v, float& d) {
       break;
     }
     case MOE_ACT_GELU: {
-      const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+      float e;
+      const float cdf = normal_cdf(z, e);
       v = z * cdf;
-      d = cdf + z * 0.39894228040143268f * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+      d = cdf + z * 0.39894228040143268f * e;
       break;
     }
     case MOE_ACT_GELU_TANH: {

@@ -132,3 +132,43 @@ def test_a_finite_forward_has_finite_gradients_past_fp16(N, a, T):
     ref = R.gated_backward(a, x, w, w2, torch.where(torch.isinf(g), low, g), u, dh)
     for name, t, k in (("dx", dx, "dx"), ("dwg", dw, "dw0"), ("dwu", dw2, "dw1"), ("dbg", db, "db0"), ("dbu", db2, "db1")):
         R.check(name, t, ref[k])
+
+
+@pytest.mark.parametrize("T", [16, 97])
+def test_gelu_keeps_its_lower_tail(N, T):
+    """Exact gelu and its derivative at z = -9 .. -3, relative to their values.  Bounds in units of E = 2^-24 (fp32's
+    half step): the argument z / sqrt 2 is within 2 E, which erfc multiplies by z^2 + 1 at most; erfc itself is within
+    16 units in the last place, 32 E; two products, 2 E.  The density's exponent z^2 / 2 is within 3 E of itself; its
+    exponential and factors add 6 E."""
+    z = (-3 - torch.arange(T, device="cuda", dtype=torch.float64) % 97 / 16).to(BF16)  # exact in bf16
+    x, one = z[:, None].contiguous(), torch.ones(8, 1, dtype=BF16, device="cuda")
+    d = N.dense_dims(1, 8, N.MOE_BF16, N.MOE_ACT_GELU)
+    ws, _ = workspace(N, d, T, True)
+    zz = z.double()[:, None].expand(T, 8)
+    cdf, pdf = 0.5 * torch.special.erfc(-zz / math.sqrt(2)), torch.exp(-zz * zz / 2) / math.sqrt(2 * math.pi)
+    e_cdf, e_pdf = (2 * (zz * zz + 1) + 34) * R.E, (1.5 * zz * zz + 6) * R.E
+    value = (zz * cdf, e_cdf * (zz * cdf).abs())
+    slope = (cdf + zz * pdf, e_cdf * cdf + e_pdf * (zz * pdf).abs() + R.E * (cdf + zz * pdf).abs())
+
+    def rounded(v, e):  # a result in bf16
+        return v, e + R.half_step(BF16) * (v.abs() + e)
+
+    y = torch.empty(T, 8, device="cuda")
+    N.moe_linear_forward(d, x, T, one, y, ws)
+    R.check("y", y, value)
+    h, g, u = (torch.empty(T, 8, dtype=BF16, device="cuda") for _ in range(3))
+    N.moe_gated_forward(d, x, T, one, torch.zeros_like(one), h, ws, up_bias=torch.ones(8, dtype=BF16, device="cuda"),
+                        gate=g, up=u)
+    R.check("h", h, rounded(*value))
+    N.moe_gated_forward(d, x, T, one, one, h, ws)  # without saved factors or a bias: h = act(z) z
+    R.check("h", h, rounded(value[0] * zz, (value[1] + R.E * value[0].abs()) * zz.abs()))
+    # one token's column sums are dz itself: a bias gradient per token
+    db, db2 = (torch.empty(T, dtype=BF16, device="cuda") for _ in range(2))
+    dt = N.dense_dims(1, T, N.MOE_BF16, N.MOE_ACT_GELU)
+    row, ones, wt = z[None, :].contiguous(), torch.ones(1, T, dtype=BF16, device="cuda"), torch.ones(T, 1, dtype=BF16, device="cuda")
+    ws, _ = workspace(N, dt, 1, True)
+    N.moe_linear_backward(dt, ones[:, :1].contiguous(), 1, wt, ones, ws, pre=row, dbias=db)
+    R.check("dz", db, rounded(slope[0][:, 0], slope[1][:, 0]))
+    N.moe_gated_backward(dt, ones[:, :1].contiguous(), 1, wt, wt, row, ones, ones, ws, dgate_bias=db, dup_bias=db2)
+    R.check("dg", db, rounded(slope[0][:, 0], slope[1][:, 0]))
+    R.check("du", db2, rounded(value[0][:, 0], value[1][:, 0]))
