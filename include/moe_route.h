@@ -479,7 +479,8 @@ MOE_API int moe_pool_debug_fail_copies(moe_pool* pool, int32_t after_n);
  *   - ld* is a matrix's row stride in elements, at least its row length and at most MOE_DENSE_MAX_LD;
  *     rows may start at any element-aligned address (a slice of a wider tensor, an odd width; an odd
  *     address is MOE_EINVAL).  Operands on 16-byte addresses with strides (and n_in) a multiple of 8 run the
- *     asynchronous-copy kernels; others are first copied into the workspace or run slower kernels.
+ *     asynchronous-copy kernels, whatever each one's stride is.  Otherwise x (and the weights, where n_in is no
+ *     multiple of 8) is first copied into the workspace where that pays, and the rest runs kernels of about half the rate.
  *   - 1 <= n_in, n_out <= MOE_DENSE_MAX_WIDTH; 1 <= n_tokens <= MOE_DENSE_MAX_TOKENS (beyond:
  *     MOE_EUNSUPPORTED).
  *   - Sums are fp32 in a fixed order, so equal calls give equal bits.  Up to

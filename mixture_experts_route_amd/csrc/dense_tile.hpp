@@ -485,45 +485,54 @@ struct OperandCopy {
 
 // The steps of one half tile, in order: a running address and the steps left, so that issuing a step costs few
 // scalar instructions (a wave issues one instruction per four to five cycles: at ~40 per copy the 64 x 64 tile
-// took 0.35 us a step, whatever was in flight). SEGS: a second matrix of the same stride follows the first.
+// took 0.35 us a step, whatever was in flight). SEGS: a second matrix follows the first; kCols operands have a stride
+// for each (dx: Wg and Wu), kRows ones the same (dg and du).
 template <int ORDER, int H, int WAVES, bool SEGS>
 struct HalfStream {
   typedef OperandCopy<ORDER, H, WAVES> Copy;
   uint64_t p, p1;       // first element of the next step; of the second matrix
   uint64_t stride;      // bytes from a step to the next
   int32_t bytes;        // of the resource in a whole step, 0 if the half tile has no outputs
-  int32_t cut;          // what the resource lacks in the last, partial step of a matrix
+  int32_t cut;          // reduction elements that the last, partial step of a matrix lacks
   int32_t left, left1;  // steps left in this matrix, the one to be issued included; in the second one
+  int32_t ld1;          // kCols: the second matrix's stride in elements
   int32_t end, end1;    // left's value after a matrix's last step if that is partial and this workgroup's, else one it never takes
 
   // first: the half tile's first element; outs: its outputs that exist; R: reduction length (kRows: readable
   // elements of a line); the workgroup takes steps begin .. begin + count - 1 of the one or two matrices of
   // `steps` steps each.
-  MOE_DEV void init(const void* m0, const void* m1, int64_t ld, int64_t o0, int O, int R, int steps, int begin, int count) {
+  MOE_DEV void init(Copy& c, const void* m0, const void* m1, int64_t ld, int64_t ld_second, int64_t o0, int O, int R, int steps,
+                    int begin, int count) {
     const int64_t first = 2 * (ORDER == kRows ? o0 * ld : o0);
     stride = ORDER == kRows ? 2 * kStepR : 2 * kStepR * (uint64_t)ld;
     const int n = O - o0 < H ? (int)(O - o0) : H;
     // (an odd row's last element shares its 4-byte word with what follows; a word is read whole or not at all)
     bytes = n <= 0 ? 0 : ORDER == kRows ? 2 * ((n - 1) * (int32_t)ld + kStepR) : 2 * ((kStepR - 1) * (int32_t)ld + n + (n & 1));
     const int tail = R - (steps - 1) * kStepR;
-    cut = n <= 0 ? 0 : 2 * (kStepR - tail) * (ORDER == kRows ? 1 : (int32_t)ld);
+    cut = n <= 0 ? 0 : kStepR - tail;
     const int in0 = begin >= steps ? 0 : (begin + count < steps ? count : steps - begin);
     const int b1 = begin > steps ? begin - steps : 0;
     p = (uint64_t)m0 + first + begin * stride;
     left = in0;
     end = cut && begin + count >= steps ? 0 : -(1 << 30);
     if constexpr (SEGS) {
-      p1 = (uint64_t)m1 + first + b1 * stride;
+      ld1 = (int32_t)ld_second;
+      p1 = (uint64_t)m1 + (ORDER == kRows ? first + b1 * stride : 2 * (o0 + b1 * kStepR * ld_second));
       left1 = count - in0;
       end1 = cut && begin + count >= 2 * steps ? 0 : -(1 << 30);
-      if (left == 0) second();
+      if (left == 0) second(c);
     }
   }
-  MOE_DEV void second() {
+  MOE_DEV void second(Copy& c) {
     p = p1;
     left = left1;
     end = end1;
     left1 = 0;
+    if constexpr (ORDER == kCols) {
+      if (bytes) bytes += 2 * (kStepR - 1) * (ld1 - (int32_t)(stride / (2 * kStepR)));
+      stride = 2 * kStepR * (uint64_t)ld1;
+      c.init(ld1, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), threadIdx.x & 63);
+    }
   }
   // Issues this wave's copies of the next step. With no steps left the same number of copies is issued, all
   // past the resource's end: nothing is read, zeros are written.
@@ -537,10 +546,10 @@ struct HalfStream {
     --left;
     const bool tail = left == end;
     if (__builtin_expect(tail, 0)) {
-      rsrc[2] = bytes - cut;
+      rsrc[2] = bytes - 2 * cut * (ORDER == kRows ? 1 : (int32_t)(stride / (2 * kStepR)));
       // a kRows line continues past the reduction's end (its next line, or what lies between): those chunks are
       // not read
-      if (ORDER == kRows && c.chunk * 8 >= kStepR - cut / 2)
+      if (ORDER == kRows && c.chunk * 8 >= kStepR - cut)
 #pragma unroll
         for (int d = 0; d < Copy::kCopies; ++d) c.voff[d] |= 0x80000000u;
     }
@@ -550,7 +559,7 @@ struct HalfStream {
 #pragma unroll
       for (int d = 0; d < Copy::kCopies; ++d) c.voff[d] &= 0x7FFFFFFFu;
     if constexpr (SEGS) {
-      if (left == 0 && left1 > 0) second();
+      if (left == 0 && left1 > 0) second(c);
     }
   }
 };
@@ -585,13 +594,14 @@ MOE_DEV void deep_tile(const TileArgs& a, uint32_t id, uint32_t ids, uint16_t* l
   HalfStream<OA, HI, W, kSegs> sa;
   HalfStream<OB, HJ, W, kSegs> sb[2];
   ca.init(a.lda[0], wave, lane);
-  sa.init(kBatches && x.batch ? a.a[1] : a.a[0], a.a[1], a.lda[0], i0, a.M, OA == kRows ? a.len_a : a.R, steps, s_begin, count);
+  sa.init(ca, kBatches && x.batch ? a.a[1] : a.a[0], a.a[1], a.lda[0], 0, i0, a.M, OA == kRows ? a.len_a : a.R, steps, s_begin,
+          count);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     constexpr bool g = KIND == kEpiGated;
     cb[h].init(a.ldb[g ? h : 0], wave, lane);
-    sb[h].init(a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], j0 + (g ? 0 : h * HJ), a.N, OB == kRows ? a.len_b : a.R, steps, s_begin,
-               count);
+    sb[h].init(cb[h], a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], a.ldb[1], j0 + (g ? 0 : h * HJ), a.N,
+               OB == kRows ? a.len_b : a.R, steps, s_begin, count);
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds;
   auto copy = [&](uint32_t to) {  // the next step into the stage at `to`
@@ -724,11 +734,11 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     constexpr bool g = KIND == kEpiGated;
-    sa[h].init(kBatches && x.batch ? a.a[1] : a.a[0], a.a[1], a.lda[0], i0 + h * HI, a.M, OA == kRows ? a.len_a : a.R, steps,
-               s_begin, count);
+    sa[h].init(ca, kBatches && x.batch ? a.a[1] : a.a[0], a.a[1], a.lda[0], 0, i0 + h * HI, a.M, OA == kRows ? a.len_a : a.R,
+               steps, s_begin, count);
     cb[h].init(a.ldb[g ? h : 0], wave, lane);
-    sb[h].init(a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], j0 + (g ? 0 : h * HJ), a.N, OB == kRows ? a.len_b : a.R, steps, s_begin,
-               count);
+    sb[h].init(cb[h], a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], a.ldb[1], j0 + (g ? 0 : h * HJ), a.N,
+               OB == kRows ? a.len_b : a.R, steps, s_begin, count);
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds;
   const uint32_t mine = lds0 + wave * 1024;
@@ -953,8 +963,7 @@ bool pack_operands(TileArgs& a, bool whole_a, const bool (&whole_b)[2], hipStrea
   }
   b.len_b = OB == kRows && !(whole_b[0] && whole_b[1]) ? (a.R + 7) / 8 * 8 : a.R;
   for (int m = 0; m < nb; ++m) {
-    const bool needs = nb == 2 ? !(whole_b[0] && whole_b[1]) : !whole_b[0];  // both, for equal strides
-    if (needs && !add(b.b[m], b.ldb[m], a.pack_b[m], OB == kRows ? a.N : a.R, OB == kRows ? a.R : a.N)) return false;
+    if (!whole_b[m] && !add(b.b[m], b.ldb[m], a.pack_b[m], OB == kRows ? a.N : a.R, OB == kRows ? a.R : a.N)) return false;
   }
   if (a.nbatch > 1) b.b[1] = b.b[0], b.ldb[1] = b.ldb[0];
   double direct, packed;
@@ -974,7 +983,6 @@ hipError_t prepare_tile(TileArgs& a, DensePlan& plan, double& us, hipStream_t st
     whole_a = whole_a && whole_chunks(OA, a.a[m], a.lda[m], a.len_a);
   for (int m = 0; m < (KIND == kEpiGated || a.nseg > 1 ? 2 : 1); ++m)
     whole_b[m] = whole_chunks(OB, a.b[m], a.ldb[m], a.R);
-  if (a.nseg > 1 && a.ldb[0] != a.ldb[1]) whole_b[1] = false;
   bool whole = whole_a && whole_b[0] && whole_b[1];
   if (!whole && g_dense_plan.kernel < MOE_DENSE_ANY64) {
     hipError_t err = hipSuccess;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import dense_reference as R
-from test_gpu_dense import ACTS, BF16, F16, F32, gen_for, guard_ok, rnd, workspace
+from test_gpu_dense import ACTS, BF16, F16, F32, Out, gen_for, guard_ok, rnd, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -172,3 +172,30 @@ def test_gelu_keeps_its_lower_tail(N, T):
     N.moe_gated_backward(dt, ones[:, :1].contiguous(), 1, wt, wt, row, ones, ones, ws, dgate_bias=db, dup_bias=db2)
     R.check("dg", db, rounded(slope[0][:, 0], slope[1][:, 0]))
     R.check("du", db2, rounded(value[0][:, 0], value[1][:, 0]))
+
+
+@pytest.mark.parametrize("splits", [0, 2, 3, 7])
+@pytest.mark.parametrize("kernel", [1, 2, 3], ids=["tile64", "tile128", "tile256"])
+def test_weights_of_two_strides_run_the_same_kernels(N, kernel, splits):
+    """dx of the gated block with whole 16-byte rows of different strides in Wg and Wu: the tile kernels take them (a kernel
+    forced on them runs, unsplit where no parts are asked for), so the bits are those of equal strides; parts that
+    begin in either matrix, partial last steps, an odd width."""
+    N.moe_debug_force_dense_plan(kernel, splits)
+    try:
+        for T, K, M, pad_g, pad_u in ((70, 264, 2056, 0, 24), (257, 520, 1000, 56, 8), (40, 261, 4160, 3, 11),
+                                      (300, 1000, 72, 0, 8)):
+            gen = gen_for(34, T, K, M)
+            x, g, u, dh = rnd(gen, (T, K), F16), *(rnd(gen, (T, M), F16) for _ in range(3))
+            wg, wu = rnd(gen, (M, K), F16, K ** -0.5, pad=pad_g), rnd(gen, (M, K), F16, K ** -0.5, pad=pad_u)
+            same = rnd(gen, (M, K), F16, pad=pad_g)
+            same.copy_(wu)
+            d = N.dense_dims(K, M, N.MOE_F16, N.MOE_ACT_SILU)
+            ws, whole = workspace(N, d, T, True)
+            out, want = Out((T, K), F16, 8), Out((T, K), F16, 8)
+            N.moe_gated_backward(d, x, T, wg, wu, g, u, dh, ws, dx=out.t)
+            N.moe_gated_backward(d, x, T, wg, same, g, u, dh, ws, dx=want.t)
+            assert torch.equal(out.t, want.t)
+            R.check("dx", out.t, R.gated_backward(N.MOE_ACT_SILU, x, wg, wu, g, u, dh)["dx"])
+            assert out.untouched() and guard_ok(whole)
+    finally:
+        N.moe_debug_force_dense_plan()
