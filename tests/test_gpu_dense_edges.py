@@ -199,3 +199,79 @@ def test_weights_of_two_strides_run_the_same_kernels(N, kernel, splits):
             assert out.untouched() and guard_ok(whole)
     finally:
         N.moe_debug_force_dense_plan()
+
+
+def ints(gen, rows, cols, dt, pad=0):
+    """Whole numbers -2 .. 2: every product and every sum here is exact in fp32, in any order."""
+    t = torch.full((rows, cols + pad), math.nan, dtype=dt, device="cuda")[:, :cols]
+    return t.copy_(torch.randint(-2, 3, (rows, cols), generator=gen, device="cuda"))
+
+
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("splits", [0, 3])
+@pytest.mark.parametrize("kernel", range(6), ids=["auto", "tile64", "tile128", "tile256", "any64", "any128"])
+def test_long_sums_of_whole_numbers_are_exact(N, kernel, splits, pad):
+    """Every product at long reductions, where a lost, stale or doubled chunk would hide in the bounds of rounded sums:
+    equal to the exact result, and to its rounding where it is stored in 16 bits."""
+    N.moe_debug_force_dense_plan(kernel, splits)
+    try:
+        for dt, short, long in ((BF16, 264, 8256), (F16, 130, 5000)):
+            gen = gen_for(35, kernel, splits, pad, short)
+            T, K, M = short, long, 392  # sums over K
+            x, w, w2 = ints(gen, T, K, dt, pad), ints(gen, M, K, dt, pad), ints(gen, M, K, dt, pad)
+            d = N.dense_dims(K, M, N.dtype_code(x), N.MOE_ACT_NONE)
+            ws, _ = workspace(N, d, T, False)
+            y = Out((T, M), F32)
+            h, g, u = (Out((T, M), dt) for _ in range(3))
+            N.moe_linear_forward(d, x, T, w, y.t, ws)
+            N.moe_gated_forward(d, x, T, w, w2, h.t, ws, gate=g.t, up=u.t)
+            zg, zu = x.double() @ w.double().T, x.double() @ w2.double().T
+            assert torch.equal(y.t.double(), zg) and torch.equal(g.t, zg.to(dt)) and torch.equal(u.t, zu.to(dt))
+            for T, K, M in ((short, 200, long), (long, 200, short)):  # sums over M (dx), over T (dW)
+                x, w, w2 = ints(gen, T, K, dt, pad), ints(gen, M, K, dt, pad), ints(gen, M, K, dt, pad)
+                g, u, dh = (ints(gen, T, M, dt, pad) for _ in range(3))
+                d = N.dense_dims(K, M, N.dtype_code(x), N.MOE_ACT_NONE)
+                ws, whole = workspace(N, d, T, True)
+                dx, dw, dw2, dx1, dw1 = (Out(s, dt) for s in ((T, K), (M, K), (M, K), (T, K), (M, K)))
+                N.moe_gated_backward(d, x, T, w, w2, g, u, dh, ws, dx=dx.t, dw_gate=dw.t, dw_up=dw2.t)
+                N.moe_linear_backward(d, x, T, w, dh, ws, dx=dx1.t, dw=dw1.t)
+                dg, du = dh.double() * u.double(), dh.double() * g.double()
+                for got, want in ((dx, dg @ w.double() + du @ w2.double()), (dw, dg.T @ x.double()), (dw2, du.T @ x.double()),
+                                  (dx1, dh.double() @ w.double()), (dw1, dh.double().T @ x.double())):
+                    assert torch.equal(got.t, want.to(dt)) and got.untouched()
+                assert guard_ok(whole)
+    finally:
+        N.moe_debug_force_dense_plan()
+
+
+@pytest.mark.parametrize("kernel,splits,shape", [
+    (0, 0, (2200, 4104, 4050)),  # the last tiles in parts
+    (0, 0, (333, 1000, 1357)), (1, 0, (300, 4096, 520)), (2, 0, (520, 4096, 520)), (3, 0, (520, 4096, 520)),
+    (3, 5, (300, 2056, 2056)), (4, 2, (130, 1001, 264)), (5, 0, (300, 1001, 264))], ids=str)
+def test_equal_calls_give_equal_bits_at_any_size(N, kernel, splits, shape):
+    """The same four calls three times, outputs and workspace full of something else in between."""
+    T, K, M = shape
+    gen = gen_for(36, kernel, splits, *shape)
+    x, dh = rnd(gen, (T, K), F16), rnd(gen, (T, M), F16)
+    w, w2 = (rnd(gen, (M, K), F16, K ** -0.5) for _ in range(2))
+    d = N.dense_dims(K, M, N.MOE_F16, N.MOE_ACT_GELU)
+    ws, _ = workspace(N, d, T, True)
+    nan = lambda *s, dt=F16: torch.full(s, math.nan, dtype=dt, device="cuda")
+    N.moe_debug_force_dense_plan(kernel, splits)
+    try:
+        first = None
+        for rep in range(3):
+            y, h, g, u, pre = nan(T, M, dt=F32), nan(T, M), nan(T, M), nan(T, M), nan(T, M)
+            dx, dw, db, dx2, dwg, dwu = nan(T, K), nan(M, K), nan(M), nan(T, K), nan(M, K), nan(M, K)
+            N.moe_linear_forward(d, x, T, w, y, ws, pre=pre)
+            N.moe_gated_forward(d, x, T, w, w2, h, ws, gate=g, up=u)
+            N.moe_linear_backward(d, x, T, w, dh, ws, pre=pre, dx=dx, dw=dw, dbias=db)
+            N.moe_gated_backward(d, x, T, w, w2, g, u, dh, ws, dx=dx2, dw_gate=dwg, dw_up=dwu)
+            out = (y, h, g, u, pre, dx, dw, db, dx2, dwg, dwu)
+            assert not any(torch.isnan(t).any() for t in out)
+            if first is None:
+                first = out
+            assert all(torch.equal(a, b) for a, b in zip(out, first)), rep
+            ws.view(torch.uint8)[4096:].fill_(0xFF)
+    finally:
+        N.moe_debug_force_dense_plan()
