@@ -487,13 +487,16 @@ MOE_API int moe_pool_debug_fail_copies(moe_pool* pool, int32_t after_n);
  *     MOE_DENSE_ROW_TOKENS tokens a forward pass gives a token the same bits alone and in any batch.
  *     Results are rounded to their type once (to nearest even); a value beyond fp16's range becomes
  *     infinite, as the type has it.  The backward passes round dz (dg, du) to dims->dtype before the
- *     matrix products; the bias gradients sum it unrounded.
+ *     matrix products; the bias gradients sum it unrounded.  In fp16 a dz past 65504 is thus an infinity to its token's
+ *     dx and its output's dW, finite though they may be, and one below 2^-25 is zero: scale the incoming gradient.
+ *   - silu and sigmoid are 0 below z = -87 (by definition less than 2^-118 from it).
  *   - A NaN or an infinity stays in the rows and columns that its definition reaches; nothing between the
  *     rows of a matrix (ld > row length) is used, nor written.
  *   - A pre-activation past dims->dtype's range is saved as an infinity.  The backward passes take the limits
  *     there: act' is 0 or 1, act is 0, 1 or infinite; a zero gradient (or act') times an infinite factor is 0.
  *   - Outputs must not overlap inputs or each other, except y on r exactly (same address and
  *     stride).  A NULL output of a backward pass is not computed; at least one must be given.
+ *   - A launch that fails (MOE_EHIP) may leave a call's earlier launches enqueued.
  *   - `ws` as everywhere: moe_dense_workspace_bytes(dims, n_tokens, backward) bytes, cleared once
  *     with moe_workspace_init.  The layer's calls and these may share one, ordered on one stream.
  */

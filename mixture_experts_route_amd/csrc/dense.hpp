@@ -28,9 +28,11 @@ struct Operand<_Float16> {
 };
 
 // ---- activations ----------------------------------------------------------------------------------
-// sigmoid by the hardware's exp2 and reciprocal (each within 1 ulp): relative error about
-// (2 + |z|) 2^-24, below a 16-bit output's half step by a factor of 2^10 and at fp32's own level for an
-// fp32 output.  exp2 overflowing to infinity gives 0, its underflow 1, as the function does.
+// sigmoid by the hardware's exp2 and reciprocal (each within 1 ulp), its argument rounded once: relative error about
+// (2 + |z|) 2^-24 (measured: up to 1.15 times that). That is 2^-17.3 at z = -87 and 2^-19.7 at -17, where fp16's
+// numbers end: at least 2^7 below a 16-bit output's half step; of an fp32 output it is 2 + |z| half steps. Below
+// z = -87 the reciprocal of 1 + exp(-z) is no normal number and the result is 0 (sigmoid is under 2^-125 there);
+// exp2's underflow gives 1, as it should.
 MOE_DEV float fast_sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }

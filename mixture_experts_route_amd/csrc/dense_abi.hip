@@ -1,5 +1,6 @@
 // The dense operators' C interface (moe_linear_*, moe_gated_*): host-side validation, workspace carving
-// and launches.  Nothing is enqueued when a call returns an error.
+// and launches.  Nothing is enqueued when a call refuses its arguments or workspace; a backward pass whose later launch
+// fails (MOE_EHIP) may have run its earlier ones.
 #include "dense.hpp"
 
 namespace moe {

@@ -24,7 +24,9 @@ MOE_DEV void load8f(const void* base, int64_t off, int e, int N, float v[8]) {
 // TB/s). A workgroup takes 512 columns (8 per lane, 16 bytes a load) of a run of rows; its 4 waves take every
 // fourth row and keep the column sums of their rows in registers, added over the waves in LDS in wave order. Infinite saved
 // values show as NaN in dz, and only a chunk with one is computed again with their limits (checks of every element
-// took the pass from 117 to 130 us).
+// took the pass from 117 to 130 us). dz is rounded to the operands' type, as the matrix cores need it: dx and dW are
+// 2.34e-3 off their definition against 1.66e-3 with an fp32 dz (bf16; fp16 2.9e-4 and 2.1e-4), at half the products of a dz in
+// two 16-bit parts; the column sums take it unrounded.
 template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void k_grad_in(GradArgs a) {
   __shared__ float red[3][2][512];

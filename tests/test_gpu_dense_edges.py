@@ -275,3 +275,29 @@ def test_equal_calls_give_equal_bits_at_any_size(N, kernel, splits, shape):
             ws.view(torch.uint8)[4096:].fill_(0xFF)
     finally:
         N.moe_debug_force_dense_plan()
+
+
+@pytest.mark.parametrize("T", [5, 90])
+def test_fp16_dz_past_its_range_is_infinite_and_stays_in_its_row(N, T):
+    """dg = dh u act'(g) of finite factors past 65504 becomes an infinity on its way into the products, as stated: its token's
+    dx and its output's dWg are not finite, everything else is right; a scaled incoming gradient gives it all."""
+    K, M = 40, 72
+    gen = gen_for(37, T)
+    x, wg, wu = rnd(gen, (T, K), F16), rnd(gen, (M, K), F16, K ** -0.5), rnd(gen, (M, K), F16, K ** -0.5)
+    g, u, dh = rnd(gen, (T, M), F16), rnd(gen, (T, M), F16), rnd(gen, (T, M), F16, 0.1)
+    g[3, 7], u[3, 7], dh[3, 7] = 4, 250, 300  # dg = 300 250 1.05 = 79000, du = 1178
+    d = N.dense_dims(K, M, N.MOE_F16, N.MOE_ACT_SILU)
+    ws, _ = workspace(N, d, T, True)
+    for scale in (1.0, 2.0 ** -6):
+        dy = dh * scale
+        dx, dwg, dwu, dbg, dbu = (torch.empty_like(t) for t in (x, wg, wu, g[0], g[0]))
+        N.moe_gated_backward(d, x, T, wg, wu, g, u, dy, ws, dx=dx, dw_gate=dwg, dw_up=dwu, dgate_bias=dbg, dup_bias=dbu)
+        ref = R.gated_backward(N.MOE_ACT_SILU, x, wg, wu, g, u, dy)
+        bad_x, bad_w, bad_b = (torch.zeros_like(t, dtype=torch.bool) for t in (dx, dwg, dbg))
+        if scale == 1:
+            bad_x[3], bad_w[7], bad_b[7] = True, True, True
+        for name, got, bad, k in (("dx", dx, bad_x, "dx"), ("dwg", dwg, bad_w, "dw0"), ("dbg", dbg, bad_b, "db0")):
+            assert torch.equal(~torch.isfinite(got), bad), name
+            R.check(name, torch.where(bad, ref[k][0].to(F16), got).double().where(~bad, ref[k][0]), ref[k])
+        R.check("dwu", dwu, ref["dw1"])
+        R.check("dbu", dbu, ref["db1"])
