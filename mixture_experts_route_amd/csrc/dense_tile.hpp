@@ -341,8 +341,8 @@ struct AnyLoad {
 
 // (64 F) x (64 F) tile, 4 waves of (32 F) x (32 F); operands pass through registers, two steps ahead, into two
 // LDS buffers, so that any address, stride and length works. Bound by the latency and rate of unaligned loads:
-// 0.9 us a step with 64-square tiles, 1.5 with 128 (4096 x 4095 outputs of 4095 terms 257 us; through copies
-// with whole rows 171 us).
+// 0.9 us a step with 64-square tiles, 1.5 with 128 (4096 x 4095 outputs of 4095 terms 216 us; through copies
+// with whole rows 142 us).
 template <typename T, int OA, int OB, int KIND, int F>
 __global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
   constexpr int H = 32 * F, kBuf = 4 * H * kStepR;  // elements: A0 A1 B0 B1
@@ -941,7 +941,7 @@ hipError_t start_plan(TileArgs a, int kernel, hipStream_t st) {
 
 // Gives the operands that lack them whole 16-byte chunks, by copies in the workspace, when that pays: the copy
 // costs a launch and the operand's bytes twice, the other kernels run at about half the rate (4096 x 4096
-// tokens and outputs of 4095 inputs: 258 us without copies).
+// tokens and outputs of 4095 inputs: 206 us without copies, 138 with; whole rows 106).
 template <int OA, int OB, int KIND>
 bool pack_operands(TileArgs& a, bool whole_a, const bool (&whole_b)[2], hipStream_t st, hipError_t* err) {
   const int na = a.nseg > 1 || a.nbatch > 1 ? 2 : 1, nb = KIND == kEpiGated || a.nseg > 1 ? 2 : 1;
