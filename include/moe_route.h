@@ -84,7 +84,7 @@ enum moe_status {
   MOE_EFILL = -6          /* a slot-pool fill (host -> HBM expert copy) failed */
 };
 
-/* MOE_F16 is an operand type of the dense operators (moe_linear_*, moe_gated_*) only. */
+/* MOE_F16 is an operand type of the dense operators (moe_linear_*, moe_gated_*) and of those after them only. */
 enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 };
 
 /* Device error word bits (moe_check_device_error). */
@@ -95,8 +95,10 @@ enum moe_device_error {
   MOE_DERR_NAN = 8,           /* a NaN logit reached the selection */
   MOE_DERR_FILL = 16,         /* the slot-pool service reported a failed fill */
   MOE_DERR_DUP_ID = 32,       /* a token's top-k list names one expert twice */
-  MOE_DERR_RANGE = 64         /* prefill: an activation, SwiGLU output or weighted expert row
+  MOE_DERR_RANGE = 64,        /* prefill: an activation, SwiGLU output or weighted expert row
                                  beyond the fp16 range (|v| > 65504) or not finite */
+  MOE_DERR_ROWS = 128         /* rows by expert: a pair out of range or in two rows, a row out of
+                                 range, perm and inv at odds */
 };
 
 /* Largest token count of a decode call.  The pages' decode batches: concurrent streams (Basalt
@@ -563,6 +565,67 @@ MOE_API int moe_gated_backward(const moe_dense_dims* dims, const void* x, int64_
                                void* dx_or_null, int64_t ld_dx, void* dw_gate_or_null, int64_t ld_dwg,
                                void* dw_up_or_null, int64_t ld_dwu, void* dbias_gate_or_null, void* dbias_up_or_null,
                                void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Rows by expert ---------------------------------------------------------------------------
+ * The routed layer's data movement where its experts are not the 4-bit blobs of moe_layer_forward, for
+ * training and for 16-bit experts: token rows laid out by expert and back, with the router weights
+ * applied, each with its gradient.  With the pairs p = t*k + j of moe_group_tokens, perm[r] the pair in
+ * row r, inv[p] the row of pair p:
+ *
+ *   dispatch  xs[r] = x[perm[r] / k]                   dx[t] = sum_j dxs[inv[t*k+j]] + r[t]    (r optional)
+ *   combine   y[t] = sum_j w[t][j] ys[inv[t*k+j]] + r[t]                                       (r optional)
+ *             dys[r] = w[perm[r]] dy[perm[r] / k]      dw[t][j] = sum_i dy[t][i] ys[inv[t*k+j]][i]
+ *
+ * Conventions, beyond those at the top of this file and those of the dense operators for types, strides,
+ * alignment, overlap and rounding:
+ *   - perm [n_rows] is moe_group_tokens' or a caller's own.  A negative entry is a padding row (groups
+ *     padded to a multiple, room behind the last group): zero in xs and dys, read by nobody.  A pair that no
+ *     row has (a dropped one) has inv = -1: it adds nothing, its dw is 0.
+ *   - A pair >= n_tokens * k in perm, a pair in two rows, an inv entry >= n_rows and, in the combine's backward
+ *     pass, an inv that is not perm's set MOE_DERR_ROWS: what they name is taken as absent, no access
+ *     leaves the arrays, and the call's outputs are invalid.
+ *   - Sums are fp32, over j (or i) in a fixed order: equal calls give equal bits.
+ *   - 1 <= k <= 16; 1 <= width <= MOE_DENSE_MAX_WIDTH; 1 <= n_tokens <= MOE_DENSE_MAX_TOKENS;
+ *     1 <= n_rows <= MOE_ROWS_MAX (beyond: MOE_EUNSUPPORTED).
+ *   - `ws`: moe_rows_workspace_bytes(dims, n_tokens) bytes, or any larger workspace of the library's.
+ */
+#define MOE_ROWS_MAX (1 << 28)
+
+typedef struct moe_rows_dims {
+  int32_t width;  /* row length of x, xs, ys, y and their gradients */
+  int32_t top_k;  /* pairs per token */
+  int32_t dtype;  /* of x, xs, ys, dxs, dys: MOE_BF16 or MOE_F16 */
+} moe_rows_dims;
+
+/* Workspace bytes of the calls below; 0 if dims are invalid or max_tokens out of range. */
+MOE_API size_t moe_rows_workspace_bytes(const moe_rows_dims* dims, int32_t max_tokens);
+
+/* xs [n_rows][width] = the rows of x [n_tokens][width] that perm [n_rows] names; inv [n_tokens][k] out. */
+MOE_API int moe_dispatch_forward(const moe_rows_dims* dims, const void* x, int64_t ldx, int32_t n_tokens,
+                                 const int32_t* perm, int32_t n_rows, void* xs, int64_t ld_xs, int32_t* inv, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* dx [n_tokens][width] (dx_dtype: dims->dtype or MOE_F32) = each token's sum of its rows of dxs [n_rows][width],
+ * plus residual of dx_dtype, if not NULL (the gradient that reaches x by another way). */
+MOE_API int moe_dispatch_backward(const moe_rows_dims* dims, const void* dxs, int64_t ld_dxs, int32_t n_rows,
+                                  const int32_t* inv, int32_t n_tokens, const void* residual_or_null,
+                                  int64_t ld_residual, void* dx, int64_t ld_dx, int32_t dx_dtype, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* y [n_tokens][width] (y_dtype: dims->dtype or MOE_F32) from ys [n_rows][width] and topk_w [n_tokens][k] fp32;
+ * residual of y_dtype or NULL (a shared expert's output, the stream it is added to). */
+MOE_API int moe_combine_forward(const moe_rows_dims* dims, const void* ys, int64_t ld_ys, int32_t n_rows,
+                                const int32_t* inv, const float* topk_w, int32_t n_tokens, const void* residual_or_null,
+                                int64_t ld_residual, void* y, int64_t ldy, int32_t y_dtype, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/* Gradients of moe_combine_forward from dy [n_tokens][width] of dy_dtype (dims->dtype or MOE_F32); the residual's is
+ * dy itself.  dys [n_rows][width] and dtopk_w [n_tokens][k] fp32: NULL = not wanted (not both).  ys is needed for
+ * dtopk_w only (else ignored, may be NULL). */
+MOE_API int moe_combine_backward(const moe_rows_dims* dims, const void* dy, int64_t ld_dy, int32_t dy_dtype,
+                                 int32_t n_tokens, const int32_t* perm, const int32_t* inv, int32_t n_rows,
+                                 const float* topk_w, const void* ys_or_null, int64_t ld_ys, void* dys_or_null,
+                                 int64_t ld_dys, float* dtopk_w_or_null, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,6 +1,7 @@
 // The dense operators' C interface (moe_linear_*, moe_gated_*): host-side validation, workspace carving
 // and launches.  Nothing is enqueued when a call refuses its arguments or workspace; a backward pass whose later launch
 // fails (MOE_EHIP) may have run its earlier ones.
+#include "checks.hpp"
 #include "dense.hpp"
 
 namespace moe {
@@ -13,8 +14,6 @@ struct DenseWs {
   size_t part, x, w[2], dz0, dz1, bias_part, total;
   int64_t ldz;
 };
-
-static size_t dense_align(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Room for the sums of split reductions: what kMaxSplits splits of the largest product would take, up to a limit.
 static size_t part_bytes(const moe_dense_dims* d, int64_t T, bool backward) {
@@ -66,35 +65,10 @@ static int check_dense(const moe_dense_dims* d) {
   return MOE_OK;
 }
 
-static int check_tokens(int32_t T) {
-  if (T < 1) return MOE_EINVAL;
-  return T > MOE_DENSE_MAX_TOKENS ? MOE_EUNSUPPORTED : MOE_OK;
-}
-
-// Collects the checks of a call's matrices: element-aligned, rows that do not overlap, strides in range.
-struct Mats {
-  int rc = MOE_OK;
-  void fail(int code) {
-    if (rc == MOE_OK) rc = code;
-  }
-  void need(const void* p, int64_t ld, int64_t len, int elem = 2) {
-    if (!p) fail(MOE_EINVAL);
-    else opt(p, ld, len, elem);
-  }
-  void opt(const void* p, int64_t ld, int64_t len, int elem = 2) {
-    if (!p) return;
-    if ((uintptr_t)p % elem || ld < len) fail(MOE_EINVAL);
-    else if (ld > MOE_DENSE_MAX_LD) fail(MOE_EUNSUPPORTED);
-  }
-  void vec(const void* p) { opt(p, 1, 1); }
-};
-
 static int check_dense_ws(const moe_dense_dims* d, int32_t T, bool backward, const void* ws, size_t ws_bytes) {
   if (!ws || ((uintptr_t)ws & 255)) return MOE_EWORKSPACE;
   return ws_bytes < dense_ws(d, T, backward).total ? MOE_EWORKSPACE : MOE_OK;
 }
-
-static int dense_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
 static TileArgs tile_args(const moe_dense_dims* d, int64_t T, bool backward, void* ws) {
   const DenseWs L = dense_ws(d, T, backward);

@@ -9,6 +9,7 @@ the native library and raises ImportError when it is missing: there is no fallba
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -24,7 +25,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP, MOE_EDEVICE, MOE_EFILL = 0, -1, -2, -3, -4, -5, -6
 MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_DECODE_MAX_TOKENS, MOE_DECODE_MAX_TOKENS_NARROW = 16, 8
-DERR_EXPERT_ID, DERR_SLOT, DERR_NOT_RESIDENT, DERR_NAN, DERR_FILL, DERR_DUP_ID, DERR_RANGE = 1, 2, 4, 8, 16, 32, 64
+DERR_EXPERT_ID, DERR_SLOT, DERR_NOT_RESIDENT, DERR_NAN, DERR_FILL, DERR_DUP_ID, DERR_RANGE, DERR_ROWS = 1, 2, 4, 8, 16, 32, 64, 128
 
 EXPORTS = [
     "moe_expert_blob_bytes", "moe_workspace_bytes", "moe_strerror", "moe_workspace_init",
@@ -35,6 +36,8 @@ EXPORTS = [
     "moe_pool_debug_fail_copies", "moe_prefill_plan_get", "moe_debug_force_prefill_plan",
     "moe_dense_workspace_bytes", "moe_linear_forward", "moe_linear_backward", "moe_gated_forward",
     "moe_gated_backward", "moe_debug_force_dense_plan",
+    "moe_rows_workspace_bytes", "moe_dispatch_forward", "moe_dispatch_backward", "moe_combine_forward",
+    "moe_combine_backward",
 ]
 
 
@@ -70,6 +73,12 @@ class moe_dense_dims(ctypes.Structure):
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_SIGMOID = range(6)
 MOE_DENSE_MAX_WIDTH, MOE_DENSE_MAX_LD, MOE_DENSE_MAX_TOKENS, MOE_DENSE_ROW_TOKENS = 1 << 20, 1 << 22, 1 << 24, 16
 
+class moe_rows_dims(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("top_k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+MOE_ROWS_MAX = 1 << 28
+
 MOE_GEMM_PIPE128, MOE_GEMM_PIPE64_DEEP, MOE_GEMM_GENERAL = 0, 1, 2
 
 
@@ -92,6 +101,7 @@ _W = ctypes.POINTER(moe_layer_weights)
 _B = ctypes.POINTER(moe_doorbell)
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _DD = ctypes.POINTER(moe_dense_dims)
+_RD = ctypes.POINTER(moe_rows_dims)
 _L = ctypes.c_int64
 
 _sig = {
@@ -130,6 +140,11 @@ _sig = {
                                          _P]),
     "moe_gated_backward": (ctypes.c_int, [_DD, _P, _L, _I, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P,
                                           _L, _P, _P, _P, _SZ, _P]),
+    "moe_rows_workspace_bytes": (_SZ, [_RD, _I]),
+    "moe_dispatch_forward": (ctypes.c_int, [_RD, _P, _L, _I, _P, _I, _P, _L, _P, _P, _SZ, _P]),
+    "moe_dispatch_backward": (ctypes.c_int, [_RD, _P, _L, _I, _P, _I, _P, _L, _P, _L, _I, _P, _SZ, _P]),
+    "moe_combine_forward": (ctypes.c_int, [_RD, _P, _L, _I, _P, _P, _I, _P, _L, _P, _L, _I, _P, _SZ, _P]),
+    "moe_combine_backward": (ctypes.c_int, [_RD, _P, _L, _I, _I, _P, _P, _I, _P, _P, _L, _P, _L, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -171,7 +186,7 @@ def dtype_code(t) -> int:
         return MOE_F32
     if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
         return MOE_BF16
-    if t.dtype == torch.float16:  # the dense operators' operands only; the layer's calls refuse it
+    if t.dtype == torch.float16:  # of the dense operators and those after them only; the layer's calls refuse it
         return MOE_F16
     raise TypeError(f"unsupported activation dtype {t.dtype}")
 
@@ -396,6 +411,81 @@ def moe_gated_backward(d: moe_dense_dims, x, n_tokens: int, w_gate, w_up, gate, 
         *_opt_mat(dw_up, N, K, ty, dev, "moe_gated_backward, dw_up"),
         _opt_vec(dgate_bias, N, ty, dev, "moe_gated_backward, dgate_bias"),
         _opt_vec(dup_bias, N, ty, dev, "moe_gated_backward, dup_bias")))
+
+
+# ---------------------------------------------------------------------------------------------
+# rows by expert
+# ---------------------------------------------------------------------------------------------
+
+def rows_dims(width: int, top_k: int, dtype: int) -> moe_rows_dims:
+    return moe_rows_dims(int(width), int(top_k), int(dtype))
+
+
+def moe_rows_workspace_bytes(d: moe_rows_dims, max_tokens: int) -> int:
+    return _lib.moe_rows_workspace_bytes(ctypes.byref(d), max_tokens)
+
+
+def _array(t, shape, dtype, device, where: str):
+    """Address of a contiguous array of this shape (a [T][k] one may come flat)."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or (
+            t.shape != shape and (t.dim() != 1 or t.shape[0] != math.prod(shape))):
+        raise MoeError(MOE_EINVAL, where)
+    return t.data_ptr()
+
+
+def _rows(t, cols: int, types, device, where: str):
+    """(address, row stride, rows) of a row-major matrix that says itself how many rows it has."""
+    if t.dim() != 2:
+        raise MoeError(MOE_EINVAL, where)
+    return (*_mat(t, t.shape[0], cols, types, device, where), t.shape[0])
+
+
+def moe_dispatch_forward(d: moe_rows_dims, x, n_tokens: int, perm, xs, inv, ws, stream=None):
+    """``xs[r] = x[perm[r] // k]`` (zero where ``perm[r]`` is negative); ``inv`` receives each pair's row, or -1."""
+    H, T, dev, ty, P = d.width, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), xs.shape[0]
+    _dense_call(_lib.moe_dispatch_forward, "moe_dispatch_forward", d, dev, ws, stream, (
+        *_mat(x, T, H, ty, dev, "moe_dispatch_forward, x"), T,
+        _array(perm, (P,), torch.int32, dev, "moe_dispatch_forward, perm"), P,
+        *_mat(xs, P, H, ty, dev, "moe_dispatch_forward, xs"),
+        _array(inv, (T, d.top_k), torch.int32, dev, "moe_dispatch_forward, inv")))
+
+
+def moe_dispatch_backward(d: moe_rows_dims, dxs, inv, n_tokens: int, dx, ws, residual=None, stream=None):
+    """``dx[t] = sum_j dxs[inv[t][j]] + residual[t]``; dx and residual in the rows' type or float32."""
+    H, T, dev, ty, xd = d.width, n_tokens, dxs.device, _DENSE_TYPES.get(d.dtype, ()), dtype_code(dx)
+    xt = _DENSE_TYPES[xd]
+    _dense_call(_lib.moe_dispatch_backward, "moe_dispatch_backward", d, dev, ws, stream, (
+        *_rows(dxs, H, ty, dev, "moe_dispatch_backward, dxs"),
+        _array(inv, (T, d.top_k), torch.int32, dev, "moe_dispatch_backward, inv"), T,
+        *_opt_mat(residual, T, H, xt, dev, "moe_dispatch_backward, residual"),
+        *_mat(dx, T, H, xt, dev, "moe_dispatch_backward, dx"), xd))
+
+
+def moe_combine_forward(d: moe_rows_dims, ys, inv, topk_w, n_tokens: int, y, ws, residual=None, stream=None):
+    """``y[t] = sum_j topk_w[t][j] ys[inv[t][j]] + residual[t]``; y and residual in the rows' type or float32."""
+    H, T, dev, ty, yd = d.width, n_tokens, ys.device, _DENSE_TYPES.get(d.dtype, ()), dtype_code(y)
+    yt = _DENSE_TYPES[yd]
+    _dense_call(_lib.moe_combine_forward, "moe_combine_forward", d, dev, ws, stream, (
+        *_rows(ys, H, ty, dev, "moe_combine_forward, ys"),
+        _array(inv, (T, d.top_k), torch.int32, dev, "moe_combine_forward, inv"),
+        _array(topk_w, (T, d.top_k), torch.float32, dev, "moe_combine_forward, topk_w"), T,
+        *_opt_mat(residual, T, H, yt, dev, "moe_combine_forward, residual"),
+        *_mat(y, T, H, yt, dev, "moe_combine_forward, y"), yd))
+
+
+def moe_combine_backward(d: moe_rows_dims, dy, n_tokens: int, perm, inv, topk_w, ws, ys=None, dys=None, dtopk_w=None,
+                         stream=None):
+    """Gradients of moe_combine_forward from ``dy`` (the rows' type or float32); None: not computed.  ``dtopk_w`` needs
+    the forward pass's ``ys``."""
+    H, T, dev, ty, yd, P = d.width, n_tokens, dy.device, _DENSE_TYPES.get(d.dtype, ()), dtype_code(dy), perm.shape[0]
+    _dense_call(_lib.moe_combine_backward, "moe_combine_backward", d, dev, ws, stream, (
+        *_mat(dy, T, H, _DENSE_TYPES[yd], dev, "moe_combine_backward, dy"), yd, T,
+        _array(perm, (P,), torch.int32, dev, "moe_combine_backward, perm"),
+        _array(inv, (T, d.top_k), torch.int32, dev, "moe_combine_backward, inv"), P,
+        _array(topk_w, (T, d.top_k), torch.float32, dev, "moe_combine_backward, topk_w"),
+        *_opt_mat(ys, P, H, ty, dev, "moe_combine_backward, ys"),
+        *_opt_mat(dys, P, H, ty, dev, "moe_combine_backward, dys"),
+        None if dtopk_w is None else _array(dtopk_w, (T, d.top_k), torch.float32, dev, "moe_combine_backward, dtopk_w")))
 
 
 def raw(name: str):
