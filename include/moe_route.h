@@ -98,7 +98,7 @@ enum moe_device_error {
   MOE_DERR_RANGE = 64,        /* prefill: an activation, SwiGLU output or weighted expert row
                                  beyond the fp16 range (|v| > 65504) or not finite */
   MOE_DERR_ROWS = 128         /* rows by expert: a pair out of range or in two rows, a row out of
-                                 range, perm and inv at odds */
+                                 range, perm and inv at odds, offsets that descend or leave the rows */
 };
 
 /* Largest token count of a decode call.  The pages' decode batches: concurrent streams (Basalt
@@ -626,6 +626,69 @@ MOE_API int moe_combine_backward(const moe_rows_dims* dims, const void* dy, int6
                                  int32_t n_tokens, const int32_t* perm, const int32_t* inv, int32_t n_rows,
                                  const float* topk_w, const void* ys_or_null, int64_t ld_ys, void* dys_or_null,
                                  int64_t ld_dys, float* dtopk_w_or_null, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Experts' products with 16-bit weights -----------------------------------------------------
+ * What runs between moe_dispatch_forward and moe_combine_forward: expert e's matrices on its rows offsets[e] ..
+ * offsets[e+1] - 1 of the rows laid out by expert (moe_group_tokens' offsets, or a caller's own), and the gradients:
+ *
+ *   linear  y_r = W_e x_r                              dx_r = W_e^T dy_r               dW_e = sum_r dy_r x_r^T
+ *   gated   g_r = Wg_e x_r, u_r = Wu_e x_r             h_r = act(g_r) * u_r
+ *           dg = dh * u * act'(g), du = dh * act(g)    dx_r = Wg_e^T dg_r + Wu_e^T du_r
+ *           dWg_e = sum_r dg_r x_r^T                   dWu_e = sum_r du_r x_r^T
+ *
+ * Conventions, beyond those of the dense operators (types, strides, alignment, rounding, saved infinities, overlap):
+ *   - weights and their gradients are [E][n_out][n_in]: row stride ld, matrices `stride` elements apart (both matrices
+ *     of a gated block alike; they may be the halves of one [E][2 n_out][n_in] tensor).
+ *   - offsets [E+1] lives on the device; no call waits for it.  An expert may have any number of rows, none among them:
+ *     its dW is then zero.  Rows before offsets[0] and from offsets[E] on belong to nobody: no result of theirs is
+ *     written.  Padding rows of a group are rows like any other.  The backward passes make dz of every one of the n_rows
+ *     rows in the workspace, but use those of groups only.
+ *   - Offsets that descend or leave 0 .. n_rows set MOE_DERR_ROWS: they are clamped, no access leaves the arrays, the
+ *     results are invalid.
+ *   - Sums are fp32 in an order that depends on the shapes (n_rows among them) and an expert's rows, not on where its rows lie.
+ *   - 1 <= n_experts <= 1024; 1 <= n_rows <= MOE_ROWS_MAX.  The linear takes MOE_ACT_NONE only.
+ *   - moe_debug_force_dense_plan's kernel holds here too.
+ *   - `ws`: moe_experts_workspace_bytes(dims, n_rows, backward) bytes.
+ */
+typedef struct moe_experts_dims {
+  int32_t n_experts;
+  int32_t n_in;   /* row length of xs and of every weight */
+  int32_t n_out;  /* rows of each weight; row length of ys, g, u, h */
+  int32_t dtype;  /* MOE_BF16 or MOE_F16 */
+  int32_t act;    /* moe_act; linear: MOE_ACT_NONE */
+} moe_experts_dims;
+
+/* Workspace bytes that the forward calls (backward = 0) or all calls (backward = 1) need for up to `max_rows` rows;
+ * 0 if dims are invalid or max_rows out of range. */
+MOE_API size_t moe_experts_workspace_bytes(const moe_experts_dims* dims, int32_t max_rows, int32_t backward);
+
+/* ys [n_rows][n_out] = each row of xs [n_rows][n_in] through its expert's matrix. */
+MOE_API int moe_experts_linear_forward(const moe_experts_dims* dims, const void* xs, int64_t ld_xs, int32_t n_rows,
+                                       const int32_t* offsets, const void* w, int64_t ldw, int64_t w_stride, void* ys,
+                                       int64_t ld_ys, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of moe_experts_linear_forward from dys [n_rows][n_out]; dxs [n_rows][n_in], dw: NULL = not wanted (not both). */
+MOE_API int moe_experts_linear_backward(const moe_experts_dims* dims, const void* xs, int64_t ld_xs, int32_t n_rows,
+                                        const int32_t* offsets, const void* w, int64_t ldw, int64_t w_stride,
+                                        const void* dys, int64_t ld_dys, void* dxs_or_null, int64_t ld_dxs,
+                                        void* dw_or_null, int64_t ld_dw, int64_t dw_stride, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/* h [n_rows][n_out] = the gated block of each row's expert, in one pass.  gate / up [n_rows][n_out] (one stride,
+ * ld_saved) or NULL receive g and u for the backward pass (both or neither). */
+MOE_API int moe_experts_gated_forward(const moe_experts_dims* dims, const void* xs, int64_t ld_xs, int32_t n_rows,
+                                      const int32_t* offsets, const void* w_gate, const void* w_up, int64_t ldw,
+                                      int64_t w_stride, void* h, int64_t ldh, void* gate_or_null, void* up_or_null,
+                                      int64_t ld_saved, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of moe_experts_gated_forward from dh [n_rows][n_out] and the saved gate and up; dw_gate and dw_up share
+ * ld_dw and dw_stride; every output NULL = not wanted (not all). */
+MOE_API int moe_experts_gated_backward(const moe_experts_dims* dims, const void* xs, int64_t ld_xs, int32_t n_rows,
+                                       const int32_t* offsets, const void* w_gate, const void* w_up, int64_t ldw,
+                                       int64_t w_stride, const void* gate, const void* up, int64_t ld_saved,
+                                       const void* dh, int64_t ld_dh, void* dxs_or_null, int64_t ld_dxs,
+                                       void* dw_gate_or_null, void* dw_up_or_null, int64_t ld_dw, int64_t dw_stride,
+                                       void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

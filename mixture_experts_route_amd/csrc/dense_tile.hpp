@@ -343,13 +343,12 @@ struct AnyLoad {
 // LDS buffers, so that any address, stride and length works. Bound by the latency and rate of unaligned loads:
 // 0.9 us a step with 64-square tiles, 1.5 with 128 (4096 x 4095 outputs of 4095 terms 216 us; through copies
 // with whole rows 142 us).
+constexpr int any_lds(int f) { return 2 * 4 * 32 * f * kStepR; }  // elements
 template <typename T, int OA, int OB, int KIND, int F>
-__global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
+MOE_DEV void any_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   constexpr int H = 32 * F, kBuf = 4 * H * kStepR;  // elements: A0 A1 B0 B1
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2 * kBuf];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wi = wave >> 1, wj = wave & 1;
-  const TileIndex x = tile_index<false>(a, blockIdx.x, gridDim.x);
   constexpr int JT = KIND == kEpiGated ? H : 2 * H;  // output columns per tile
   const int64_t i0 = (int64_t)x.ti * 2 * H, j0 = (int64_t)x.tj * JT;
   const int steps = (a.R + kStepR - 1) / kStepR;
@@ -440,6 +439,12 @@ __global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
   __syncthreads();
   finish_blocks<T, KIND>(a, x, i0 + wi * 16 * F, H, j0 + wj * 16 * F, H, acc,
                          (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * F * F * 256, lane);
+}
+
+template <typename T, int OA, int OB, int KIND, int F>
+__global__ __launch_bounds__(256, 2) void k_tile_any(TileArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[any_lds(F)];
+  any_tile<T, OA, OB, KIND, F>(a, tile_index<false>(a, blockIdx.x, gridDim.x), lds);
 }
 
 // ---- 16-byte aligned operands ------------------------------------------------------------------------
@@ -571,7 +576,7 @@ struct HalfStream {
 // 128-square tiles 15 us. While a step's MFMAs run from registers the next step's fragments are read.
 constexpr int kDeepStages = 5, kDeepStageBytes = (64 + 2 * 32) * kStepR * 2;
 template <typename T, int OA, int OB, int KIND>
-MOE_DEV void deep_tile(const TileArgs& a, uint32_t id, uint32_t ids, uint16_t* lds) {
+MOE_DEV void deep_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   constexpr int STAGES = kDeepStages, W = 4, HI = 64, HJ = 32;
   constexpr int kBytes = kDeepStageBytes;  // A, B0, B1
   typedef typename Operand<T>::v8 v8;
@@ -580,7 +585,6 @@ MOE_DEV void deep_tile(const TileArgs& a, uint32_t id, uint32_t ids, uint16_t* l
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave >> 1, wj = wave & 1;
-  const TileIndex x = tile_index<false>(a, id, ids);
   constexpr int JT = KIND == kEpiGated ? HJ : 2 * HJ;
   const int64_t i0 = (int64_t)x.ti * HI, j0 = (int64_t)x.tj * JT;
 
@@ -665,7 +669,7 @@ MOE_DEV void deep_tile(const TileArgs& a, uint32_t id, uint32_t ids, uint16_t* l
 template <typename T, int OA, int OB, int KIND>
 __global__ __launch_bounds__(256, 2) void k_tile_deep(TileArgs a) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[kDeepStages * kDeepStageBytes / 2];
-  deep_tile<T, OA, OB, KIND>(a, blockIdx.x, gridDim.x, lds);
+  deep_tile<T, OA, OB, KIND>(a, tile_index<false>(a, blockIdx.x, gridDim.x), lds);
 }
 
 // A small backward pass in one launch: dx's tiles, dW's tiles, then the bias gradients' columns. Alone each of
@@ -676,12 +680,12 @@ __global__ __launch_bounds__(256, 2) void k_backward_small(TileArgs dx, TileArgs
   __shared__ __attribute__((aligned(1024))) uint16_t lds[kDeepStages * kDeepStageBytes / 2];
   uint32_t id = blockIdx.x;
   if (id < n_dx) {
-    deep_tile<T, kRows, kCols, kEpiStore>(dx, id, n_dx, lds);
+    deep_tile<T, kRows, kCols, kEpiStore>(dx, tile_index<false>(dx, id, n_dx), lds);
     return;
   }
   id -= n_dx;
   if (id < n_dw) {
-    deep_tile<T, kCols, kCols, kEpiStore>(dw, id, n_dw, lds);
+    deep_tile<T, kCols, kCols, kEpiStore>(dw, tile_index<false>(dw, id, n_dw), lds);
     return;
   }
   bias_sum_block<T>(db, id - n_dw, (float*)lds);
@@ -706,18 +710,17 @@ __global__ __launch_bounds__(256, 2) void k_backward_small(TileArgs dx, TileArgs
 // tiles for the first copies and the stores. 8192^3 bf16: forward 808-910 us (1,210-1,360 TFLOP/s), dx 824, dW
 // 810 us. 128-square tiles, two workgroups per CU, where 256-square ones would leave CUs idle: 4096 x 2048
 // outputs of 8192 terms 134 against 181 us.
+constexpr int big_lds(int wi, int wj, int fi, int fj) { return 2 * 2 * 16 * (wi * fi + wj * fj) * kStepR; }  // elements
 template <typename T, int OA, int OB, int KIND, int WI, int WJ, int FI, int FJ>
-__global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
+MOE_DEV void big_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   constexpr int W = WI * WJ, HI = WI * FI * 16, HJ = WJ * FJ * 16;
   constexpr int kBuf = 2 * (HI + HJ) * kStepR;  // elements of one buffer: A0 A1 B0 B1
   typedef typename Operand<T>::v8 v8;
   constexpr int DA = OperandCopy<OA, HI, W>::kCopies, DB = OperandCopy<OB, HJ, W>::kCopies;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2 * kBuf];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave / WJ, wj = wave % WJ;
-  const TileIndex x = tile_index<true>(a, blockIdx.x, gridDim.x);
   constexpr int JT = KIND == kEpiGated ? HJ : 2 * HJ;
   const int64_t i0 = (int64_t)x.ti * 2 * HI, j0 = (int64_t)x.tj * JT;
 
@@ -832,6 +835,12 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
 
   finish_blocks<T, KIND>(a, x, i0 + wi * FI * 16, HI, j0 + wj * FJ * 16, HJ, acc,
                          (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * FI * FJ * 256, lane);
+}
+
+template <typename T, int OA, int OB, int KIND, int WI, int WJ, int FI, int FJ>
+__global__ __launch_bounds__(64 * WI * WJ, 2) void k_tile(TileArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[big_lds(WI, WJ, FI, FJ)];
+  big_tile<T, OA, OB, KIND, WI, WJ, FI, FJ>(a, tile_index<true>(a, blockIdx.x, gridDim.x), lds);
 }
 
 // A line's chunks lie on 16-byte addresses. kRows: and end with the reduction (or with zeros past it: len

@@ -38,6 +38,8 @@ EXPORTS = [
     "moe_gated_backward", "moe_debug_force_dense_plan",
     "moe_rows_workspace_bytes", "moe_dispatch_forward", "moe_dispatch_backward", "moe_combine_forward",
     "moe_combine_backward",
+    "moe_experts_workspace_bytes", "moe_experts_linear_forward", "moe_experts_linear_backward",
+    "moe_experts_gated_forward", "moe_experts_gated_backward",
 ]
 
 
@@ -73,8 +75,14 @@ class moe_dense_dims(ctypes.Structure):
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_SIGMOID = range(6)
 MOE_DENSE_MAX_WIDTH, MOE_DENSE_MAX_LD, MOE_DENSE_MAX_TOKENS, MOE_DENSE_ROW_TOKENS = 1 << 20, 1 << 22, 1 << 24, 16
 
+
 class moe_rows_dims(ctypes.Structure):
     _fields_ = [("width", ctypes.c_int32), ("top_k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class moe_experts_dims(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
 MOE_ROWS_MAX = 1 << 28
@@ -102,6 +110,7 @@ _B = ctypes.POINTER(moe_doorbell)
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _DD = ctypes.POINTER(moe_dense_dims)
 _RD = ctypes.POINTER(moe_rows_dims)
+_ED = ctypes.POINTER(moe_experts_dims)
 _L = ctypes.c_int64
 
 _sig = {
@@ -145,6 +154,13 @@ _sig = {
     "moe_dispatch_backward": (ctypes.c_int, [_RD, _P, _L, _I, _P, _I, _P, _L, _P, _L, _I, _P, _SZ, _P]),
     "moe_combine_forward": (ctypes.c_int, [_RD, _P, _L, _I, _P, _P, _I, _P, _L, _P, _L, _I, _P, _SZ, _P]),
     "moe_combine_backward": (ctypes.c_int, [_RD, _P, _L, _I, _I, _P, _P, _I, _P, _P, _L, _P, _L, _P, _P, _SZ, _P]),
+    "moe_experts_workspace_bytes": (_SZ, [_ED, _I, _I]),
+    "moe_experts_linear_forward": (ctypes.c_int, [_ED, _P, _L, _I, _P, _P, _L, _L, _P, _L, _P, _SZ, _P]),
+    "moe_experts_linear_backward": (ctypes.c_int, [_ED, _P, _L, _I, _P, _P, _L, _L, _P, _L, _P, _L, _P, _L, _L, _P, _SZ,
+                                                   _P]),
+    "moe_experts_gated_forward": (ctypes.c_int, [_ED, _P, _L, _I, _P, _P, _P, _L, _L, _P, _L, _P, _P, _L, _P, _SZ, _P]),
+    "moe_experts_gated_backward": (ctypes.c_int, [_ED, _P, _L, _I, _P, _P, _P, _L, _L, _P, _P, _L, _P, _L, _P, _L, _P, _P,
+                                                  _L, _L, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -486,6 +502,93 @@ def moe_combine_backward(d: moe_rows_dims, dy, n_tokens: int, perm, inv, topk_w,
         *_opt_mat(ys, P, H, ty, dev, "moe_combine_backward, ys"),
         *_opt_mat(dys, P, H, ty, dev, "moe_combine_backward, dys"),
         None if dtopk_w is None else _array(dtopk_w, (T, d.top_k), torch.float32, dev, "moe_combine_backward, dtopk_w")))
+
+
+# ---------------------------------------------------------------------------------------------
+# experts' products with 16-bit weights
+# ---------------------------------------------------------------------------------------------
+
+def experts_dims(n_experts: int, n_in: int, n_out: int, dtype: int, act: int = MOE_ACT_NONE) -> moe_experts_dims:
+    return moe_experts_dims(int(n_experts), int(n_in), int(n_out), int(dtype), int(act))
+
+
+def moe_experts_workspace_bytes(d: moe_experts_dims, max_rows: int, backward: bool = False) -> int:
+    return _lib.moe_experts_workspace_bytes(ctypes.byref(d), max_rows, int(backward))
+
+
+def _stack(t, d: moe_experts_dims, types, device, where: str):
+    """(address, row stride, matrix stride) of an [E][n_out][n_in] tensor; (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    E, R, K = d.n_experts, d.n_out, d.n_in
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != E or shape[1] != R or shape[2] != K or t.dtype not in types or t.device != device:
+        raise MoeError(MOE_EINVAL, where)
+    each, ld, step = t.stride()
+    if step != 1 and K > 1:
+        raise MoeError(MOE_EINVAL, where)
+    ld = ld if R > 1 else K
+    return t.data_ptr(), ld, each if E > 1 else (R - 1) * ld + K
+
+
+def _stacks(a, b, d: moe_experts_dims, types, device, where: str):
+    """(address, address, row stride, matrix stride) of two such tensors of equal strides; either may be None."""
+    pa, la, sa = _stack(a, d, types, device, where)
+    pb, lb, sb = _stack(b, d, types, device, where)
+    if a is not None and b is not None and (la, sa) != (lb, sb):
+        raise MoeError(MOE_EINVAL, where)
+    return pa, pb, la or lb, sa or sb
+
+
+def _pair(a, b, rows: int, cols: int, types, device, where: str):
+    """(address, address, row stride) of two matrices of equal stride, or of none."""
+    pa, la = _opt_mat(a, rows, cols, types, device, where)
+    pb, lb = _opt_mat(b, rows, cols, types, device, where)
+    if a is not None and b is not None and la != lb:
+        raise MoeError(MOE_EINVAL, where)
+    return pa, pb, la or lb
+
+
+def moe_experts_linear_forward(d: moe_experts_dims, xs, offsets, w, ys, ws, stream=None):
+    """``ys[r] = w[e] xs[r]`` for the rows ``offsets[e] .. offsets[e+1]-1`` of every expert e."""
+    dev, ty, n = xs.device, _DENSE_TYPES.get(d.dtype, ()), "moe_experts_linear_forward, "
+    px, ldx, P = _rows(xs, d.n_in, ty, dev, n + "xs")
+    _dense_call(_lib.moe_experts_linear_forward, "moe_experts_linear_forward", d, dev, ws, stream, (
+        px, ldx, P, _array(offsets, (d.n_experts + 1,), torch.int32, dev, n + "offsets"),
+        *_stack(w, d, ty, dev, n + "w"), *_mat(ys, P, d.n_out, ty, dev, n + "ys")))
+
+
+def moe_experts_linear_backward(d: moe_experts_dims, xs, offsets, w, dys, ws, dx=None, dw=None, stream=None):
+    """Gradients of moe_experts_linear_forward from ``dys``; None: not computed."""
+    dev, ty, n = xs.device, _DENSE_TYPES.get(d.dtype, ()), "moe_experts_linear_backward, "
+    px, ldx, P = _rows(xs, d.n_in, ty, dev, n + "xs")
+    _dense_call(_lib.moe_experts_linear_backward, "moe_experts_linear_backward", d, dev, ws, stream, (
+        px, ldx, P, _array(offsets, (d.n_experts + 1,), torch.int32, dev, n + "offsets"),
+        *_stack(w, d, ty, dev, n + "w"), *_mat(dys, P, d.n_out, ty, dev, n + "dys"),
+        *_opt_mat(dx, P, d.n_in, ty, dev, n + "dx"), *_stack(dw, d, ty, dev, n + "dw")))
+
+
+def moe_experts_gated_forward(d: moe_experts_dims, xs, offsets, w_gate, w_up, h, ws, gate=None, up=None, stream=None):
+    """``h[r] = act(w_gate[e] xs[r]) * (w_up[e] xs[r])``; ``gate`` and ``up`` receive the two factors for the backward
+    pass.  The two weights share their strides, and so do gate and up."""
+    dev, ty, n = xs.device, _DENSE_TYPES.get(d.dtype, ()), "moe_experts_gated_forward, "
+    px, ldx, P = _rows(xs, d.n_in, ty, dev, n + "xs")
+    _dense_call(_lib.moe_experts_gated_forward, "moe_experts_gated_forward", d, dev, ws, stream, (
+        px, ldx, P, _array(offsets, (d.n_experts + 1,), torch.int32, dev, n + "offsets"),
+        *_stacks(w_gate, w_up, d, ty, dev, n + "w_gate, w_up"), *_mat(h, P, d.n_out, ty, dev, n + "h"),
+        *_pair(gate, up, P, d.n_out, ty, dev, n + "gate, up")))
+
+
+def moe_experts_gated_backward(d: moe_experts_dims, xs, offsets, w_gate, w_up, gate, up, dh, ws, dx=None, dw_gate=None,
+                               dw_up=None, stream=None):
+    """Gradients of moe_experts_gated_forward from ``dh`` and the saved ``gate`` and ``up``; None: not computed."""
+    dev, ty, n = xs.device, _DENSE_TYPES.get(d.dtype, ()), "moe_experts_gated_backward, "
+    px, ldx, P = _rows(xs, d.n_in, ty, dev, n + "xs")
+    _dense_call(_lib.moe_experts_gated_backward, "moe_experts_gated_backward", d, dev, ws, stream, (
+        px, ldx, P, _array(offsets, (d.n_experts + 1,), torch.int32, dev, n + "offsets"),
+        *_stacks(w_gate, w_up, d, ty, dev, n + "w_gate, w_up"), *_pair(gate, up, P, d.n_out, ty, dev, n + "gate, up"),
+        *_mat(dh, P, d.n_out, ty, dev, n + "dh"), *_opt_mat(dx, P, d.n_in, ty, dev, n + "dx"),
+        *_stacks(dw_gate, dw_up, d, ty, dev, n + "dw_gate, dw_up")))
 
 
 def raw(name: str):
