@@ -97,6 +97,7 @@ enum moe_device_error {
   MOE_DERR_DUP_ID = 32,       /* a token's top-k list names one expert twice */
   MOE_DERR_RANGE = 64,        /* prefill: an activation, SwiGLU output or weighted expert row
                                  beyond the fp16 range (|v| > 65504) or not finite */
+  MOE_DERR_TARGET = 256,      /* loss: a target outside [0, vocab) that is not `ignore` */
   MOE_DERR_ROWS = 128         /* rows by expert: a pair out of range or in two rows, a row out of
                                  range, perm and inv at odds, offsets that descend or leave the rows */
 };
@@ -689,6 +690,56 @@ MOE_API int moe_experts_gated_backward(const moe_experts_dims* dims, const void*
                                        const void* dh, int64_t ld_dh, void* dxs_or_null, int64_t ld_dxs,
                                        void* dw_gate_or_null, void* dw_up_or_null, int64_t ld_dw, int64_t dw_stride,
                                        void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Loss over an output head ------------------------------------------------------------------
+ * Softmax cross entropy of z = x W^T over a vocabulary, with its gradient, in pieces of the vocabulary: the logits are
+ * never kept (a moe_linear_forward of the same sizes writes them; this is its training form).
+ *
+ *   lse_t = log sum_v exp(z_tv)        loss_t = lse_t - z_t,target
+ *   dz_tv = dloss_t (exp(z_tv - lse_t) - [v = target])      dx = dz W      dW = dz^T x
+ *
+ * Conventions, beyond those of the dense operators (types, strides, alignment, rounding, overlap):
+ *   - targets [n_tokens] int32.  A token whose target is `ignore` has loss and lse 0 and no gradient (x may hold
+ *     anything finite).  Any other target outside [0, vocab) sets MOE_DERR_TARGET: its loss and lse are NaN, it adds
+ *     nothing to the gradients.
+ *   - loss, lse, dloss [n_tokens] fp32.  Reductions over the tokens are the caller's: dloss is 1 / count for their mean, a
+ *     token's weight for a weighted one.
+ *   - Logits are fp32 sums and are not rounded.  loss is formed from what the other columns add to the target's, so
+ *     that a small loss keeps its relative precision; the gradient takes both saved values for the same reason
+ *     (exp(z - lse) - 1 at the target is expm1(-loss)).
+ *   - The backward pass computes the logits again and rounds dz to dims->dtype before the products, in fp16 after a scaling
+ *     by a power of two that brings the largest |dloss| to 2^11 (undone in fp32): a token whose dloss is less than 2^-20 of the
+ *     largest loses precision there.  A result past 65504 is an infinity, one below 2^-25 zero: scale dloss.
+ *   - An infinite logit gives the limits: loss 0 where it is the target's alone, else infinite; NaN stays in its token.
+ *   - Sums are in a fixed order: equal calls give equal bits.
+ *   - 1 <= n_in, vocab <= MOE_DENSE_MAX_WIDTH; 1 <= n_tokens <= MOE_LOSS_MAX_TOKENS (beyond: MOE_EUNSUPPORTED).
+ *   - moe_debug_force_dense_plan holds here too.
+ *   - `ws`: moe_loss_workspace_bytes(dims, n_tokens, backward) bytes: for the backward pass about 256 MiB of dz and, with
+ *     more than one piece, dx in fp32.
+ */
+#define MOE_LOSS_MAX_TOKENS (1 << 20)
+
+typedef struct moe_loss_dims {
+  int32_t n_in;    /* row length of x and W */
+  int32_t vocab;   /* rows of W */
+  int32_t dtype;   /* of x, W, dx, dW: MOE_BF16 or MOE_F16 */
+  int32_t ignore;  /* target of tokens that are left out: any value, inside [0, vocab) too (a padding token's id) */
+} moe_loss_dims;
+
+/* Workspace bytes that the forward call (backward = 0) or both calls (backward = 1) need for up to `max_tokens`
+ * tokens; 0 if dims are invalid or max_tokens out of range. */
+MOE_API size_t moe_loss_workspace_bytes(const moe_loss_dims* dims, int32_t max_tokens, int32_t backward);
+
+/* loss and lse [n_tokens] of x [n_tokens][n_in] against w [vocab][n_in]. */
+MOE_API int moe_loss_forward(const moe_loss_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
+                             int64_t ldw, const int32_t* targets, float* loss, float* lse, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* dx [n_tokens][n_in] and dw [vocab][n_in] (NULL = not wanted, not both) from moe_loss_forward's loss and lse. */
+MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
+                              int64_t ldw, const int32_t* targets, const float* loss, const float* lse,
+                              const float* dloss, void* dx_or_null, int64_t ld_dx, void* dw_or_null, int64_t ld_dw,
+                              void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

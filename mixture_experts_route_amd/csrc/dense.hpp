@@ -156,7 +156,22 @@ MOE_DEV void act_both_far(int act, float z, float& v, float& d) {
 MOE_DEV float times_far(float p, float f) { return p == 0.0f && f == f ? p : p * f; }
 
 // ---- epilogues ------------------------------------------------------------------------------------
-enum DenseEpiKind { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2 };
+enum DenseEpiKind { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2,
+                    kEpiLoss = 3,    // logits: a row's maximum and sum of exponentials over the tile's columns
+                    kEpiLossDz = 4,  // logits: their gradient, from the row's saved loss and lse
+                    kEpiSum = 5 };   // sums onto earlier ones, scaled
+
+// The loss's epilogues (moe_loss_*); the arrays are indexed by the product's rows.
+struct LossEpi {
+  const int32_t* targets;
+  const float *loss, *lse, *dloss;  // kEpiLossDz
+  float2* part;                     // kEpiLoss: [tiles_j][M], the target's column left out
+  float* zt;                        // kEpiLoss: [M], the target's logit
+  const float* scale;               // kEpiLossDz: dz's factor; kEpiSum: the results' (NULL: 1)
+  const float* acc;                 // kEpiSum: the earlier sums, row stride DenseEpi::ldr (NULL: none)
+  int32_t* ctrl;
+  int32_t col0, vocab, ignore;      // the product's first column, and all of them
+};
 
 struct DenseEpi {
   void* y[2];          // the output (kEpiStore: one per batch)
@@ -171,6 +186,7 @@ struct DenseEpi {
   int32_t stream;      // outputs larger than the L2s: stored with the non-temporal hint (launch_tile), so that
                        // they leave the operands in the caches (4096 tokens and outputs: 512 inputs 28.6 ->
                        // 24.9 us, 4096 inputs 110.8 -> 106.3 us)
+  LossEpi loss;
 };
 
 // 8 consecutive elements of a row as fp32, or the first n of them. Global accesses of 16 bytes need only the
@@ -216,6 +232,21 @@ MOE_DEV void finish8(const DenseEpi& e, int batch, int64_t i, int j, int n, floa
     return;
   }
   float t[8];
+  if constexpr (KIND == kEpiSum) {
+    if (e.loss.acc) {
+      load8<float>(e.loss.acc, i * e.ldr + j, n, t);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s0[c] += t[c];
+    }
+    if (e.loss.scale) {
+      const float f = *e.loss.scale;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s0[c] *= f;
+    }
+    if (e.y_f32) store8<float>(e.y[0], i * e.ldy[0] + j, n, s0, false);
+    else store8<T>(e.y[0], i * e.ldy[0] + j, n, s0, stream);
+    return;
+  }
   if (e.bias[0]) {
     load8<T>(e.bias[0], j, n, t);
 #pragma unroll

@@ -202,6 +202,7 @@ static void start_finish(const TileArgs& a, int kind, hipStream_t st) {
   const dim3 grid((uint32_t)((threads + 255) / 256)), block(256);
   if (kind == kEpiGated) k_finish<T, kEpiGated><<<grid, block, 0, st>>>(a);
   else if (kind == kEpiLinear) k_finish<T, kEpiLinear><<<grid, block, 0, st>>>(a);
+  else if (kind == kEpiSum) k_finish<T, kEpiSum><<<grid, block, 0, st>>>(a);
   else k_finish<T, kEpiStore><<<grid, block, 0, st>>>(a);
 }
 

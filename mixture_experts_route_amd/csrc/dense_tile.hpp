@@ -241,7 +241,38 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
       return;
     }
   }
-  const bool plain = KIND == kEpiStore || (KIND == kEpiLinear && !e.bias[0] && !e.pre[0] && !e.res && !e.y_f32 && e.act == MOE_ACT_NONE);
+  if constexpr (KIND == kEpiLossDz) {
+    const LossEpi& l = e.loss;
+    const float scale = l.scale ? *l.scale : 1.0f;
+#pragma unroll
+    for (int h = 0; h < NI; ++h) {
+      float4v v[2][FI][FJ];
+#pragma unroll
+      for (int f = 0; f < FI; ++f) {
+        const int64_t i = i0 + h * di + f * 16 + (lane & 15);
+        const int64_t row = i < a.M ? i : a.M - 1;
+        const int target = l.targets[row];
+        const bool live = (uint32_t)target < (uint32_t)l.vocab && target != l.ignore;
+        if (!live && target != l.ignore && j0 == 0 && l.col0 == 0) set_error(l.ctrl, MOE_DERR_TARGET);
+        const float lse = l.lse[row], g = l.dloss[row] * scale, own = g * expm1f(-l.loss[row]);
+#pragma unroll
+        for (int hj = 0; hj < 2; ++hj)
+#pragma unroll
+          for (int n = 0; n < FJ; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int64_t j = j0 + hj * dj + n * 16 + 4 * (lane >> 4) + c;
+              const float p = g * __builtin_amdgcn_exp2f((s[h][hj][f][n][c] - lse) * 1.44269504088896341f);
+              v[hj][f][n][c] = !live || j >= a.N ? 0.0f : (j + l.col0 == target ? own : p);
+            }
+      }
+#pragma unroll
+      for (int hj = 0; hj < 2; ++hj)  // rows zero past N up to whole 16-byte chunks
+        store_block<T, FI, FJ>(e.y[0], e.ldy[0], i0 + h * di, j0 + hj * dj, a.M, (a.N + 7) / 8 * 8, e.stream, v[hj], (uint16_t*)lds, lane);
+    }
+    return;
+  }
+  const bool plain = KIND == kEpiStore || (KIND == kEpiSum && !e.loss.acc && !e.loss.scale && !e.y_f32) || (KIND == kEpiLinear && !e.bias[0] && !e.pre[0] && !e.res && !e.y_f32 && e.act == MOE_ACT_NONE);
 #pragma unroll
   for (int h = 0; h < NI; ++h)
 #pragma unroll
@@ -257,6 +288,71 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
         finish_fragments<T, KIND, FI, FJ>(a, x, i, j, s[h][hj], s[h][1], lds, lane);
       }
     }
+}
+
+// A tile of logits: for each row the maximum over the tile's columns and the sum of exp(z - maximum), the row's target left
+// out (its logit goes to zt), so that a small loss is log1p of what the others add and keeps its digits.  A lane has 4
+// columns of every fragment of a row, four lanes a row's fragment, and the WJ waves beside each other meet in LDS.  A
+// maximum that is infinite is not subtracted: its exponentials are then infinite, zero or NaN as the sum's limit is.
+MOE_DEV float not_infinite(float m) { return __builtin_isinf(m) ? 0.0f : m; }
+MOE_DEV float exp_below(float z, float m) { return __builtin_amdgcn_exp2f((z - m) * 1.44269504088896341f); }
+
+template <int TI, int WJ, int NI, int FI, int FJ>
+MOE_DEV void finish_loss(const TileArgs& a, const TileIndex& x, int64_t i0, int64_t di, int64_t j0, int64_t dj, int wj,
+                         const float4v (&s)[NI][2][FI][FJ], float* lds, int lane) {
+  const LossEpi& l = a.epi.loss;
+  const int64_t first = (int64_t)x.ti * TI;
+#pragma unroll
+  for (int h = 0; h < NI; ++h)
+#pragma unroll
+    for (int f = 0; f < FI; ++f) {
+      const int64_t i = i0 + h * di + f * 16 + (lane & 15);
+      const int target = i < a.M ? l.targets[i] : -1;
+      float m = -INFINITY, sum = 0.0f;
+      bool in[2][FJ][4];
+#pragma unroll
+      for (int hj = 0; hj < 2; ++hj)
+#pragma unroll
+        for (int n = 0; n < FJ; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int64_t j = j0 + hj * dj + n * 16 + 4 * (lane >> 4) + c;
+            const float z = s[h][hj][f][n][c];
+            const bool own = j == target;
+            in[hj][n][c] = j < a.N && !own;
+            if (own && i < a.M && j < a.N) l.zt[i] = z;
+            m = in[hj][n][c] ? fmaxf(m, z) : m;
+          }
+      m = fmaxf(m, __shfl_xor(m, 16, 64));
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      const float base = not_infinite(m);
+#pragma unroll
+      for (int hj = 0; hj < 2; ++hj)
+#pragma unroll
+        for (int n = 0; n < FJ; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sum += in[hj][n][c] ? exp_below(s[h][hj][f][n][c], base) : 0.0f;
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+      if (lane < 16) {
+        float* p = lds + ((i - first) * WJ + wj) * 2;
+        p[0] = m;
+        p[1] = sum;
+      }
+    }
+  __syncthreads();
+  for (int r = threadIdx.x; r < TI; r += blockDim.x) {
+    if (first + r >= a.M) break;
+    const float* p = lds + r * WJ * 2;
+    float m = p[0];
+#pragma unroll
+    for (int w = 1; w < WJ; ++w) m = fmaxf(m, p[2 * w]);
+    const float base = not_infinite(m);
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WJ; ++w) sum += p[2 * w] == m ? p[2 * w + 1] : p[2 * w + 1] * exp_below(p[2 * w], base);
+    l.part[(int64_t)x.tj * a.M + first + r] = make_float2(m, sum);
+  }
 }
 
 // ---- any alignment --------------------------------------------------------------------------------
@@ -437,8 +533,11 @@ MOE_DEV void any_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   if (s < s_end) step(s, zero);
 
   __syncthreads();
-  finish_blocks<T, KIND>(a, x, i0 + wi * 16 * F, H, j0 + wj * 16 * F, H, acc,
-                         (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * F * F * 256, lane);
+  if constexpr (KIND == kEpiLoss)
+    finish_loss<2 * H, 2>(a, x, i0 + wi * 16 * F, H, j0 + wj * 16 * F, H, wj, acc, (float*)lds, lane);
+  else
+    finish_blocks<T, KIND>(a, x, i0 + wi * 16 * F, H, j0 + wj * 16 * F, H, acc,
+                           (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * F * F * 256, lane);
 }
 
 template <typename T, int OA, int OB, int KIND, int F>
@@ -663,7 +762,10 @@ MOE_DEV void deep_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int n = 0; n < 2; ++n) s[0][h][n][0] = acc[h][n];
-  finish_blocks<T, KIND>(a, x, i0 + wi * 32, 0, j0 + wj * 16, HJ, s, (float*)lds + wave * 1024, lane);
+  if constexpr (KIND == kEpiLoss)
+    finish_loss<HI, 2>(a, x, i0 + wi * 32, 0, j0 + wj * 16, HJ, wj, s, (float*)lds, lane);
+  else
+    finish_blocks<T, KIND>(a, x, i0 + wi * 32, 0, j0 + wj * 16, HJ, s, (float*)lds + wave * 1024, lane);
 }
 
 template <typename T, int OA, int OB, int KIND>
@@ -833,8 +935,11 @@ MOE_DEV void big_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   if (k < count) step(std::integral_constant<int, 0>{});
   copies_barrier<0>();  // no copy may land after the workgroup has given its LDS back
 
-  finish_blocks<T, KIND>(a, x, i0 + wi * FI * 16, HI, j0 + wj * FJ * 16, HJ, acc,
-                         (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * FI * FJ * 256, lane);
+  if constexpr (KIND == kEpiLoss)
+    finish_loss<2 * HI, WJ>(a, x, i0 + wi * FI * 16, HI, j0 + wj * FJ * 16, HJ, wj, acc, (float*)lds, lane);
+  else
+    finish_blocks<T, KIND>(a, x, i0 + wi * FI * 16, HI, j0 + wj * FJ * 16, HJ, acc,
+                           (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * FI * FJ * 256, lane);
 }
 
 template <typename T, int OA, int OB, int KIND, int WI, int WJ, int FI, int FJ>

@@ -1,0 +1,343 @@
+// Softmax cross entropy over an output head (moe_loss_*): C interface, workspace and the kernels beside the products.
+//
+// Forward: one pass of tiles over the whole vocabulary; a tile's logits live in registers only and leave a maximum and a
+// sum per row (8 bytes per row and tile of 64 to 256 columns), which a second launch joins.
+// Backward, for one piece of the vocabulary after another: dz = dloss (exp(z - lse) - [target]) of the piece from its
+// logits, computed again and rounded to the operands' type; then dW of the piece, whole, and the piece's share of dx, summed
+// in fp32 over the pieces.
+#include "loss.hpp"
+
+namespace moe {
+
+constexpr int kLossTokens = 8192;          // tokens of a forward launch: bounds the parts
+constexpr size_t kLossDzBytes = 256u << 20;  // dz of a piece, about
+constexpr int kLossTile = 64;              // the smallest tile's columns
+
+struct LossWs {
+  size_t part, zt, scale, x, w, dz, acc, sums, sums_bytes, total;
+  int64_t ld_in, piece, ldz;
+};
+
+// Columns of a piece: a multiple of 256, at least one, its dz within the limit where that allows it.
+static int64_t piece_columns(int64_t T, int64_t V) {
+  int64_t c = (int64_t)(kLossDzBytes / 2) / T / 1024 * 1024;
+  if (c < 1024) c = (int64_t)(kLossDzBytes / 2) / T / 256 * 256;
+  if (c < 256) c = 256;
+  const int64_t all = (V + 7) / 8 * 8;
+  return c < all ? c : all;
+}
+
+static LossWs loss_ws(const moe_loss_dims* d, int64_t T, bool backward) {
+  LossWs L{};
+  const int64_t V = d->vocab, chunk = T < kLossTokens ? T : kLossTokens;
+  L.ld_in = ((int64_t)d->n_in + 7) / 8 * 8;
+  size_t off = kCtrlBytes;
+  L.scale = off;
+  off = dense_align(off + 2 * sizeof(float));
+  L.zt = off;
+  off = dense_align(off + sizeof(float) * chunk);
+  L.part = off;
+  off = dense_align(off + sizeof(float2) * (size_t)(chunk * ((V + kLossTile - 1) / kLossTile)));
+  // copies of operands without whole 16-byte rows: x always (its stride is the caller's), the weights when n_in says so
+  L.x = off;
+  off = dense_align(off + 2 * (size_t)(T * L.ld_in));
+  if (d->n_in % 8) {
+    L.w = off;
+    off = dense_align(off + 2 * (size_t)(V * L.ld_in));
+  }
+  if (backward) {
+    L.piece = piece_columns(T, V);
+    L.ldz = L.piece;
+    L.dz = off;
+    off = dense_align(off + 2 * (size_t)(T * L.ldz));
+    L.acc = off;
+    if (L.piece < V) off = dense_align(off + sizeof(float) * (size_t)(T * L.ld_in));
+    L.sums = off;
+    const size_t dx = split_bytes(kMaxSplits, 1, T, d->n_in), dw = split_bytes(kMaxSplits, 1, L.piece, d->n_in);
+    L.sums_bytes = dx > dw ? dx : dw;
+    if (L.sums_bytes > kDensePartBytes) L.sums_bytes = kDensePartBytes;
+    off = dense_align(off + L.sums_bytes);
+  }
+  L.total = off;
+  return L;
+}
+
+struct LossJoinArgs {
+  const float2* part;
+  const float* zt;
+  const int32_t* targets;
+  float *loss, *lse;
+  int32_t* ctrl;
+  int32_t T, tiles, vocab, ignore;
+};
+
+// A token's tiles joined: with m, s the maximum and sum of the other columns and zt the target's logit,
+//   loss = log(1 + s exp(m - zt)) or, with zt below m, (m - zt) + log(s + exp(zt - m));  lse = zt + loss likewise.
+// BLOCK tokens per workgroup share its 256 threads; a token's tiles are joined in a fixed order.  Memory-bound.
+template <int BLOCK>
+__global__ __launch_bounds__(256) void k_loss_join(LossJoinArgs a) {
+  constexpr int kShares = 256 / BLOCK;
+  __shared__ float ms[256], ss[256];
+  const int t = blockIdx.x * BLOCK + threadIdx.x % BLOCK, share = threadIdx.x / BLOCK;
+  float m = -INFINITY, s = 0.0f;
+  if (t < a.T) {
+    for (int i = share; i < a.tiles; i += kShares * 8) {
+      float2 p[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int at = i + u * kShares;
+        p[u] = a.part[(int64_t)(at < a.tiles ? at : i) * a.T + t];
+        if (at >= a.tiles) p[u] = make_float2(-INFINITY, 0.0f);
+      }
+      float most = m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) most = fmaxf(most, p[u].x);
+      const float base = __builtin_isinf(most) ? 0.0f : most;
+      s = m == most ? s : s * expf(m - base);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += p[u].x == most ? p[u].y : p[u].y * expf(p[u].x - base);
+      m = most;
+    }
+  }
+  ms[threadIdx.x] = m;
+  ss[threadIdx.x] = s;
+  __syncthreads();
+  if (share || t >= a.T) return;
+  for (int i = 1; i < kShares; ++i) m = fmaxf(m, ms[threadIdx.x + i * BLOCK]);
+  const float base = __builtin_isinf(m) ? 0.0f : m;
+  s = 0.0f;
+  for (int i = 0; i < kShares; ++i) {
+    const float mi = ms[threadIdx.x + i * BLOCK], si = ss[threadIdx.x + i * BLOCK];
+    s += mi == m ? si : si * expf(mi - base);
+  }
+  const int target = a.targets[t];
+  float loss = 0.0f, lse = 0.0f;
+  if ((uint32_t)target < (uint32_t)a.vocab && target != a.ignore) {
+    const float z = a.zt[t];
+    if (z >= m) {
+      loss = log1pf(s * expf(m - z));
+      lse = z + loss;
+    } else {
+      const float rest = logf(s + expf(z - m));
+      loss = (m - z) + rest;
+      lse = m + rest;
+    }
+  } else if (target != a.ignore) {
+    set_error(a.ctrl, MOE_DERR_TARGET);
+    loss = lse = __builtin_nanf("");
+  }
+  a.loss[t] = loss;
+  a.lse[t] = lse;
+}
+
+// fp16's dz is kept in its normal range by a power of two S with S max|dloss| in [2^11, 2^12): at most 4096 for a target, normal
+// down to probabilities of 2^-25, 8 bits left at 2^-32.  out = {S, 1 / S}.
+__global__ __launch_bounds__(1024) void k_loss_scale(const float* dloss, const int32_t* targets, int T, int vocab, int ignore,
+                                                     float* out) {
+  __shared__ float most[16];
+  float m = 0.0f;
+  for (int t = threadIdx.x; t < T; t += 1024) {
+    const float g = fabsf(dloss[t]);
+    if ((uint32_t)targets[t] < (uint32_t)vocab && targets[t] != ignore && g < INFINITY) m = fmaxf(m, g);
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int i = 1; i < 16; ++i) m = fmaxf(m, most[i]);
+  int e = 0;
+  if (m > 0.0f) e = 11 - ilogbf(m);
+  e = e < -100 ? -100 : (e > 100 ? 100 : e);
+  out[0] = ldexpf(1.0f, e);
+  out[1] = ldexpf(1.0f, -e);
+}
+
+static int check_loss(const moe_loss_dims* d) {
+  if (!d || d->n_in < 1 || d->vocab < 1) return MOE_EINVAL;
+  if (d->n_in > MOE_DENSE_MAX_WIDTH || d->vocab > MOE_DENSE_MAX_WIDTH) return MOE_EUNSUPPORTED;
+  return d->dtype == MOE_BF16 || d->dtype == MOE_F16 ? MOE_OK : MOE_EUNSUPPORTED;
+}
+
+static int check_loss_tokens(const moe_loss_dims* d, int32_t T) {
+  const int rc = check_loss(d);
+  if (rc) return rc;
+  if (T < 1) return MOE_EINVAL;
+  return T > MOE_LOSS_MAX_TOKENS ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
+static int check_loss_ws(const moe_loss_dims* d, int32_t T, bool backward, const void* ws, size_t ws_bytes) {
+  if (!ws || ((uintptr_t)ws & 255)) return MOE_EWORKSPACE;
+  return ws_bytes < loss_ws(d, T, backward).total ? MOE_EWORKSPACE : MOE_OK;
+}
+
+static TileArgs logits_args(const moe_loss_dims* d, const int32_t* targets, void* ws) {
+  TileArgs a{};
+  a.nseg = a.nbatch = 1;
+  a.R = a.len_a = a.len_b = d->n_in;
+  a.epi.loss.targets = targets;
+  a.epi.loss.ctrl = (int32_t*)ws;
+  a.epi.loss.vocab = d->vocab;
+  a.epi.loss.ignore = d->ignore;
+  return a;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+MOE_API size_t moe_loss_workspace_bytes(const moe_loss_dims* dims, int32_t max_tokens, int32_t backward) {
+  return check_loss_tokens(dims, max_tokens) != MOE_OK ? 0 : loss_ws(dims, max_tokens, backward != 0).total;
+}
+
+MOE_API int moe_loss_forward(const moe_loss_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
+                             int64_t ldw, const int32_t* targets, float* loss, float* lse, void* ws, size_t ws_bytes,
+                             void* stream) {
+  int rc = check_loss_tokens(dims, n_tokens);
+  if (rc) return rc;
+  Mats m;
+  m.need(x, ldx, dims->n_in);
+  m.need(w, ldw, dims->n_in);
+  m.need(targets, 1, 1, 4);
+  m.need(loss, 1, 1, 4);
+  m.need(lse, 1, 1, 4);
+  if (m.rc) return m.rc;
+  if ((rc = check_loss_ws(dims, n_tokens, false, ws, ws_bytes))) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  const LossWs L = loss_ws(dims, n_tokens, false);
+  auto at = [&](size_t off) { return (uint8_t*)ws + off; };
+  for (int32_t t0 = 0; t0 < n_tokens; t0 += kLossTokens) {
+    TileArgs a = logits_args(dims, targets + t0, ws);
+    a.a[0] = (const uint16_t*)x + t0 * ldx;
+    a.lda[0] = ldx;
+    a.b[0] = w;
+    a.ldb[0] = ldw;
+    a.M = n_tokens - t0 < kLossTokens ? n_tokens - t0 : kLossTokens;
+    a.N = dims->vocab;
+    a.pack_a = (uint16_t*)at(L.x);
+    a.pack_b[0] = L.w ? (uint16_t*)at(L.w) : nullptr;
+    a.epi.loss.part = (float2*)at(L.part);
+    a.epi.loss.zt = (float*)at(L.zt);
+    LossJoinArgs j{};
+    if ((rc = dense_status(dims->dtype == MOE_BF16 ? launch_loss_bf16(a, &j.tiles, st) : launch_loss_f16(a, &j.tiles, st)))) return rc;
+    j.part = a.epi.loss.part;
+    j.zt = a.epi.loss.zt;
+    j.targets = targets + t0;
+    j.loss = loss + t0;
+    j.lse = lse + t0;
+    j.ctrl = (int32_t*)ws;
+    j.T = a.M;
+    j.vocab = dims->vocab;
+    j.ignore = dims->ignore;
+    if (a.M >= 16) k_loss_join<16><<<(a.M + 15) / 16, 256, 0, st>>>(j);
+    else if (a.M >= 4) k_loss_join<4><<<(a.M + 3) / 4, 256, 0, st>>>(j);
+    else k_loss_join<1><<<a.M, 256, 0, st>>>(j);
+    if (hipGetLastError() != hipSuccess) return MOE_EHIP;
+  }
+  return MOE_OK;
+}
+
+MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t ldx, int32_t n_tokens, const void* w,
+                              int64_t ldw, const int32_t* targets, const float* loss, const float* lse,
+                              const float* dloss, void* dx_or_null, int64_t ld_dx, void* dw_or_null, int64_t ld_dw,
+                              void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_loss_tokens(dims, n_tokens);
+  if (rc) return rc;
+  if (!dx_or_null && !dw_or_null) return MOE_EINVAL;
+  Mats m;
+  m.need(x, ldx, dims->n_in);
+  m.need(w, ldw, dims->n_in);
+  m.need(targets, 1, 1, 4);
+  m.need(loss, 1, 1, 4);
+  m.need(lse, 1, 1, 4);
+  m.need(dloss, 1, 1, 4);
+  m.opt(dx_or_null, ld_dx, dims->n_in);
+  m.opt(dw_or_null, ld_dw, dims->n_in);
+  if (m.rc) return m.rc;
+  if ((rc = check_loss_ws(dims, n_tokens, true, ws, ws_bytes))) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  const bool bf16 = dims->dtype == MOE_BF16;
+  const LossWs L = loss_ws(dims, n_tokens, true);
+  auto at = [&](size_t off) { return (uint8_t*)ws + off; };
+  float* scale = bf16 ? nullptr : (float*)at(L.scale);
+  if (scale) {
+    k_loss_scale<<<1, 1024, 0, st>>>(dloss, targets, n_tokens, dims->vocab, dims->ignore, scale);
+    if (hipGetLastError() != hipSuccess) return MOE_EHIP;
+  }
+  // Rows of whole 16-byte chunks for all three products, by one copy.
+  const void *xs = x, *wt = w;
+  int64_t ld_x = ldx, ld_w = ldw;
+  int32_t len = dims->n_in;
+  PackArgs p{};
+  if ((uintptr_t)x % 16 || ldx % 8 || dims->n_in % 8) {
+    p.m[p.count++] = {(const uint16_t*)x, (uint16_t*)at(L.x), ldx, L.ld_in, n_tokens, dims->n_in};
+    xs = at(L.x);
+    ld_x = L.ld_in;
+  }
+  if (L.w) {
+    p.m[p.count++] = {(const uint16_t*)w, (uint16_t*)at(L.w), ldw, L.ld_in, dims->vocab, dims->n_in};
+    wt = at(L.w);
+    ld_w = len = L.ld_in;
+  }
+  if (p.count && (rc = dense_status(launch_pack(p, st)))) return rc;
+  for (int32_t c0 = 0; c0 < dims->vocab; c0 += L.piece) {
+    const int32_t cols = dims->vocab - c0 < L.piece ? dims->vocab - c0 : (int32_t)L.piece, whole = (cols + 7) / 8 * 8;
+    const bool first = c0 == 0, last = c0 + cols == dims->vocab;
+    const uint16_t* wp = (const uint16_t*)wt + c0 * ld_w;
+    TileArgs z = logits_args(dims, targets, ws);
+    z.a[0] = xs;
+    z.lda[0] = ld_x;
+    z.b[0] = wp;
+    z.ldb[0] = ld_w;
+    z.M = n_tokens;
+    z.N = cols;
+    z.R = z.len_a = z.len_b = len;
+    z.epi.y[0] = at(L.dz);
+    z.epi.ldy[0] = L.ldz;
+    z.epi.loss.loss = loss;
+    z.epi.loss.lse = lse;
+    z.epi.loss.dloss = dloss;
+    z.epi.loss.scale = scale;
+    z.epi.loss.col0 = c0;
+    if ((rc = dense_status(bf16 ? launch_loss_dz_bf16(z, st) : launch_loss_dz_f16(z, st)))) return rc;
+    TileArgs s{};
+    s.nseg = s.nbatch = 1;
+    s.part = (float*)at(L.sums);
+    s.part_bytes = L.sums_bytes;
+    s.a[0] = at(L.dz);
+    s.lda[0] = L.ldz;
+    if (dw_or_null) {
+      TileArgs a = s;
+      a.b[0] = xs;
+      a.ldb[0] = ld_x;
+      a.M = cols;
+      a.N = dims->n_in;
+      a.R = n_tokens;
+      a.epi.loss.scale = scale ? scale + 1 : nullptr;
+      a.epi.y[0] = (uint16_t*)dw_or_null + c0 * ld_dw;
+      a.epi.ldy[0] = ld_dw;
+      if ((rc = dense_status(bf16 ? launch_loss_dw_bf16(a, st) : launch_loss_dw_f16(a, st)))) return rc;
+    }
+    if (dx_or_null) {
+      TileArgs a = s;
+      a.b[0] = wp;
+      a.ldb[0] = ld_w;
+      a.M = n_tokens;
+      a.N = dims->n_in;
+      a.R = cols;
+      a.len_a = whole;
+      a.epi.loss.acc = first ? nullptr : (const float*)at(L.acc);
+      a.epi.ldr = L.ld_in;
+      a.epi.y_f32 = !last;
+      a.epi.y[0] = last ? dx_or_null : at(L.acc);
+      a.epi.ldy[0] = last ? ld_dx : L.ld_in;
+      a.epi.loss.scale = scale && last ? scale + 1 : nullptr;
+      if ((rc = dense_status(bf16 ? launch_loss_dx_bf16(a, st) : launch_loss_dx_f16(a, st)))) return rc;
+    }
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -25,7 +25,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP, MOE_EDEVICE, MOE_EFILL = 0, -1, -2, -3, -4, -5, -6
 MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_DECODE_MAX_TOKENS, MOE_DECODE_MAX_TOKENS_NARROW = 16, 8
-DERR_EXPERT_ID, DERR_SLOT, DERR_NOT_RESIDENT, DERR_NAN, DERR_FILL, DERR_DUP_ID, DERR_RANGE, DERR_ROWS = 1, 2, 4, 8, 16, 32, 64, 128
+DERR_EXPERT_ID, DERR_SLOT, DERR_NOT_RESIDENT, DERR_NAN, DERR_FILL, DERR_DUP_ID, DERR_RANGE = 1, 2, 4, 8, 16, 32, 64
+DERR_ROWS, DERR_TARGET = 128, 256
 
 EXPORTS = [
     "moe_expert_blob_bytes", "moe_workspace_bytes", "moe_strerror", "moe_workspace_init",
@@ -40,6 +41,7 @@ EXPORTS = [
     "moe_combine_backward",
     "moe_experts_workspace_bytes", "moe_experts_linear_forward", "moe_experts_linear_backward",
     "moe_experts_gated_forward", "moe_experts_gated_backward",
+    "moe_loss_workspace_bytes", "moe_loss_forward", "moe_loss_backward",
 ]
 
 
@@ -85,7 +87,11 @@ class moe_experts_dims(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
-MOE_ROWS_MAX = 1 << 28
+class moe_loss_dims(ctypes.Structure):
+    _fields_ = [("n_in", ctypes.c_int32), ("vocab", ctypes.c_int32), ("dtype", ctypes.c_int32), ("ignore", ctypes.c_int32)]
+
+
+MOE_ROWS_MAX, MOE_LOSS_MAX_TOKENS = 1 << 28, 1 << 20
 
 MOE_GEMM_PIPE128, MOE_GEMM_PIPE64_DEEP, MOE_GEMM_GENERAL = 0, 1, 2
 
@@ -111,6 +117,7 @@ _PP = ctypes.POINTER(ctypes.c_void_p)
 _DD = ctypes.POINTER(moe_dense_dims)
 _RD = ctypes.POINTER(moe_rows_dims)
 _ED = ctypes.POINTER(moe_experts_dims)
+_LD = ctypes.POINTER(moe_loss_dims)
 _L = ctypes.c_int64
 
 _sig = {
@@ -161,6 +168,9 @@ _sig = {
     "moe_experts_gated_forward": (ctypes.c_int, [_ED, _P, _L, _I, _P, _P, _P, _L, _L, _P, _L, _P, _P, _L, _P, _SZ, _P]),
     "moe_experts_gated_backward": (ctypes.c_int, [_ED, _P, _L, _I, _P, _P, _P, _L, _L, _P, _P, _L, _P, _L, _P, _L, _P, _P,
                                                   _L, _L, _P, _SZ, _P]),
+    "moe_loss_workspace_bytes": (_SZ, [_LD, _I, _I]),
+    "moe_loss_forward": (ctypes.c_int, [_LD, _P, _L, _I, _P, _L, _P, _P, _P, _P, _SZ, _P]),
+    "moe_loss_backward": (ctypes.c_int, [_LD, _P, _L, _I, _P, _L, _P, _P, _P, _P, _P, _L, _P, _L, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -589,6 +599,37 @@ def moe_experts_gated_backward(d: moe_experts_dims, xs, offsets, w_gate, w_up, g
         *_stacks(w_gate, w_up, d, ty, dev, n + "w_gate, w_up"), *_pair(gate, up, P, d.n_out, ty, dev, n + "gate, up"),
         *_mat(dh, P, d.n_out, ty, dev, n + "dh"), *_opt_mat(dx, P, d.n_in, ty, dev, n + "dx"),
         *_stacks(dw_gate, dw_up, d, ty, dev, n + "dw_gate, dw_up")))
+
+
+# ---------------------------------------------------------------------------------------------
+# loss over an output head
+# ---------------------------------------------------------------------------------------------
+
+def loss_dims(n_in: int, vocab: int, dtype: int, ignore: int = -100) -> moe_loss_dims:
+    return moe_loss_dims(int(n_in), int(vocab), int(dtype), int(ignore))
+
+
+def moe_loss_workspace_bytes(d: moe_loss_dims, max_tokens: int, backward: bool = False) -> int:
+    return _lib.moe_loss_workspace_bytes(ctypes.byref(d), max_tokens, int(backward))
+
+
+def moe_loss_forward(d: moe_loss_dims, x, n_tokens: int, w, targets, loss, lse, ws, stream=None):
+    """Each token's softmax cross entropy ``loss`` and ``lse`` of the logits ``x w^T``, without keeping them."""
+    T, dev, ty, n = n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_loss_forward, "
+    _dense_call(_lib.moe_loss_forward, "moe_loss_forward", d, dev, ws, stream, (
+        *_mat(x, T, d.n_in, ty, dev, n + "x"), T, *_mat(w, d.vocab, d.n_in, ty, dev, n + "w"),
+        _array(targets, (T,), torch.int32, dev, n + "targets"), _array(loss, (T,), torch.float32, dev, n + "loss"),
+        _array(lse, (T,), torch.float32, dev, n + "lse")))
+
+
+def moe_loss_backward(d: moe_loss_dims, x, n_tokens: int, w, targets, loss, lse, dloss, ws, dx=None, dw=None, stream=None):
+    """Gradients of the losses from each token's ``dloss`` and the saved ``loss`` and ``lse``; None: not computed."""
+    T, dev, ty, n = n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), "moe_loss_backward, "
+    _dense_call(_lib.moe_loss_backward, "moe_loss_backward", d, dev, ws, stream, (
+        *_mat(x, T, d.n_in, ty, dev, n + "x"), T, *_mat(w, d.vocab, d.n_in, ty, dev, n + "w"),
+        _array(targets, (T,), torch.int32, dev, n + "targets"), _array(loss, (T,), torch.float32, dev, n + "loss"),
+        _array(lse, (T,), torch.float32, dev, n + "lse"), _array(dloss, (T,), torch.float32, dev, n + "dloss"),
+        *_opt_mat(dx, T, d.n_in, ty, dev, n + "dx"), *_opt_mat(dw, d.vocab, d.n_in, ty, dev, n + "dw")))
 
 
 def raw(name: str):

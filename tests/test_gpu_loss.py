@@ -1,0 +1,286 @@
+"""The loss over an output head on the GPU against float64, elementwise within the bounds of loss_reference."""
+
+import math
+
+import pytest
+import torch
+
+import dense_reference as R
+import loss_reference as L
+from test_gpu_dense import Out, guard_ok, rnd
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+IGNORE = -100
+
+
+@pytest.fixture(scope="module")
+def N():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mixture_experts_route_amd import native
+
+    return native
+
+
+def gen_for(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def workspace(N, d, T, backward):
+    n = N.moe_loss_workspace_bytes(d, T, backward)
+    whole = torch.full((n + 1024,), 0xA5, dtype=torch.uint8, device="cuda")
+    N.moe_workspace_init(whole[:n])
+    return whole[:n], whole
+
+
+def inputs(gen, T, K, V, dt, skip=0.1, pad=0, offset=0, sure=True):
+    x, w = rnd(gen, (T, K), dt, pad=pad, offset=offset), rnd(gen, (V, K), dt, K ** -0.5, pad, offset)
+    targets = torch.randint(0, V, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    if sure:  # some tokens are nearly certain of their target
+        lean = 8.0 * torch.rand(T, 1, generator=gen, device="cuda")
+        x.copy_((x.float() + lean * w[targets.long()].float()).to(dt))
+    targets[torch.rand(T, generator=gen, device="cuda") < skip] = IGNORE
+    return x, w, targets
+
+
+def floats(T, n=1):
+    return [torch.full((T,), float("nan"), device="cuda") for _ in range(n)]
+
+
+def check_all(N, seed, T, K, V, dt, skip=0.1, pad=0, offset=0, sure=True):
+    gen = gen_for(seed)
+    x, w, targets = inputs(gen, T, K, V, dt, skip, pad, offset, sure)
+    d = N.loss_dims(K, V, N.dtype_code(x), IGNORE)
+    ws, whole = workspace(N, d, T, False)
+    loss, lse = floats(T, 2)
+    N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+    ref = L.forward(x, w, targets, IGNORE)
+    R.check("loss", loss, ref["loss"])
+    R.check("lse", lse, ref["lse"])
+    assert N.moe_check_device_error(ws) == 0 and guard_ok(whole)
+    ws, whole = workspace(N, d, T, True)
+    dloss = torch.randn(T, generator=gen, device="cuda") / T
+    dx, dw = Out((T, K), dt, pad, offset), Out((V, K), dt, pad, offset)
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dx=dx.t, dw=dw.t)
+    ref = L.backward(x, w, targets, IGNORE, loss, lse, dloss, dt)
+    R.check("dx", dx.t, ref["dx"])
+    R.check("dw", dw.t, ref["dw"])
+    assert dx.untouched() and dw.untouched()
+    one, two = Out((T, K), dt, pad, offset), Out((V, K), dt, pad, offset)
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dx=one.t)
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dw=two.t)
+    assert torch.equal(one.t, dx.t) and torch.equal(two.t, dw.t)
+    assert N.moe_check_device_error(ws) == 0 and guard_ok(whole)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("T,K,V", [(1, 8, 1), (1, 64, 2), (2, 8, 7), (5, 64, 64), (3, 128, 65), (16, 64, 129), (17, 200, 1000),
+                                   (64, 72, 257), (65, 64, 4099), (300, 136, 513), (129, 512, 2000), (1000, 64, 100)])
+def test_against_float64(N, T, K, V, dt):
+    check_all(N, T + V, T, K, V, dt)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("T,K,V", [(1, 1, 1), (3, 7, 5), (33, 65, 130), (130, 61, 1003), (257, 131, 64)])
+def test_odd_widths(N, T, K, V, dt):
+    check_all(N, T * K, T, K, V, dt)
+
+
+@pytest.mark.parametrize("pad,offset", [(1, 0), (0, 3), (8, 8), (8, 0), (7, 1)])
+def test_strides_and_alignments(N, pad, offset):
+    check_all(N, 30 + pad, 70, 64, 300, BF16, pad=pad, offset=offset)
+    check_all(N, 31 + pad, 70, 61, 301, F16, pad=pad, offset=offset)
+
+
+@pytest.mark.parametrize("kernel", range(1, 6))
+@pytest.mark.parametrize("splits", [0, 3])
+def test_every_kernel(N, kernel, splits):
+    N.moe_debug_force_dense_plan(kernel, splits)
+    try:
+        check_all(N, kernel, 300, 192, 777, BF16)
+        check_all(N, kernel + 9, 5, 64, 600, F16)
+    finally:
+        N.moe_debug_force_dense_plan()
+
+
+def test_all_and_no_tokens_left_out(N):
+    check_all(N, 40, 20, 64, 100, BF16, skip=0.0)
+    check_all(N, 41, 20, 64, 100, F16, skip=1.1)
+
+
+def test_many_tokens_in_several_launches(N):
+    check_all(N, 42, 8192 + 5, 64, 200, BF16)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_vocabulary_in_several_pieces(N, dt):
+    check_all(N, 43, 40000, 40, 4000, dt)  # pieces of 2048 and 1952 columns
+    check_all(N, 44, 40001, 33, 3077, dt)
+
+
+def test_small_losses_keep_their_digits(N):
+    """Targets ahead by up to 40: losses down to 2^-58, each within a relative bound."""
+    T, V = 41, 300
+    x = torch.zeros(T, 8, dtype=BF16, device="cuda")
+    w = torch.zeros(V, 8, dtype=BF16, device="cuda")
+    x[:, 0] = torch.arange(T, device="cuda").to(BF16)
+    w[7, 0] = 1.0
+    targets = torch.full((T,), 7, dtype=torch.int32, device="cuda")
+    d = N.loss_dims(8, V, N.MOE_BF16)
+    ws, _ = workspace(N, d, T, True)
+    loss, lse = floats(T, 2)
+    N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+    want = torch.log1p((V - 1) * torch.exp(-torch.arange(T, device="cuda", dtype=torch.float64)))
+    # the logits are exact; (40 + 4 + 64) roundings of 2 e in the sum, 8 e after it
+    assert ((loss.double() - want).abs() <= want * 232 * R.E).all() and loss[40] > 0
+    dx = torch.empty_like(x)
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, torch.ones(T, device="cuda"), ws, dx=dx)
+    want = torch.expm1(-want)
+    assert ((dx[:, 0].double() - want).abs() <= want.abs() * (2 * R.half_step(BF16) + 300 * R.E)).all()
+
+
+def test_targets_out_of_range_are_reported(N):
+    T, K, V = 40, 64, 300
+    gen = gen_for(45)
+    x, w, targets = inputs(gen, T, K, V, BF16, skip=0.0)
+    d = N.loss_dims(K, V, N.MOE_BF16, IGNORE)
+    ws, _ = workspace(N, d, T, True)
+    good = targets.clone()
+    for at, bad in ((3, -1), (17, V), (39, 2 ** 31 - 1), (0, -2 ** 31)):
+        targets = good.clone()
+        targets[at] = bad
+        loss, lse = floats(T, 2)
+        N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+        assert N.moe_check_device_error(ws) == N.DERR_TARGET
+        assert torch.isnan(loss[at]) and torch.isnan(lse[at]) and torch.isnan(loss).sum() == 1
+        dx, dw = Out((T, K), BF16), Out((V, K), BF16)
+        dloss = torch.ones(T, device="cuda")
+        N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dx=dx.t, dw=dw.t)
+        assert N.moe_check_device_error(ws) == N.DERR_TARGET
+        assert (dx.t[at] == 0).all() and dx.untouched() and dw.untouched()
+        targets[at], loss[at], lse[at] = IGNORE, 0.0, 0.0
+        R.check("dw", dw.t, L.backward(x, w, targets, IGNORE, loss, lse, dloss, BF16)["dw"])
+
+
+def test_ignore_may_be_any_value(N):
+    T, K, V = 30, 64, 50
+    gen = gen_for(46)
+    x, w, targets = inputs(gen, T, K, V, BF16, skip=0.0)
+    targets[4] = -1
+    d = N.loss_dims(K, V, N.MOE_BF16, -1)
+    ws, _ = workspace(N, d, T, False)
+    loss, lse = floats(T, 2)
+    N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+    assert N.moe_check_device_error(ws) == 0 and loss[4] == 0 and lse[4] == 0
+    targets[4], targets[:3] = 3, 7
+    d = N.loss_dims(K, V, N.MOE_F16, 7)  # inside the vocabulary: a padding token's id
+    ws, _ = workspace(N, d, T, True)
+    x, w = x.half(), w.half()
+    N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+    assert (loss[:3] == 0).all()
+    ref = L.forward(x, w, targets, 7)
+    R.check("loss", loss, ref["loss"])
+    dloss = torch.ones(T, device="cuda")
+    dloss[0] = 1e30  # a token that is left out does not count for the scaling either
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dx=dx, dw=dw)
+    ref = L.backward(x, w, targets, 7, loss, lse, dloss, F16)
+    R.check("dx", dx, ref["dx"])
+    R.check("dw", dw, ref["dw"])
+    assert N.moe_check_device_error(ws) == 0
+
+
+def test_infinities_and_nan(N):
+    """Limits where logits are infinite; a NaN stays in its token."""
+    V, K = 100, 64
+    w = torch.zeros(V, K, dtype=BF16, device="cuda")
+    w[:, 0], w[5, 1], w[9, 2] = 1.0, float("inf"), float("-inf")
+    x = torch.zeros(6, K, dtype=BF16, device="cuda")
+    x[0, 0], x[:, 1:3], x[5, 0] = 1.0, 1.0, float("nan")
+    targets = torch.tensor([5, 9, 0, 5, IGNORE, 0], dtype=torch.int32, device="cuda")
+    d = N.loss_dims(K, V, N.MOE_BF16, IGNORE)
+    ws, _ = workspace(N, d, 6, True)
+    loss, lse = floats(6, 2)
+    N.moe_loss_forward(d, x, 6, w, targets, loss, lse, ws)
+    assert loss[0] == 0 and lse[0] == math.inf and loss[3] == 0  # the target's logit alone is infinite
+    assert loss[1] == math.inf and loss[2] == math.inf           # another's is
+    assert loss[4] == 0 and lse[4] == 0 and torch.isnan(loss[5]) and torch.isnan(lse[5])
+    assert N.moe_check_device_error(ws) == 0
+
+
+def test_equal_calls_give_equal_bits_captured_too(N):
+    gen = gen_for(47)
+    T, K, V = 200, 128, 1003
+    x, w, targets = inputs(gen, T, K, V, F16)
+    d = N.loss_dims(K, V, N.MOE_F16, IGNORE)
+    ws, _ = workspace(N, d, T, True)
+    dloss = torch.full((T,), 1.0 / T, device="cuda")
+
+    def outs():
+        return floats(T, 2) + [torch.empty_like(x), torch.empty_like(w)]
+
+    def step(o):
+        N.moe_loss_forward(d, x, T, w, targets, o[0], o[1], ws)
+        N.moe_loss_backward(d, x, T, w, targets, o[0], o[1], dloss, ws, dx=o[2], dw=o[3])
+
+    cap = outs()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(cap)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(cap)
+    for rep in range(4):
+        nx, _, nt = inputs(gen, T, K, V, F16)
+        x.copy_(nx)
+        targets.copy_(nt)
+        dloss.mul_(3.0)
+        eager = outs()
+        for v in (*cap, *eager):
+            v.fill_(float("nan"))
+        step(eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(eager, cap)):
+            assert torch.equal(a, b), (rep, i)
+
+
+def test_large_vocabulary_and_2_31_elements(N):
+    """A head of 2^31 elements: a few tokens, sampled columns of dW."""
+    T, K, V = 3, 2048, (1 << 20)
+    gen = gen_for(48)
+    w = torch.empty(V, K, dtype=BF16, device="cuda")
+    for i in range(0, V, 1 << 17):
+        w[i:i + (1 << 17)] = (torch.randn(1 << 17, K, generator=gen, device="cuda") / 45).to(BF16)
+    x = rnd(gen, (T, K), BF16)
+    targets = torch.tensor([V - 1, 0, 700000], dtype=torch.int32, device="cuda")
+    d = N.loss_dims(K, V, N.MOE_BF16, IGNORE)
+    ws, whole = workspace(N, d, T, True)
+    loss, lse = floats(T, 2)
+    N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+    z = torch.cat([x.double() @ w[i:i + (1 << 16)].double().T for i in range(0, V, 1 << 16)], 1)
+    want = torch.logsumexp(z, 1)
+    bound = 1e-4  # ez = 2 K e sum|terms| < 2 * 2048 * 2^-24 * 0.1, the sum's (24 + 64 + 2048) 2 e; both below
+    assert (lse.double() - want).abs().max() < bound and (loss.double() - (want - z.gather(1, targets.long()[:, None])[:, 0])).abs().max() < bound
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    dloss = torch.tensor([1.0, -2.0, 0.5], device="cuda")
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dx=dx, dw=dw)
+    p = torch.exp(z - lse.double()[:, None])
+    p[torch.arange(T), targets.long()] = torch.expm1(-loss.double())
+    dz = p * dloss.double()[:, None]
+    cols = torch.tensor([0, 1, 65535, 699999, 700000, V - 2, V - 1], device="cuda")
+    val = dz[:, cols].T @ x.double()
+    mag = dz[:, cols].abs().T @ x.double().abs()
+    R.check("dw", dw[cols], (val, R._round(val, mag * (R.half_step(BF16) + bound), BF16)))
+    val, mag = torch.zeros(T, K, dtype=torch.float64, device="cuda"), torch.zeros(T, K, dtype=torch.float64, device="cuda")
+    for i in range(0, V, 1 << 16):
+        val += dz[:, i:i + (1 << 16)] @ w[i:i + (1 << 16)].double()
+        mag += dz[:, i:i + (1 << 16)].abs() @ w[i:i + (1 << 16)].double().abs()
+    # 2^20 terms in fp32: each wave's chain has at most 2^20 additions, 2 e of what is summed so far, which the bound takes
+    # as the sum of magnitudes
+    R.check("dx", dx, (val, R._round(val, mag * (R.half_step(BF16) + bound + 2 * V * R.E), BF16)))
+    assert guard_ok(whole) and N.moe_check_device_error(ws) == 0
