@@ -155,6 +155,11 @@ MOE_DEV void act_both_far(int act, float z, float& v, float& d) {
 // every value that f may have had. NaN passes.
 MOE_DEV float times_far(float p, float f) { return p == 0.0f && f == f ? p : p * f; }
 
+// exp(z - m) below a maximum m.  One that is infinite is not subtracted: its exponentials are then infinite, zero or NaN as
+// the sum's limit is.
+MOE_DEV float not_infinite(float m) { return __builtin_isinf(m) ? 0.0f : m; }
+MOE_DEV float exp_below(float z, float m) { return __builtin_amdgcn_exp2f((z - m) * 1.44269504088896341f); }
+
 // ---- epilogues ------------------------------------------------------------------------------------
 enum DenseEpiKind { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2,
                     kEpiLoss = 3,    // logits: a row's maximum and sum of exponentials over the tile's columns
@@ -166,7 +171,6 @@ struct LossEpi {
   const int32_t* targets;
   const float *loss, *lse, *dloss;  // kEpiLossDz
   float2* part;                     // kEpiLoss: [tiles_j][M], the target's column left out
-  float* zt;                        // kEpiLoss: [M], the target's logit
   const float* scale;               // kEpiLossDz: dz's factor; kEpiSum: the results' (NULL: 1)
   const float* acc;                 // kEpiSum: the earlier sums, row stride DenseEpi::ldr (NULL: none)
   int32_t* ctrl;

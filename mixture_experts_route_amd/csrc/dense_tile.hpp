@@ -244,6 +244,7 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
   if constexpr (KIND == kEpiLossDz) {
     const LossEpi& l = e.loss;
     const float scale = l.scale ? *l.scale : 1.0f;
+    const bool inside = j0 + dj + FJ * 16 <= a.N;
 #pragma unroll
     for (int h = 0; h < NI; ++h) {
       float4v v[2][FI][FJ];
@@ -254,21 +255,34 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
         const int target = l.targets[row];
         const bool live = (uint32_t)target < (uint32_t)l.vocab && target != l.ignore;
         if (!live && target != l.ignore && j0 == 0 && l.col0 == 0) set_error(l.ctrl, MOE_DERR_TARGET);
-        const float lse = l.lse[row], g = l.dloss[row] * scale, own = g * expm1f(-l.loss[row]);
+        const float lse = l.lse[row], g = l.dloss[row] * scale;
+        const int at = target - l.col0 - (int)j0;  // its column in this block
 #pragma unroll
         for (int hj = 0; hj < 2; ++hj)
 #pragma unroll
           for (int n = 0; n < FJ; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const int64_t j = j0 + hj * dj + n * 16 + 4 * (lane >> 4) + c;
-              const float p = g * __builtin_amdgcn_exp2f((s[h][hj][f][n][c] - lse) * 1.44269504088896341f);
-              v[hj][f][n][c] = !live || j >= a.N ? 0.0f : (j + l.col0 == target ? own : p);
+              const float p = g * exp_below(s[h][hj][f][n][c], lse);
+              v[hj][f][n][c] = live ? p : 0.0f;
             }
+        if (!inside || __any(live && at >= 0 && at < (int)dj + FJ * 16)) {  // the targets' columns, and those past N
+          const float own = g * expm1f(-l.loss[row]);
+#pragma unroll
+          for (int hj = 0; hj < 2; ++hj)
+#pragma unroll
+            for (int n = 0; n < FJ; ++n)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int j = hj * (int)dj + n * 16 + 4 * (lane >> 4) + c;
+                if (live && j == at) v[hj][f][n][c] = own;
+                if (j0 + j >= a.N) v[hj][f][n][c] = 0.0f;
+              }
+        }
       }
 #pragma unroll
-      for (int hj = 0; hj < 2; ++hj)  // rows zero past N up to whole 16-byte chunks
-        store_block<T, FI, FJ>(e.y[0], e.ldy[0], i0 + h * di, j0 + hj * dj, a.M, (a.N + 7) / 8 * 8, e.stream, v[hj], (uint16_t*)lds, lane);
+      for (int hj = 0; hj < 2; ++hj)  // rows zero past N up to whole 16-byte chunks; they are read again soon: no hint
+        store_block<T, FI, FJ>(e.y[0], e.ldy[0], i0 + h * di, j0 + hj * dj, a.M, (a.N + 7) / 8 * 8, false, v[hj], (uint16_t*)lds, lane);
     }
     return;
   }
@@ -291,38 +305,44 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
 }
 
 // A tile of logits: for each row the maximum over the tile's columns and the sum of exp(z - maximum), the row's target left
-// out (its logit goes to zt), so that a small loss is log1p of what the others add and keeps its digits.  A lane has 4
-// columns of every fragment of a row, four lanes a row's fragment, and the WJ waves beside each other meet in LDS.  A
-// maximum that is infinite is not subtracted: its exponentials are then infinite, zero or NaN as the sum's limit is.
-MOE_DEV float not_infinite(float m) { return __builtin_isinf(m) ? 0.0f : m; }
-MOE_DEV float exp_below(float z, float m) { return __builtin_amdgcn_exp2f((z - m) * 1.44269504088896341f); }
-
+// out, so that a small loss is log1p of what the others add and keeps its digits.  A lane has 4
+// columns of every fragment of a row, four lanes a row's fragment, and the WJ waves beside each other meet in LDS.
 template <int TI, int WJ, int NI, int FI, int FJ>
 MOE_DEV void finish_loss(const TileArgs& a, const TileIndex& x, int64_t i0, int64_t di, int64_t j0, int64_t dj, int wj,
                          const float4v (&s)[NI][2][FI][FJ], float* lds, int lane) {
   const LossEpi& l = a.epi.loss;
   const int64_t first = (int64_t)x.ti * TI;
+  const bool inside = j0 + dj + FJ * 16 <= a.N;
 #pragma unroll
   for (int h = 0; h < NI; ++h)
 #pragma unroll
     for (int f = 0; f < FI; ++f) {
       const int64_t i = i0 + h * di + f * 16 + (lane & 15);
-      const int target = i < a.M ? l.targets[i] : -1;
-      float m = -INFINITY, sum = 0.0f;
-      bool in[2][FJ][4];
+      const int at = (i < a.M ? l.targets[i] : -1) - (int)j0;
+      float z[2][FJ][4], m = -INFINITY, sum = 0.0f;
 #pragma unroll
       for (int hj = 0; hj < 2; ++hj)
 #pragma unroll
         for (int n = 0; n < FJ; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int64_t j = j0 + hj * dj + n * 16 + 4 * (lane >> 4) + c;
-            const float z = s[h][hj][f][n][c];
-            const bool own = j == target;
-            in[hj][n][c] = j < a.N && !own;
-            if (own && i < a.M && j < a.N) l.zt[i] = z;
-            m = in[hj][n][c] ? fmaxf(m, z) : m;
-          }
+          for (int c = 0; c < 4; ++c) z[hj][n][c] = s[h][hj][f][n][c];
+      if (!inside || __any(at >= 0 && at < (int)dj + FJ * 16)) {  // left out: exp gives 0
+#pragma unroll
+        for (int hj = 0; hj < 2; ++hj)
+#pragma unroll
+          for (int n = 0; n < FJ; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int j = hj * (int)dj + n * 16 + 4 * (lane >> 4) + c;
+              if (j == at || j0 + j >= a.N) z[hj][n][c] = -INFINITY;
+            }
+      }
+#pragma unroll
+      for (int hj = 0; hj < 2; ++hj)
+#pragma unroll
+        for (int n = 0; n < FJ; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) m = fmaxf(m, z[hj][n][c]);
       m = fmaxf(m, __shfl_xor(m, 16, 64));
       m = fmaxf(m, __shfl_xor(m, 32, 64));
       const float base = not_infinite(m);
@@ -331,7 +351,7 @@ MOE_DEV void finish_loss(const TileArgs& a, const TileIndex& x, int64_t i0, int6
 #pragma unroll
         for (int n = 0; n < FJ; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) sum += in[hj][n][c] ? exp_below(s[h][hj][f][n][c], base) : 0.0f;
+          for (int c = 0; c < 4; ++c) sum += exp_below(z[hj][n][c], base);
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);
       if (lane < 16) {

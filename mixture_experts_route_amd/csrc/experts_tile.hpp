@@ -99,23 +99,42 @@ MOE_DEV bool group_rows(const GroupArgs& g, TileArgs& a, TileIndex& x) {
   return true;
 }
 
-// This workgroup's tile of dW, its reduction the expert's rows.  Consecutive tiles are of one expert, and an XCD takes a
-// run of them.
-MOE_DEV void group_sums(const GroupArgs& g, TileArgs& a, TileIndex& x) {
-  a = g.tile;
-  const uint32_t each = (uint32_t)a.tiles_i * (uint32_t)a.tiles_j, count = gridDim.x;
-  const uint32_t q = count / 8, rem = count % 8, xcd = blockIdx.x % 8;
-  const uint32_t t = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / 8;
-  const uint32_t me = t / each, in = t - me * each;
-  const int e = (int)(me / (uint32_t)g.mats), m = (int)(me - (uint32_t)e * g.mats);
-  x = {0, (int)(in / (uint32_t)a.tiles_j), (int)(in % (uint32_t)a.tiles_j), 0, 1};
-  const int o0 = g.offsets[e], o1 = g.offsets[e + 1];
+// Tiles of dW, whose reduction is an expert's rows.  A tile's time goes by its expert's rows, so each matrix's tiles are
+// spread over all XCDs, each XCD taking a run of an eighth of them (a run of whole experts per XCD: 8 experts of 4096 rows
+// on average, the longest three times that, 4096 x 4096, 2273 us; spread 922), along the shorter side first, which reads the
+// fewest different operand columns.
+struct DwTile {
+  int e, m, ti, tj, row0, rows, steps;
+};
+MOE_DEV uint32_t dw_run(const GroupArgs& g) { return ((uint32_t)g.tile.tiles_i * (uint32_t)g.tile.tiles_j + 7) / 8; }
+// Tile `at` of this XCD's; false: there is none there.
+MOE_DEV bool dw_tile(const GroupArgs& g, const int32_t* offsets, uint32_t run, uint32_t at, DwTile& x) {
+  const uint32_t ti = (uint32_t)g.tile.tiles_i, tj = (uint32_t)g.tile.tiles_j;
+  const uint32_t me = at / run, in = blockIdx.x % 8 * run + (at - me * run);
+  if (in >= ti * tj) return false;
+  x.e = (int)(me / (uint32_t)g.mats);
+  x.m = (int)(me - (uint32_t)x.e * g.mats);
+  x.ti = (int)(ti < tj ? in % ti : in / tj);
+  x.tj = (int)(ti < tj ? in / ti : in % tj);
+  const int o0 = __builtin_amdgcn_readfirstlane(offsets[x.e]), o1 = __builtin_amdgcn_readfirstlane(offsets[x.e + 1]);
   const int lo = clamp_rows(o0, g.P), hi = clamp_rows(o1, g.P);
   if (in == 0 && threadIdx.x == 0 && (o0 != lo || o1 != hi || hi < lo)) set_error(g.ctrl, MOE_DERR_ROWS);
-  a.R = hi > lo ? hi - lo : 0;
-  a.a[0] = (const uint16_t*)(m ? a.a[1] : a.a[0]) + lo * a.lda[0];
-  a.b[0] = (const uint16_t*)a.b[0] + lo * a.ldb[0];
-  a.epi.y[0] = (uint16_t*)(m ? a.epi.y[1] : a.epi.y[0]) + e * g.stride;
+  x.row0 = lo;
+  x.rows = hi > lo ? hi - lo : 0;
+  x.steps = x.rows ? (x.rows + kStepR - 1) / kStepR : 1;
+  return true;
+}
+// This workgroup's tile of dW, as arguments of its expert's product; false: there is none.
+MOE_DEV bool group_sums(const GroupArgs& g, TileArgs& a, TileIndex& x) {
+  DwTile t;
+  if (!dw_tile(g, g.offsets, dw_run(g), blockIdx.x / 8, t)) return false;
+  a = g.tile;
+  x = {0, t.ti, t.tj, 0, 1};
+  a.R = t.rows;
+  a.a[0] = (const uint16_t*)(t.m ? a.a[1] : a.a[0]) + t.row0 * a.lda[0];
+  a.b[0] = (const uint16_t*)a.b[0] + t.row0 * a.ldb[0];
+  a.epi.y[0] = (uint16_t*)(t.m ? a.epi.y[1] : a.epi.y[0]) + t.e * g.stride;
+  return true;
 }
 
 // The dW of an expert without rows.
@@ -136,7 +155,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_group_big(GroupArgs g) {
   TileArgs a;
   TileIndex x;
   if constexpr (OA == kCols) {
-    group_sums(g, a, x);
+    if (!group_sums(g, a, x)) return;
     if (a.R == 0) return zero_tile<T, 64 * WI * WJ>(a, (int64_t)x.ti * TI, TI, (int64_t)x.tj * TJ, TJ);
   } else if (!group_rows<TI>(g, a, x)) {
     return;
@@ -150,7 +169,7 @@ __global__ __launch_bounds__(256, 2) void k_group_deep(GroupArgs g) {
   TileArgs a;
   TileIndex x;
   if constexpr (OA == kCols) {
-    group_sums(g, a, x);
+    if (!group_sums(g, a, x)) return;
     if (a.R == 0) return zero_tile<T, 256>(a, (int64_t)x.ti * 64, 64, (int64_t)x.tj * 64, 64);
   } else if (!group_rows<64>(g, a, x)) {
     return;
@@ -165,12 +184,68 @@ __global__ __launch_bounds__(256, 2) void k_group_any(GroupArgs g) {
   TileArgs a;
   TileIndex x;
   if constexpr (OA == kCols) {
-    group_sums(g, a, x);
+    if (!group_sums(g, a, x)) return;
     if (a.R == 0) return zero_tile<T, 256>(a, (int64_t)x.ti * TT, TT, (int64_t)x.tj * TT, TT);
   } else if (!group_rows<TT>(g, a, x)) {
     return;
   }
   any_tile<T, OA, OB, KIND, F>(a, x, lds);
+}
+
+// Mean rows of an expert up to which dW takes k_group_dw.  Against the best of the pipelined tiles, lengths spread
+// exponentially, 768 x 2048: 512 experts of 20 rows 337 and 356 us, of 80 rows 467 and 473; 64 of 640 rows 174 and 184;
+// 16 of 2048 rows 121 and 158; 8 of 4096 rows, 4096 x 4096, 931 and 922.
+constexpr int kShortRows = 2048;
+
+// dW of experts with few rows: 128 x 128 tile, 4 waves of 64 x 64.  A reduction of a step or two is over before a pipeline has
+// filled, so there is none: a step's operands come into one LDS buffer of 32 KB, and the four workgroups that fit a CU
+// cover each other's loads and stores.  A wave's results leave as whole 128-byte lines.
+template <typename T, int WJ>
+__global__ __launch_bounds__(128 * WJ, 4) void k_group_dw(GroupArgs g) {
+  constexpr int HI = 128, HJ = 64 * WJ, W = 2 * WJ, F = 4;
+  typedef typename Operand<T>::v8 v8;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[(HI + HJ) * kStepR > W * 4096 ? (HI + HJ) * kStepR : W * 4096];
+  TileArgs a;
+  TileIndex x;
+  if (!group_sums(g, a, x)) return;
+  const int64_t i0 = (int64_t)x.ti * HI, j0 = (int64_t)x.tj * HJ;
+  if (a.R == 0) return zero_tile<T, 64 * W>(a, i0, HI, j0, HJ);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave / WJ, wj = wave % WJ;
+  const int steps = (a.R + kStepR - 1) / kStepR;
+  OperandCopy<kCols, HI, W> ca;
+  OperandCopy<kCols, HJ, W> cb;
+  HalfStream<kCols, HI, W, false> sa;
+  HalfStream<kCols, HJ, W, false> sb;
+  ca.init(a.lda[0], wave, lane);
+  cb.init(a.ldb[0], wave, lane);
+  sa.init(ca, a.a[0], nullptr, a.lda[0], 0, i0, a.M, a.R, steps, 0, steps);
+  sb.init(cb, a.b[0], nullptr, a.ldb[0], 0, j0, a.N, a.R, steps, 0, steps);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds;
+  const uint32_t addr_a = frag_addr<kCols, HI>(lds0, wi * 64, lane);
+  const uint32_t addr_b = frag_addr<kCols, HJ>(lds0 + 2 * HI * kStepR, wj * 64, lane);
+  float4v acc[F][F] = {};
+  for (int k = 0; k < steps; ++k) {
+    sa.issue(ca, lds0 + wave * 1024);
+    sb.issue(cb, lds0 + 2 * HI * kStepR + wave * 1024);
+    copies_barrier<0>();
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      v8 fa[F], fb[F];
+#pragma unroll
+      for (int n = 0; n < F; ++n) {
+        fa[n] = read_frag<T, kCols, HI>(addr_a, n, kk, 0);
+        fb[n] = read_frag<T, kCols, HJ>(addr_b, n, kk, 0);
+      }
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int n = 0; n < F; ++n) acc[f][n] = Operand<T>::mma(fb[n], fa[f], acc[f][n]);
+    }
+    copies_barrier<0>();  // every wave has read the step
+  }
+  store_block<T, F, F>(a.epi.y[0], a.epi.ldy[0], i0 + wi * 64, j0 + wj * 64, a.M, a.N, a.epi.stream, acc, lds + wave * 4096, lane);
 }
 
 // The tile with the least estimated time, by the costs measured for the dense products (TileCost).  The rows of an
@@ -214,7 +289,7 @@ bool group_grid(GroupArgs& g, int tile, int threads, uint32_t* grid) {
   int64_t count;
   if (OA == kCols) {
     g.tile.tiles_i = (g.tile.M + tile - 1) / tile;
-    count = (int64_t)g.E * g.mats * g.tile.tiles_i * g.tile.tiles_j;
+    count = (int64_t)g.E * g.mats * (((int64_t)g.tile.tiles_i * g.tile.tiles_j + 7) / 8) * 8;
   } else {
     count = most_tiles(g, tile) * g.tile.tiles_j;
   }
@@ -235,6 +310,13 @@ hipError_t launch_experts(const GroupArgs& args, hipStream_t st) {
   const double out = OA == kCols ? 2.0 * g.E * g.mats * g.tile.M * g.tile.N : 2.0 * g.P * g.tile.N;
   g.tile.epi.stream = out >= 16e6;
   uint32_t grid;
+  if constexpr (OA == kCols) {
+    if (whole && g_dense_plan.kernel == MOE_DENSE_AUTO && g.P <= kShortRows * (int64_t)g.E) {
+      if (!group_grid<OA, KIND>(g, 128, 256, &grid)) return hipErrorInvalidConfiguration;
+      k_group_dw<T, 2><<<grid, 256, 0, st>>>(g);
+      return hipGetLastError();
+    }
+  }
   switch (kernel) {
     case MOE_DENSE_TILE64:
       if (!group_grid<OA, KIND>(g, 64, 256, &grid)) return hipErrorInvalidConfiguration;

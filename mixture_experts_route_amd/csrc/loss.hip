@@ -14,7 +14,7 @@ constexpr size_t kLossDzBytes = 256u << 20;  // dz of a piece, about
 constexpr int kLossTile = 64;              // the smallest tile's columns
 
 struct LossWs {
-  size_t part, zt, scale, x, w, dz, acc, sums, sums_bytes, total;
+  size_t part, scale, x, w, dz, acc, sums, sums_bytes, total;
   int64_t ld_in, piece, ldz;
 };
 
@@ -34,8 +34,6 @@ static LossWs loss_ws(const moe_loss_dims* d, int64_t T, bool backward) {
   size_t off = kCtrlBytes;
   L.scale = off;
   off = dense_align(off + 2 * sizeof(float));
-  L.zt = off;
-  off = dense_align(off + sizeof(float) * chunk);
   L.part = off;
   off = dense_align(off + sizeof(float2) * (size_t)(chunk * ((V + kLossTile - 1) / kLossTile)));
   // copies of operands without whole 16-byte rows: x always (its stride is the caller's), the weights when n_in says so
@@ -64,62 +62,86 @@ static LossWs loss_ws(const moe_loss_dims* d, int64_t T, bool backward) {
 
 struct LossJoinArgs {
   const float2* part;
-  const float* zt;
+  const void *x, *w;
   const int32_t* targets;
   float *loss, *lse;
   int32_t* ctrl;
-  int32_t T, tiles, vocab, ignore;
+  int64_t ldx, ldw;
+  int32_t T, tiles, vocab, ignore, K;
 };
 
 // A token's tiles joined: with m, s the maximum and sum of the other columns and zt the target's logit,
 //   loss = log(1 + s exp(m - zt)) or, with zt below m, (m - zt) + log(s + exp(zt - m));  lse = zt + loss likewise.
-// BLOCK tokens per workgroup share its 256 threads; a token's tiles are joined in a fixed order.  Memory-bound.
-template <int BLOCK>
+// zt is summed here, in 64 bits (16-bit products are exact in 32): a sure token's loss is nothing but its distance from the
+// others, and the target's logit, the largest in magnitude, would bring the most error into it.
+// BLOCK tokens per workgroup share its 256 threads: neighbouring threads have neighbouring tokens while they read the
+// tiles, and parts of the same token, in one wave, for the rest.  Every order is fixed.  Bound by the latency of a few dependent
+// loads at small sizes, then by memory.
+template <typename T, int BLOCK>
 __global__ __launch_bounds__(256) void k_loss_join(LossJoinArgs a) {
   constexpr int kShares = 256 / BLOCK;
-  __shared__ float ms[256], ss[256];
-  const int t = blockIdx.x * BLOCK + threadIdx.x % BLOCK, share = threadIdx.x / BLOCK;
-  float m = -INFINITY, s = 0.0f;
-  if (t < a.T) {
-    for (int i = share; i < a.tiles; i += kShares * 8) {
-      float2 p[8];
+  static_assert(kShares <= 64, "a token's threads are in one wave");
+  __shared__ float ms[kShares][BLOCK + 1], ss[kShares][BLOCK + 1];
+  const int t = blockIdx.x * BLOCK + threadIdx.x / kShares, part = threadIdx.x % kShares;
+  double zt = 0.0;
+  const int target = t < a.T ? a.targets[t] : -1;
+  const bool live = t < a.T && (uint32_t)target < (uint32_t)a.vocab && target != a.ignore;
+  if (live) {
+#pragma unroll 4
+    for (int c = part * 8; c < a.K; c += kShares * 8) {
+      const int n = a.K - c < 8 ? a.K - c : 8;
+      float u[8], v[8];
+      load8<T>(a.x, t * a.ldx + c, n, u);
+      load8<T>(a.w, target * a.ldw + c, n, v);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int at = i + u * kShares;
-        p[u] = a.part[(int64_t)(at < a.tiles ? at : i) * a.T + t];
-        if (at >= a.tiles) p[u] = make_float2(-INFINITY, 0.0f);
-      }
-      float most = m;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) most = fmaxf(most, p[u].x);
-      const float base = __builtin_isinf(most) ? 0.0f : most;
-      s = m == most ? s : s * expf(m - base);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) s += p[u].x == most ? p[u].y : p[u].y * expf(p[u].x - base);
-      m = most;
+      for (int i = 0; i < 8; ++i) zt += (double)(u[i] * v[i]);
     }
   }
-  ms[threadIdx.x] = m;
-  ss[threadIdx.x] = s;
-  __syncthreads();
-  if (share || t >= a.T) return;
-  for (int i = 1; i < kShares; ++i) m = fmaxf(m, ms[threadIdx.x + i * BLOCK]);
-  const float base = __builtin_isinf(m) ? 0.0f : m;
-  s = 0.0f;
-  for (int i = 0; i < kShares; ++i) {
-    const float mi = ms[threadIdx.x + i * BLOCK], si = ss[threadIdx.x + i * BLOCK];
-    s += mi == m ? si : si * expf(mi - base);
+  {
+    const int to = blockIdx.x * BLOCK + threadIdx.x % BLOCK, share = threadIdx.x / BLOCK;
+    float m = -INFINITY, s = 0.0f;
+    if (to < a.T) {
+      for (int i = share; i < a.tiles; i += kShares * 8) {
+        float2 p[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int at = i + u * kShares;
+          p[u] = a.part[(int64_t)(at < a.tiles ? at : i) * a.T + to];
+          if (at >= a.tiles) p[u] = make_float2(-INFINITY, 0.0f);
+        }
+        float most = m;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) most = fmaxf(most, p[u].x);
+        const float base = not_infinite(most);
+        s = m == most ? s : s * exp_below(m, base);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += p[u].x == most ? p[u].y : p[u].y * exp_below(p[u].x, base);
+        m = most;
+      }
+    }
+    ms[share][threadIdx.x % BLOCK] = m;
+    ss[share][threadIdx.x % BLOCK] = s;
   }
-  const int target = a.targets[t];
+  __syncthreads();
+  float m = ms[part][threadIdx.x / kShares], s = ss[part][threadIdx.x / kShares];
+#pragma unroll
+  for (int o = 1; o < kShares; o <<= 1) {
+    const float mo = __shfl_xor(m, o, 64), so = __shfl_xor(s, o, 64), most = fmaxf(m, mo), base = not_infinite(most);
+    const float mine = m == most ? s : s * exp_below(m, base), other = mo == most ? so : so * exp_below(mo, base);
+    s = mine + other;
+    m = most;
+    zt += __shfl_xor(zt, o, 64);
+  }
+  if (part || t >= a.T) return;
   float loss = 0.0f, lse = 0.0f;
-  if ((uint32_t)target < (uint32_t)a.vocab && target != a.ignore) {
-    const float z = a.zt[t];
+  if (live) {
+    const float z = (float)zt;
     if (z >= m) {
-      loss = log1pf(s * expf(m - z));
+      loss = log1pf(s * expf((float)(m - zt)));
       lse = z + loss;
     } else {
-      const float rest = logf(s + expf(z - m));
-      loss = (m - z) + rest;
+      const float rest = logf(s + expf((float)(zt - m)));
+      loss = (float)((m - zt) + rest);
       lse = m + rest;
     }
   } else if (target != a.ignore) {
@@ -128,6 +150,13 @@ __global__ __launch_bounds__(256) void k_loss_join(LossJoinArgs a) {
   }
   a.loss[t] = loss;
   a.lse[t] = lse;
+}
+
+template <typename T>
+static hipError_t start_join(const LossJoinArgs& j, hipStream_t st) {
+  if (j.T >= 4096) k_loss_join<T, 16><<<(j.T + 15) / 16, 256, 0, st>>>(j);
+  else k_loss_join<T, 4><<<(j.T + 3) / 4, 256, 0, st>>>(j);
+  return hipGetLastError();
 }
 
 // fp16's dz is kept in its normal range by a power of two S with S max|dloss| in [2^11, 2^12): at most 4096 for a target, normal
@@ -219,22 +248,22 @@ MOE_API int moe_loss_forward(const moe_loss_dims* dims, const void* x, int64_t l
     a.pack_a = (uint16_t*)at(L.x);
     a.pack_b[0] = L.w ? (uint16_t*)at(L.w) : nullptr;
     a.epi.loss.part = (float2*)at(L.part);
-    a.epi.loss.zt = (float*)at(L.zt);
     LossJoinArgs j{};
     if ((rc = dense_status(dims->dtype == MOE_BF16 ? launch_loss_bf16(a, &j.tiles, st) : launch_loss_f16(a, &j.tiles, st)))) return rc;
     j.part = a.epi.loss.part;
-    j.zt = a.epi.loss.zt;
+    j.x = a.a[0];
+    j.w = w;
+    j.ldx = ldx;
+    j.ldw = ldw;
     j.targets = targets + t0;
     j.loss = loss + t0;
     j.lse = lse + t0;
     j.ctrl = (int32_t*)ws;
     j.T = a.M;
+    j.K = dims->n_in;
     j.vocab = dims->vocab;
     j.ignore = dims->ignore;
-    if (a.M >= 16) k_loss_join<16><<<(a.M + 15) / 16, 256, 0, st>>>(j);
-    else if (a.M >= 4) k_loss_join<4><<<(a.M + 3) / 4, 256, 0, st>>>(j);
-    else k_loss_join<1><<<a.M, 256, 0, st>>>(j);
-    if (hipGetLastError() != hipSuccess) return MOE_EHIP;
+    if ((rc = dense_status(dims->dtype == MOE_BF16 ? start_join<__bf16>(j, st) : start_join<_Float16>(j, st)))) return rc;
   }
   return MOE_OK;
 }
