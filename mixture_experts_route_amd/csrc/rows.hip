@@ -23,8 +23,14 @@ struct RowsArgs {
   int64_t ld_src, ld_ys, ld_res, ld_dst;
   int32_t T, k, P, H;
   int32_t shift;        // log2 of the span
-  int32_t blocks;       // combine's backward: workgroups that take tokens; the others look after padding rows
+  int32_t blocks;       // workgroups that take tokens; those behind them look after padding rows
 };
+
+// A thread's chunk at column c of a row of H: the 8 elements from the returned column on.  The last chunk of an odd width begins
+// earlier, inside the one before it, so that every access is a whole 16 bytes; the elements that both have are written
+// twice with the same value.  Rows under 8 elements are one short chunk.
+MOE_DEV int chunk_at(int c, int H) { return c + 8 <= H || H < 8 ? c : H - 8; }
+MOE_DEV int chunk_len(int H) { return H < 8 ? H : 8; }
 
 constexpr int kInvPairs = 2048;  // pairs and rows whose inverse map one workgroup makes in LDS
 
@@ -48,80 +54,127 @@ __global__ __launch_bounds__(256) void k_inv_clear(int32_t* inv, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) inv[i] = -1;
 }
 
-// xs[r] = x[perm[r] / k], four rows of a thread in flight.  SMALL: the last workgroup makes inv; otherwise it is -1
-// already, and each row enters itself (the highest row where a pair has several, whatever the order).
-template <typename T, bool SMALL>
-__global__ __launch_bounds__(256) void k_dispatch(RowsArgs a) {
-  __shared__ int32_t map[SMALL ? kInvPairs : 1];
-  if constexpr (SMALL) {
-    if (blockIdx.x == gridDim.x - 1) {
-      invert_small(a, map);
-      return;
+// Each row enters itself: the highest one where a pair has several, whatever the order.
+__global__ __launch_bounds__(256) void k_inv_fill(RowsArgs a) {
+  const int64_t pairs = (int64_t)a.T * a.k;
+  for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < a.P; r += (int64_t)gridDim.x * 256) {
+    const int p = a.perm[r];
+    if (p >= 0 && p < pairs) atomicMax(&a.inv[p], (int32_t)r);
+  }
+}
+
+// Zeros in the rows that are no pair's, by the workgroups from a.blocks on: padding rows, and the rows of a bad layout
+// (a pair out of range, a pair that another row has), which are reported.
+template <typename T>
+MOE_DEV void zero_rows(const RowsArgs& a) {
+  const int64_t pairs = (int64_t)a.T * a.k;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t movers = (int64_t)(gridDim.x - a.blocks) * 4;
+  for (int64_t r0 = ((int64_t)(blockIdx.x - a.blocks) * 4 + wave) * 64; r0 < a.P; r0 += movers * 64) {
+    const int64_t r = r0 + lane;
+    bool zero = false;
+    if (r < a.P) {
+      const int32_t p = a.perm[r];
+      if (p >= 0) {
+        zero = p >= pairs || a.inv[p] != r;
+        if (zero) set_error(a.ctrl, MOE_DERR_ROWS);
+      } else {
+        zero = true;
+      }
     }
+    uint64_t todo = __ballot(zero);
+    if (!a.dst) continue;
+    while (todo) {
+      const int64_t row = r0 + __ffsll((unsigned long long)todo) - 1;
+      todo &= todo - 1;
+      float v[8] = {};
+      for (int c = lane * 8; c < a.H; c += 512) store8<T>(a.dst, row * a.ld_dst + chunk_at(c, a.H), chunk_len(a.H), v);
+    }
+  }
+}
+
+// The dispatch of a few pairs in one launch, row by row: xs[r] = x[perm[r] / k], four rows of a thread in flight; the last
+// workgroup makes inv.
+template <typename T>
+__global__ __launch_bounds__(256) void k_dispatch_few(RowsArgs a) {
+  __shared__ int32_t map[kInvPairs];
+  if (blockIdx.x == gridDim.x - 1) {
+    invert_small(a, map);
+    return;
   }
   typedef typename Operand<T>::v8 v8;
   typedef v8 v8_any __attribute__((aligned(2)));
   constexpr int U = 4;
   const int span = 1 << a.shift, per = 256 >> a.shift;
   const int lane = threadIdx.x & (span - 1), slot = threadIdx.x >> a.shift;
-  const int64_t movers = gridDim.x - (SMALL ? 1 : 0);
-  const int64_t pairs = (int64_t)a.T * a.k;
-  for (int64_t base = (int64_t)blockIdx.x * per * U; base < a.P; base += movers * per * U) {
-    int32_t pair[U];
-    const T* src[U];
-    T* dst[U];
+  const int base = blockIdx.x * per * U, pairs = a.T * a.k;
+  int32_t pair[U];
+  const T* src[U];
+  T* dst[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = base + u * per + slot;
-      pair[u] = r < a.P ? a.perm[r] : -1;
+  for (int u = 0; u < U; ++u) {
+    const int r = base + u * per + slot;
+    pair[u] = r < a.P ? a.perm[r] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (pair[u] >= pairs) {
+      if (lane == 0) set_error(a.ctrl, MOE_DERR_ROWS);
+      pair[u] = -1;
     }
+    src[u] = (const T*)a.src + (int64_t)(pair[u] < 0 ? 0 : pair[u] / a.k) * a.ld_src;
+    dst[u] = (T*)a.dst + (int64_t)(base + u * per + slot) * a.ld_dst;
+  }
+  for (int col = lane * 8; col < a.H; col += span * 8) {
+    const int c = chunk_at(col, a.H);
+    if (a.H >= 8) {
+      v8 v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = base + u * per + slot;
-      if (pair[u] >= pairs) {
-        if (lane == 0) set_error(a.ctrl, MOE_DERR_ROWS);
-        pair[u] = -1;
+      for (int u = 0; u < U; ++u) v[u] = *(const v8_any*)(src[u] + c);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (pair[u] < 0) v[u] = v8{};
+        if (base + u * per + slot < a.P) *(v8_any*)(dst[u] + c) = v[u];
       }
-      if (!SMALL && lane == 0 && pair[u] >= 0 && atomicMax(&a.inv[pair[u]], (int32_t)r) != -1) set_error(a.ctrl, MOE_DERR_ROWS);
-      src[u] = (const T*)a.src + (int64_t)(pair[u] < 0 ? 0 : pair[u] / a.k) * a.ld_src;
-      dst[u] = (T*)a.dst + r * a.ld_dst;
-    }
-    for (int c = lane * 8; c < a.H; c += span * 8) {
-      const int n = a.H - c;
-      if (n >= 8) {
-        v8 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = *(const v8_any*)(src[u] + c);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (pair[u] < 0) v[u] = v8{};
-          if (base + u * per + slot < a.P) *(v8_any*)(dst[u] + c) = v[u];
-        }
-      } else {
-        for (int u = 0; u < U; ++u)
-          if (base + u * per + slot < a.P)
-            for (int i = 0; i < n; ++i) dst[u][c + i] = pair[u] < 0 ? (T)0.0f : src[u][c + i];
-      }
+    } else {
+      for (int u = 0; u < U; ++u)
+        if (base + u * per + slot < a.P)
+          for (int i = 0; i < a.H; ++i) dst[u][i] = pair[u] < 0 ? (T)0.0f : src[u][i];
     }
   }
+}
+
+// The 8 elements of a chunk as they are stored (the first n, zeros after them).
+template <typename T>
+MOE_DEV typename Operand<T>::v8 load_raw(const void* base, int64_t off, int n) {
+  typedef typename Operand<T>::v8 v8;
+  typedef v8 v8_any __attribute__((aligned(2)));
+  const T* p = (const T*)base + off;
+  if (n == 8) return *(const v8_any*)p;
+  v8 v = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) v[i] = p[i];
+  return v;
 }
 
 // acc += the chunks of N rows of a token, all loads before the sums.  An absent row reads row 0, which exists, and
 // is left out by a select, so that nothing of it (a NaN) arrives.
 template <typename T, int N, bool WEIGHTS, typename Row, typename Weight>
 MOE_DEV void add_rows(const RowsArgs& a, int j0, int c, int n, Row row, Weight weight, float (&acc)[8]) {
-  float v[N][8];
+  typename Operand<T>::v8 v[N];
   int32_t r[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     r[j] = row(j0 + j);
-    load8<T>(a.src, (int64_t)(r[j] < 0 ? 0 : r[j]) * a.ld_src + c, n, v[j]);
+    v[j] = load_raw<T>(a.src, (int64_t)(r[j] < 0 ? 0 : r[j]) * a.ld_src + c, n);
   }
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const float w = WEIGHTS ? weight(j0 + j) : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = r[j] < 0 ? acc[i] : (WEIGHTS ? fmaf(w, v[j][i], acc[i]) : acc[i] + v[j][i]);
+    for (int i = 0; i < 8; ++i) acc[i] = r[j] < 0 ? acc[i] : (WEIGHTS ? fmaf(w, (float)v[j][i], acc[i]) : acc[i] + (float)v[j][i]);
   }
 }
 
@@ -158,9 +211,11 @@ struct Choices {
   }
 };
 
-// y[t] = sum_j w[t][j] rows[inv[t][j]] + r[t] (WEIGHTS), or without the weights; Y the type of y and r.
-template <typename T, typename Y, bool WEIGHTS, bool WIDE>
+// y[t] = sum_j w[t][j] rows[inv[t][j]] + r[t] (WEIGHTS), or without the weights; Y the type of y and r.  K: the number of
+// choices, all of whose rows are then on their way at once, or 0: any number, in groups (narrow rows).
+template <typename T, typename Y, bool WEIGHTS, int K>
 __global__ __launch_bounds__(256) void k_combine(RowsArgs a) {
+  constexpr bool WIDE = K > 0;
   const int span = 1 << a.shift, per = 256 >> a.shift;
   const int lane = threadIdx.x & (span - 1);
   int slot = threadIdx.x >> a.shift;
@@ -173,55 +228,65 @@ __global__ __launch_bounds__(256) void k_combine(RowsArgs a) {
         if (ch.inv[j] >= a.P) set_error(a.ctrl, MOE_DERR_ROWS);
     auto row = [&](int j) { return ch.row(j); };
     auto weight = [&](int j) { return ch.weight(j); };
-    for (int c = lane * 8; c < a.H; c += span * 8) {
-      const int n = a.H - c < 8 ? a.H - c : 8;
-      float acc[8] = {};
-      int j = 0;
-      for (; j + 8 <= a.k; j += 8) add_rows<T, 8, WEIGHTS>(a, j, c, n, row, weight, acc);
-      if (a.k & 4) {
-        add_rows<T, 4, WEIGHTS>(a, j, c, n, row, weight, acc);
-        j += 4;
+    for (int col = lane * 8; col < a.H; col += span * 8) {
+      const int c = chunk_at(col, a.H), n = chunk_len(a.H);
+      float acc[8] = {}, r[8] = {};
+      if (a.res) load8<Y>(a.res, t * a.ld_res + c, n, r);
+      if constexpr (K > 0) {
+        add_rows<T, K, WEIGHTS>(a, 0, c, n, row, weight, acc);
+      } else {
+        int j = 0;
+        for (; j + 8 <= a.k; j += 8) add_rows<T, 8, WEIGHTS>(a, j, c, n, row, weight, acc);
+        if (a.k & 4) {
+          add_rows<T, 4, WEIGHTS>(a, j, c, n, row, weight, acc);
+          j += 4;
+        }
+        if (a.k & 2) {
+          add_rows<T, 2, WEIGHTS>(a, j, c, n, row, weight, acc);
+          j += 2;
+        }
+        if (a.k & 1) add_rows<T, 1, WEIGHTS>(a, j, c, n, row, weight, acc);
       }
-      if (a.k & 2) {
-        add_rows<T, 2, WEIGHTS>(a, j, c, n, row, weight, acc);
-        j += 2;
-      }
-      if (a.k & 1) add_rows<T, 1, WEIGHTS>(a, j, c, n, row, weight, acc);
       if (a.res) {
-        float v[8];
-        load8<Y>(a.res, t * a.ld_res + c, n, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += v[i];
+        for (int i = 0; i < 8; ++i) acc[i] += r[i];
       }
       store8<Y>(a.dst, t * a.ld_dst + c, n, acc);
     }
   }
 }
 
-// dys and dw of N of a token's choices for one chunk: dot[j] += dy . ys[row], dys[row] = w dy.
-template <typename T, int N>
-MOE_DEV void grad_rows_of(const RowsArgs& a, int c, int n, const float (&dy)[8], const int32_t* row, const float* w, float* dot) {
-  if (a.dw) {
-    float v[N][8];
-#pragma unroll
-    for (int j = 0; j < N; ++j) load8<T>(a.ys, (int64_t)(row[j] < 0 ? 0 : row[j]) * a.ld_ys + c, n, v[j]);
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      float s = dot[j];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(dy[i], v[j][i], s);  // both zero past the row's end
-      dot[j] = row[j] < 0 ? 0.0f : s;
-    }
-  }
-  if (a.dst) {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (row[j] >= 0) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = w[j] * dy[i];
-        store8<T>(a.dst, (int64_t)row[j] * a.ld_dst + c, n, v);
+// The dispatch, token by token once inv is there: x is read once and written to its token's rows (row by row 32768 tokens'
+// ten rows of 2048 took 437 us: every row read again from memory).
+template <typename T, bool WIDE>
+__global__ __launch_bounds__(256) void k_dispatch(RowsArgs a) {
+  if ((int)blockIdx.x >= a.blocks) return zero_rows<T>(a);
+  typedef typename Operand<T>::v8 v8;
+  typedef v8 v8_any __attribute__((aligned(2)));
+  const int span = 1 << a.shift, per = 256 >> a.shift;
+  const int lane = threadIdx.x & (span - 1);
+  int slot = threadIdx.x >> a.shift;
+  if (WIDE) slot = __builtin_amdgcn_readfirstlane(slot);
+  for (int64_t t = (int64_t)blockIdx.x * per + slot; t < a.T; t += (int64_t)a.blocks * per) {
+    Choices<WIDE> ch;
+    ch.init(a, t, false);
+    const T* src = (const T*)a.src + t * a.ld_src;
+    for (int col = lane * 8; col < a.H; col += span * 8) {
+      const int c = chunk_at(col, a.H);
+      if (a.H >= 8) {
+        const v8 v = *(const v8_any*)(src + c);
+        for (int j = 0; j < a.k; ++j) {
+          const int32_t r = ch.row(j);
+          if (r >= 0) *(v8_any*)((T*)a.dst + r * a.ld_dst + c) = v;
+        }
+      } else {
+        for (int j = 0; j < a.k; ++j) {
+          const int32_t r = ch.row(j);
+          if (r >= 0)
+            for (int i = 0; i < a.H; ++i) ((T*)a.dst)[r * a.ld_dst + i] = src[i];
+        }
       }
+    }
   }
 }
 
@@ -231,40 +296,14 @@ MOE_DEV void grad_rows_of(const RowsArgs& a, int c, int n, const float (&dy)[8],
 template <typename T, typename Y>
 __global__ __launch_bounds__(256) void k_combine_grad(RowsArgs a) {
   __shared__ float sums[4][kMaxK];
-  const int64_t pairs = (int64_t)a.T * a.k;
-  if ((int)blockIdx.x >= a.blocks) {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t movers = (int64_t)(gridDim.x - a.blocks) * 4;
-    for (int64_t r0 = ((int64_t)(blockIdx.x - a.blocks) * 4 + wave) * 64; r0 < a.P; r0 += movers * 64) {
-      const int64_t r = r0 + lane;
-      bool zero = false;
-      if (r < a.P) {
-        const int32_t p = a.perm[r];
-        if (p >= 0) {
-          zero = p >= pairs || a.inv[p] != r;
-          if (zero) set_error(a.ctrl, MOE_DERR_ROWS);
-        } else {
-          zero = true;
-        }
-      }
-      uint64_t todo = __ballot(zero);
-      if (!a.dst) continue;
-      while (todo) {
-        const int64_t row = r0 + __ffsll((unsigned long long)todo) - 1;
-        todo &= todo - 1;
-        float v[8] = {};
-        for (int c = lane * 8; c < a.H; c += 512) store8<T>(a.dst, row * a.ld_dst + c, a.H - c < 8 ? a.H - c : 8, v);
-      }
-    }
-    return;
-  }
+  if ((int)blockIdx.x >= a.blocks) return zero_rows<T>(a);
   const int span = 1 << a.shift, per = 256 >> a.shift;
   const int lane = threadIdx.x & (span - 1), slot = threadIdx.x >> a.shift;
   for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < a.T; t0 += (int64_t)a.blocks * per) {
     const int64_t t = t0 + slot;
     const bool live = t < a.T;
     for (int j0 = 0; j0 < a.k; j0 += 4) {
-      int32_t row[4];
+      int32_t row[4], pair[4];
       float w[4], dot[4] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -273,18 +312,46 @@ __global__ __launch_bounds__(256) void k_combine_grad(RowsArgs a) {
         w[j] = on && a.dst ? a.w[t * a.k + j0 + j] : 0.0f;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (row[j] >= 0 && (row[j] >= a.P || a.perm[row[j]] != t * a.k + j0 + j)) {
+      for (int j = 0; j < 4; ++j) {
+        if (row[j] >= a.P) {
           if (lane == 0) set_error(a.ctrl, MOE_DERR_ROWS);
           row[j] = -1;
         }
-      if (live)
-        for (int c = lane * 8; c < a.H; c += span * 8) {
-          const int n = a.H - c < 8 ? a.H - c : 8;
-          float dy[8];
-          load8<Y>(a.src, t * a.ld_src + c, n, dy);
-          grad_rows_of<T, 4>(a, c, n, dy, row, w, dot);
-        }
+        pair[j] = a.perm[row[j] < 0 ? 0 : row[j]];  // compared after the rows' loads have left
+      }
+      for (int col = lane * 8; live && col < a.H; col += span * 8) {
+        const int c = chunk_at(col, a.H), n = chunk_len(a.H);
+        float dy[8];
+        typename Operand<T>::v8 v[4];
+        load8<Y>(a.src, t * a.ld_src + c, n, dy);
+        if (a.dw)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = load_raw<T>(a.ys, (int64_t)(row[j] < 0 ? 0 : row[j]) * a.ld_ys + c, n);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (row[j] >= 0 && pair[j] != t * a.k + j0 + j) {
+            if (lane == 0) set_error(a.ctrl, MOE_DERR_ROWS);
+            row[j] = -1;
+          }
+        if (a.dst)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (row[j] >= 0) {
+              float o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = w[j] * dy[i];
+              store8<T>(a.dst, (int64_t)row[j] * a.ld_dst + c, n, o);
+            }
+        if (a.dw)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float s = dot[j];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = i < col - c ? s : fmaf(dy[i], (float)v[j][i], s);  // (zeros past a short row's end)
+            dot[j] = row[j] < 0 ? 0.0f : s;
+          }
+      }
       if (!a.dw) continue;
       const int inner = span < 64 ? span : 64;
 #pragma unroll
@@ -311,11 +378,14 @@ __global__ __launch_bounds__(256) void k_combine_grad(RowsArgs a) {
   }
 }
 
-// Threads per row: the power of two from 8 to `most` that idles the fewest in a row of `chunks` 16-byte chunks.
+// Threads per row: of the powers of two up to `most` that take a row of `chunks` 16-byte chunks in at most four passes, or the
+// largest, the one that idles the fewest; the larger of two that idle as many.  (8 threads for 168 chunks, which idle none,
+// took 72 us where 64 take 51: 8191 tokens' four rows.)
 static int span_shift(int chunks, int most) {
   int best = 3;
   int64_t waste = INT64_MAX;
   for (int s = 3; (1 << s) <= most; ++s) {
+    if (chunks > 4 << s && (2 << s) <= most) continue;
     const int64_t n = ((int64_t)chunks + (1 << s) - 1) / (1 << s) << s;
     if (n <= waste) {
       waste = n;
@@ -326,40 +396,59 @@ static int span_shift(int chunks, int most) {
 }
 static uint32_t grid_of(int64_t blocks) { return (uint32_t)(blocks < (1 << 20) ? blocks : 1 << 20); }
 
+// Threads of a token: up to 256 while fewer than `wave` tokens leave room for them, else a wave at most.
+static int token_span(int64_t T, int H, int64_t wave) { return span_shift((H + 7) / 8, T < wave ? 256 : 64); }
+static uint32_t row_blocks(int64_t P) { return (uint32_t)((P + 255) / 256 < 1024 ? (P + 255) / 256 : 1024); }
+
 template <typename T>
 static hipError_t start_dispatch(RowsArgs a, hipStream_t st) {
   const int64_t pairs = (int64_t)a.T * a.k;
-  a.shift = span_shift((a.H + 7) / 8, 256);
-  const int64_t per = (256 >> a.shift) * 4;
-  const uint32_t grid = grid_of((a.P + per - 1) / per);
   if (pairs <= kInvPairs && a.P <= kInvPairs) {
-    k_dispatch<T, true><<<grid + 1, 256, 0, st>>>(a);
+    a.shift = span_shift((a.H + 7) / 8, 256);
+    const int per = (256 >> a.shift) * 4;
+    k_dispatch_few<T><<<(a.P + per - 1) / per + 1, 256, 0, st>>>(a);
     return hipGetLastError();
   }
-  const int64_t clear = (pairs + 1023) / 1024;
+  const int64_t clear = (pairs + 1023) / 1024, fill = ((int64_t)a.P + 255) / 256;
   k_inv_clear<<<(uint32_t)(clear < 4096 ? clear : 4096), 256, 0, st>>>(a.inv, pairs);
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_dispatch<T, false><<<grid, 256, 0, st>>>(a);
+  k_inv_fill<<<grid_of(fill), 256, 0, st>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  a.shift = token_span(a.T, a.H, 16384);
+  const int64_t per = 256 >> a.shift;
+  a.blocks = (int32_t)grid_of((a.T + per - 1) / per);
+  if (a.shift >= 6) k_dispatch<T, true><<<a.blocks + row_blocks(a.P), 256, 0, st>>>(a);
+  else k_dispatch<T, false><<<a.blocks + row_blocks(a.P), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, typename Y, bool WEIGHTS>
 static hipError_t start_combine(RowsArgs a, hipStream_t st) {
-  a.shift = span_shift((a.H + 7) / 8, a.T < 2048 ? 256 : 64);
+  a.shift = token_span(a.T, a.H, 16384);
   const int64_t per = 256 >> a.shift;
   const uint32_t grid = grid_of((a.T + per - 1) / per);
-  if (a.shift >= 6) k_combine<T, Y, WEIGHTS, true><<<grid, 256, 0, st>>>(a);
-  else k_combine<T, Y, WEIGHTS, false><<<grid, 256, 0, st>>>(a);
+#define MOE_COMBINE_CASE(K)                                          \
+  case K:                                                            \
+    k_combine<T, Y, WEIGHTS, K><<<grid, 256, 0, st>>>(a);            \
+    break;
+  switch (a.shift >= 6 ? a.k : 0) {
+    MOE_COMBINE_CASE(1) MOE_COMBINE_CASE(2) MOE_COMBINE_CASE(3) MOE_COMBINE_CASE(4)
+    MOE_COMBINE_CASE(5) MOE_COMBINE_CASE(6) MOE_COMBINE_CASE(7) MOE_COMBINE_CASE(8)
+    MOE_COMBINE_CASE(9) MOE_COMBINE_CASE(10) MOE_COMBINE_CASE(11) MOE_COMBINE_CASE(12)
+    MOE_COMBINE_CASE(13) MOE_COMBINE_CASE(14) MOE_COMBINE_CASE(15) MOE_COMBINE_CASE(16)
+    default: k_combine<T, Y, WEIGHTS, 0><<<grid, 256, 0, st>>>(a);
+  }
+#undef MOE_COMBINE_CASE
   return hipGetLastError();
 }
 
 template <typename T, typename Y>
 static hipError_t start_combine_grad(RowsArgs a, hipStream_t st) {
-  a.shift = span_shift((a.H + 7) / 8, a.T < 2048 ? 256 : 64);
-  const int64_t per = 256 >> a.shift, rows = ((int64_t)a.P + 255) / 256;
+  a.shift = token_span(a.T, a.H, 2048);
+  const int64_t per = 256 >> a.shift;
   a.blocks = (int32_t)grid_of((a.T + per - 1) / per);
-  k_combine_grad<T, Y><<<a.blocks + (uint32_t)(rows < 1024 ? rows : 1024), 256, 0, st>>>(a);
+  k_combine_grad<T, Y><<<a.blocks + row_blocks(a.P), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
