@@ -309,6 +309,7 @@ struct TileArgs {
   int32_t len_a, len_b;    // readable elements of A's and B's rows (kRows): R, or more where what follows is zeros
   int32_t nseg, nbatch;    // 1 or 2 each
   int32_t tiles_i, tiles_j;
+  int32_t b_once;          // B's rows are read by one row of tiles only (the experts' products)
   int32_t splits;          // workgroups sharing a tile's reduction, in rows of tiles from `head` on
   int32_t head, head_rows; // rows of tiles before them, each tile by one workgroup; their outputs' rows
   float* part;

@@ -578,6 +578,14 @@ MOE_DEV void copy_to_lds(u32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
                : "memory", "m0");
 }
 
+// The same with the non-temporal hint, for operands that are read once.
+MOE_DEV void copy_to_lds_once(u32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+               :
+               : "s"(lds_addr), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+
 // Waits until at most N of this wave's copies are outstanding and its LDS reads have returned, then for the
 // workgroup's other waves to have done the same.
 template <int N>
@@ -610,8 +618,8 @@ struct OperandCopy {
 // The steps of one half tile, in order: a running address and the steps left, so that issuing a step costs few
 // scalar instructions (a wave issues one instruction per four to five cycles: at ~40 per copy the 64 x 64 tile
 // took 0.35 us a step, whatever was in flight). SEGS: a second matrix follows the first; kCols operands have a stride
-// for each (dx: Wg and Wu), kRows ones the same (dg and du).
-template <int ORDER, int H, int WAVES, bool SEGS>
+// for each (dx: Wg and Wu), kRows ones the same (dg and du). HINT: the copies are hinted as `once` says.
+template <int ORDER, int H, int WAVES, bool SEGS, bool HINT = false>
 struct HalfStream {
   typedef OperandCopy<ORDER, H, WAVES> Copy;
   uint64_t p, p1;       // first element of the next step; of the second matrix
@@ -620,6 +628,7 @@ struct HalfStream {
   int32_t cut;          // reduction elements that the last, partial step of a matrix lacks
   int32_t left, left1;  // steps left in this matrix, the one to be issued included; in the second one
   int32_t ld1;          // kCols: the second matrix's stride in elements
+  bool once;            // HINT: the operand is read by this workgroup only
   int32_t end, end1;    // left's value after a matrix's last step if that is partial and this workgroup's, else one it never takes
 
   // first: the half tile's first element; outs: its outputs that exist; R: reduction length (kRows: readable
@@ -677,8 +686,13 @@ struct HalfStream {
 #pragma unroll
         for (int d = 0; d < Copy::kCopies; ++d) c.voff[d] |= 0x80000000u;
     }
+    if (HINT && once) {
 #pragma unroll
-    for (int d = 0; d < Copy::kCopies; ++d) copy_to_lds(rsrc, lds_addr + d * WAVES * 1024, c.voff[d]);
+      for (int d = 0; d < Copy::kCopies; ++d) copy_to_lds_once(rsrc, lds_addr + d * WAVES * 1024, c.voff[d]);
+    } else {
+#pragma unroll
+      for (int d = 0; d < Copy::kCopies; ++d) copy_to_lds(rsrc, lds_addr + d * WAVES * 1024, c.voff[d]);
+    }
     if (ORDER == kRows && __builtin_expect(tail, 0))
 #pragma unroll
       for (int d = 0; d < Copy::kCopies; ++d) c.voff[d] &= 0x7FFFFFFFu;
@@ -833,7 +847,7 @@ __global__ __launch_bounds__(256, 2) void k_backward_small(TileArgs dx, TileArgs
 // 810 us. 128-square tiles, two workgroups per CU, where 256-square ones would leave CUs idle: 4096 x 2048
 // outputs of 8192 terms 134 against 181 us.
 constexpr int big_lds(int wi, int wj, int fi, int fj) { return 2 * 2 * 16 * (wi * fi + wj * fj) * kStepR; }  // elements
-template <typename T, int OA, int OB, int KIND, int WI, int WJ, int FI, int FJ>
+template <typename T, int OA, int OB, int KIND, int WI, int WJ, int FI, int FJ, bool HINT = false>
 MOE_DEV void big_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   constexpr int W = WI * WJ, HI = WI * FI * 16, HJ = WJ * FJ * 16;
   constexpr int kBuf = 2 * (HI + HJ) * kStepR;  // elements of one buffer: A0 A1 B0 B1
@@ -854,13 +868,14 @@ MOE_DEV void big_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   OperandCopy<OA, HI, W> ca;
   OperandCopy<OB, HJ, W> cb[2];
   HalfStream<OA, HI, W, kSegs> sa[2];
-  HalfStream<OB, HJ, W, kSegs> sb[2];
+  HalfStream<OB, HJ, W, kSegs, HINT> sb[2];
   ca.init(a.lda[0], wave, lane);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     constexpr bool g = KIND == kEpiGated;
     sa[h].init(ca, kBatches && x.batch ? a.a[1] : a.a[0], a.a[1], a.lda[0], 0, i0 + h * HI, a.M, OA == kRows ? a.len_a : a.R,
                steps, s_begin, count);
+    if constexpr (HINT) sb[h].once = a.b_once;
     cb[h].init(a.ldb[g ? h : 0], wave, lane);
     sb[h].init(cb[h], a.b[g ? h : 0], a.b[1], a.ldb[g ? h : 0], a.ldb[1], j0 + (g ? 0 : h * HJ), a.N,
                OB == kRows ? a.len_b : a.R, steps, s_begin, count);

@@ -89,6 +89,7 @@ MOE_DEV bool group_rows(const GroupArgs& g, TileArgs& a, TileIndex& x) {
   const GroupTile t = find_tile<TI>(g, x.ti, per, mine, incl);
   x.ti = t.tile;
   a.M = t.rows;
+  a.b_once = t.rows <= TI;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     a.a[m] = (const uint16_t*)a.a[m] + t.row0 * a.lda[0];
@@ -148,6 +149,9 @@ MOE_DEV void zero_tile(const TileArgs& a, int64_t i0, int rows, int64_t j0, int 
   }
 }
 
+// The weights of an expert with one row of tiles are read once, and hinted so: 2048 x 768 gated, 512 experts, 256 tokens' ten
+// 420 -> 389 us, 4096 tokens' 808 -> 790; hinted throughout, the popular experts' tiles miss each other's (4096: 812).  (Not
+// in the 64-square kernel: one token 14.5 us, 15.1 hinted.)
 template <typename T, int OA, int OB, int KIND, int WI, int WJ, int FI, int FJ>
 __global__ __launch_bounds__(64 * WI * WJ, 2) void k_group_big(GroupArgs g) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[big_lds(WI, WJ, FI, FJ)];
@@ -160,7 +164,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_group_big(GroupArgs g) {
   } else if (!group_rows<TI>(g, a, x)) {
     return;
   }
-  big_tile<T, OA, OB, KIND, WI, WJ, FI, FJ>(a, x, lds);
+  big_tile<T, OA, OB, KIND, WI, WJ, FI, FJ, OA == kRows>(a, x, lds);
 }
 
 template <typename T, int OA, int OB, int KIND>
@@ -248,11 +252,29 @@ __global__ __launch_bounds__(128 * WJ, 4) void k_group_dw(GroupArgs g) {
   store_block<T, F, F>(a.epi.y[0], a.epi.ldy[0], i0 + wi * 64, j0 + wj * 64, a.M, a.N, a.epi.stream, acc, lds + wave * 4096, lane);
 }
 
-// The tile with the least estimated time, by the costs measured for the dense products (TileCost).  The rows of an
-// expert are not known here: rows of tiles are taken as P / tile + half the experts that can have rows, but at least
-// those.
+// The tile of a product over rows of whole 16-byte chunks.  How many rows an expert has is not known here: rows of tiles are taken
+// as P / tile + half the experts that can have rows, but at least those.  128-square tiles carry everything but the ends:
+// they draw the weights fastest even where an expert has two rows (16 tokens' ten of 512 experts, 2048 x 768: 56 us, 64-square
+// 71), but below two for three CUs the 64-square ones' number counts for more (one token, 768 gated of 2048: 15.5 and 23.5 us;
+// 24 experts of 28 rows, 1360 of 1000, 264 tiles: 21.6 and 16.9), and from 256 rows per expert on the 256-square ones'
+// reuse does (128 experts of 320 rows, 2048 x 768: 176 us, 128-square 197; 256 of 160: 241 and 250, 512 Zipf ones of 160 980
+// and 966).
+template <int KIND>
+int plan_rows_whole(const GroupArgs& g) {
+  const int64_t active = g.E < g.P ? g.E : g.P;
+  auto tiles = [&](int tile) {
+    const int64_t rows = g.P / tile + active / 2, tj = KIND == kEpiGated ? tile / 2 : tile;
+    return (rows > active ? rows : active) * ((g.tile.N + tj - 1) / tj);
+  };
+  if (tiles(128) <= 176) return MOE_DENSE_TILE64;
+  return g.P >= 256 * active && tiles(256) >= 256 ? MOE_DENSE_TILE256 : MOE_DENSE_TILE128;
+}
+
+// Of the kernels for any alignment, and for dW of long reductions, the tile with the least estimated time by the costs
+// measured for the dense products (TileCost).
 template <int OA, int KIND>
 int plan_group(const GroupArgs& g, bool whole) {
+  if (OA == kRows && whole) return plan_rows_whole<KIND>(g);
   const int64_t active = g.E < g.P ? g.E : g.P;
   const TileCost* costs = whole ? kWholeCosts : kAnyCosts;
   int best = 0;

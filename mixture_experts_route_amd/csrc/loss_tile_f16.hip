@@ -10,6 +10,7 @@ hipError_t launch_loss_f16(const TileArgs& args, int* tiles, hipStream_t st) {
   double us;
   const hipError_t e = prepare_tile<kRows, kRows, kEpiLoss>(a, plan, us, st);
   if (e != hipSuccess) return e;
+  plan.kernel = few_tokens_kernel(a, plan.kernel);
   const int tile = plan.kernel == MOE_DENSE_TILE256 ? 256 : plan.kernel == MOE_DENSE_TILE64 || plan.kernel == MOE_DENSE_ANY64 ? 64 : 128;
   *tiles = (a.N + tile - 1) / tile;
   return start_plan<_Float16, kRows, kRows, kEpiLoss>(a, plan.kernel, st);
