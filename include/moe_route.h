@@ -710,7 +710,8 @@ MOE_API int moe_experts_gated_backward(const moe_experts_dims* dims, const void*
  *   - The backward pass computes the logits again and rounds dz to dims->dtype before the products, in fp16 after a scaling
  *     by a power of two that brings the largest |dloss| to 2^11 (undone in fp32): a token whose dloss is less than 2^-20 of the
  *     largest loses precision there.  A result past 65504 is an infinity, one below 2^-25 zero: scale dloss.
- *   - An infinite logit gives the limits: loss 0 where it is the target's alone, else infinite; NaN stays in its token.
+ *   - An infinite logit gives the limits: loss 0 where it is the target's alone, infinite where it is another's (the
+ *     gradient of that column is then NaN), NaN where it is both; a NaN stays in its token, its dx and the dW it reaches.
  *   - Sums are in a fixed order: equal calls give equal bits.
  *   - 1 <= n_in, vocab <= MOE_DENSE_MAX_WIDTH; 1 <= n_tokens <= MOE_LOSS_MAX_TOKENS (beyond: MOE_EUNSUPPORTED).
  *   - moe_debug_force_dense_plan holds here too.
