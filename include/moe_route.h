@@ -707,9 +707,9 @@ MOE_API int moe_experts_gated_backward(const moe_experts_dims* dims, const void*
  *   - Logits are fp32 sums and are not rounded.  loss is formed from what the other columns add to the target's, so
  *     that a small loss keeps its relative precision; the gradient takes both saved values for the same reason
  *     (exp(z - lse) - 1 at the target is expm1(-loss)).
- *   - The backward pass computes the logits again and rounds dz to dims->dtype before the products, in fp16 after a scaling
- *     by a power of two that brings the largest |dloss| to 2^11 (undone in fp32): a token whose dloss is less than 2^-20 of the
- *     largest loses precision there.  A result past 65504 is an infinity, one below 2^-25 zero: scale dloss.
+ *   - The backward pass computes the logits again and rounds dz to dims->dtype before the products, with dloss taken
+ *     relative to the largest |dloss| of the call (fp16: brought to 2^11; undone in fp32 afterwards): in fp16 a token whose dloss is
+ *     less than 2^-20 of the largest loses precision.  A result past 65504 is an infinity, one below 2^-25 zero: scale dloss.
  *   - An infinite logit gives the limits: loss 0 where it is the target's alone, infinite where it is another's (the
  *     gradient of that column is then NaN), NaN where it is both; a NaN stays in its token, its dx and the dW it reaches.
  *   - Sums are in a fixed order: equal calls give equal bits.

@@ -171,7 +171,7 @@ struct LossEpi {
   const int32_t* targets;
   const float *loss, *lse, *dloss;  // kEpiLossDz
   float2* part;                     // kEpiLoss: [tiles_j][M], the target's column left out
-  const float* scale;               // kEpiLossDz: dz's factor; kEpiSum: the results' (NULL: 1)
+  const float* scale;               // kEpiLossDz: dloss's factor; kEpiSum: the results' (NULL: 1, for sums that go on)
   const float* acc;                 // kEpiSum: the earlier sums, row stride DenseEpi::ldr (NULL: none)
   int32_t* ctrl;
   int32_t col0, vocab, ignore;      // the product's first column, and all of them

@@ -243,7 +243,7 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
   }
   if constexpr (KIND == kEpiLossDz) {
     const LossEpi& l = e.loss;
-    const float scale = l.scale ? *l.scale : 1.0f;
+    const float scale = *l.scale;
     const bool inside = j0 + dj + FJ * 16 <= a.N;
 #pragma unroll
     for (int h = 0; h < NI; ++h) {
@@ -286,7 +286,26 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
     }
     return;
   }
-  const bool plain = KIND == kEpiStore || (KIND == kEpiSum && !e.loss.acc && !e.loss.scale && !e.y_f32) || (KIND == kEpiLinear && !e.bias[0] && !e.pre[0] && !e.res && !e.y_f32 && e.act == MOE_ACT_NONE);
+  if constexpr (KIND == kEpiSum) {
+    if (x.splits == 1 && !e.loss.acc && !e.y_f32) {  // scaled in the registers
+      const float scale = *e.loss.scale;
+#pragma unroll
+      for (int h = 0; h < NI; ++h)
+#pragma unroll
+        for (int hj = 0; hj < 2; ++hj) {
+          float4v v[FI][FJ];
+#pragma unroll
+          for (int f = 0; f < FI; ++f)
+#pragma unroll
+            for (int n = 0; n < FJ; ++n)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) v[f][n][c] = s[h][hj][f][n][c] * scale;
+          store_block<T, FI, FJ>(e.y[0], e.ldy[0], i0 + h * di, j0 + hj * dj, a.M, a.N, e.stream, v, (uint16_t*)lds, lane);
+        }
+      return;
+    }
+  }
+  const bool plain = KIND == kEpiStore || (KIND == kEpiLinear && !e.bias[0] && !e.pre[0] && !e.res && !e.y_f32 && e.act == MOE_ACT_NONE);
 #pragma unroll
   for (int h = 0; h < NI; ++h)
 #pragma unroll

@@ -159,10 +159,13 @@ static hipError_t start_join(const LossJoinArgs& j, hipStream_t st) {
   return hipGetLastError();
 }
 
-// fp16's dz is kept in its normal range by a power of two S with S max|dloss| in [2^11, 2^12): at most 4096 for a target, normal
-// down to probabilities of 2^-25, 8 bits left at 2^-32.  out = {S, 1 / S}.
+// dz is formed with dloss over the largest |dloss|, and the products are multiplied by that again, in fp32: with the same dloss
+// for every token, a mean's 1 / count, an unsure token's dz at its target is then near -1, which no rounding moves, and not
+// near -dloss, which one and the same rounding moves for all of them (bf16: dx and dW of a few tokens up to 2.6e-3 off their
+// definition that way, 1.7e-3 to 2.0e-3 so; the plain form 1.7e-3).  fp16's dz is brought to 2^11 by it: at most 2048 at a target,
+// normal down to probabilities of 2^-25, 8 bits left at 2^-32.  out = {factor of dloss, factor of the products}.
 __global__ __launch_bounds__(1024) void k_loss_scale(const float* dloss, const int32_t* targets, int T, int vocab, int ignore,
-                                                     float* out) {
+                                                     float most_dz, float* out) {
   __shared__ float most[16];
   float m = 0.0f;
   for (int t = threadIdx.x; t < T; t += 1024) {
@@ -175,11 +178,9 @@ __global__ __launch_bounds__(1024) void k_loss_scale(const float* dloss, const i
   __syncthreads();
   if (threadIdx.x) return;
   for (int i = 1; i < 16; ++i) m = fmaxf(m, most[i]);
-  int e = 0;
-  if (m > 0.0f) e = 11 - ilogbf(m);
-  e = e < -100 ? -100 : (e > 100 ? 100 : e);
-  out[0] = ldexpf(1.0f, e);
-  out[1] = ldexpf(1.0f, -e);
+  m = fminf(fmaxf(m, 0x1p-100f), 0x1p100f);
+  out[0] = most_dz / m;
+  out[1] = m / most_dz;
 }
 
 static int check_loss(const moe_loss_dims* d) {
@@ -290,11 +291,9 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
   const bool bf16 = dims->dtype == MOE_BF16;
   const LossWs L = loss_ws(dims, n_tokens, true);
   auto at = [&](size_t off) { return (uint8_t*)ws + off; };
-  float* scale = bf16 ? nullptr : (float*)at(L.scale);
-  if (scale) {
-    k_loss_scale<<<1, 1024, 0, st>>>(dloss, targets, n_tokens, dims->vocab, dims->ignore, scale);
-    if (hipGetLastError() != hipSuccess) return MOE_EHIP;
-  }
+  float* scale = (float*)at(L.scale);
+  k_loss_scale<<<1, 1024, 0, st>>>(dloss, targets, n_tokens, dims->vocab, dims->ignore, bf16 ? 1.0f : 0x1p11f, scale);
+  if (hipGetLastError() != hipSuccess) return MOE_EHIP;
   // Rows of whole 16-byte chunks for all three products, by one copy.
   const void *xs = x, *wt = w;
   int64_t ld_x = ldx, ld_w = ldw;
@@ -344,7 +343,7 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
       a.M = cols;
       a.N = dims->n_in;
       a.R = n_tokens;
-      a.epi.loss.scale = scale ? scale + 1 : nullptr;
+      a.epi.loss.scale = scale + 1;
       a.epi.y[0] = (uint16_t*)dw_or_null + c0 * ld_dw;
       a.epi.ldy[0] = ld_dw;
       if ((rc = dense_status(bf16 ? launch_loss_dw_bf16(a, st) : launch_loss_dw_f16(a, st)))) return rc;
@@ -362,7 +361,7 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
       a.epi.y_f32 = !last;
       a.epi.y[0] = last ? dx_or_null : at(L.acc);
       a.epi.ldy[0] = last ? ld_dx : L.ld_in;
-      a.epi.loss.scale = scale && last ? scale + 1 : nullptr;
+      a.epi.loss.scale = last ? scale + 1 : nullptr;
       if ((rc = dense_status(bf16 ? launch_loss_dx_bf16(a, st) : launch_loss_dx_f16(a, st)))) return rc;
     }
   }

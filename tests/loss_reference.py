@@ -5,8 +5,9 @@ of a rounded argument a: relative (|a| + 4) 2 e; the sum of exponentials through
   loss   a shift of every other logit against the target's by s moves it by at most (1 - p) (e^s - 1), with s two ez; the
          sum's relative error counts with the same factor; 8 e of the result and of the logits' distance
   lse    ez, the sum's relative error, 8 e of the magnitudes added
-  dz     p's relative error is ez's and exp's; at the target expm1's, 8 e; then 2 e for the product with dloss;
-         rounded to the type h |dz| + d / S, S the power of two that fp16's dz is scaled by
+  dz     p's relative error is ez's and exp's; at the target expm1's, 8 e; then 2 e for each of: the factor S that dloss is
+         multiplied by (1 / the largest |dloss|, fp16 2^11 / it), that product, the one with p, and the results' factor;
+         rounded to the type h |dz| + d / S
 """
 
 import torch
@@ -58,18 +59,15 @@ def dz_of(x, w, targets, ignore, loss, lse, dloss):
     p, ep = p.scatter(1, at, own), ep.scatter(1, at, 8 * E * own.abs())
     g = dloss.double()[:, None]
     dz = torch.where(live[:, None], p * g, 0.0)
-    return dz, torch.where(live[:, None], ep * g.abs() + 2 * E * dz.abs(), 0.0)
+    return dz, torch.where(live[:, None], ep * g.abs() + 8 * E * dz.abs(), 0.0)
 
 
 def backward(x, w, targets, ignore, loss, lse, dloss, dt):
     dz, e = dz_of(x, w, targets, ignore, loss, lse, dloss)
     x, w = x.double(), w.double()
     live = (targets >= 0) & (targets < w.shape[0]) & (targets != ignore)
-    tiny = R.tiny_step(dt)
-    if dt == torch.float16:
-        most = torch.where(live, dloss.double().abs(), 0.0).max()
-        if most > 0:
-            tiny = tiny / 2.0 ** (11 - torch.floor(torch.log2(most))).item()
+    most = torch.where(live, dloss.double().abs(), 0.0).max().item()
+    tiny = R.tiny_step(dt) * most / (2.0 ** 11 if dt == torch.float16 else 1.0)
     r = e + R.half_step(dt) * (dz.abs() + e) + torch.where(live[:, None], tiny, 0.0)
     out = {}
     for name, a, ra, b in (("dx", dz, r, w), ("dw", dz.T, r.T, x)):
