@@ -75,13 +75,14 @@ struct LossJoinArgs {
 // zt is summed here, in 64 bits (16-bit products are exact in 32): a sure token's loss is nothing but its distance from the
 // others, and the target's logit, the largest in magnitude, would bring the most error into it.
 // BLOCK tokens per workgroup share its 256 threads: neighbouring threads have neighbouring tokens while they read the
-// tiles, and parts of the same token, in one wave, for the rest.  Every order is fixed.  Bound by the latency of a few dependent
+// tiles, and parts of the same token, in one wave (BLOCK 1: the workgroup), for the rest.  Every order is fixed.  Bound by the latency of a few dependent
 // loads at small sizes, then by memory.
 template <typename T, int BLOCK>
 __global__ __launch_bounds__(256) void k_loss_join(LossJoinArgs a) {
-  constexpr int kShares = 256 / BLOCK;
-  static_assert(kShares <= 64, "a token's threads are in one wave");
+  constexpr int kShares = 256 / BLOCK, kWaveShares = kShares < 64 ? kShares : 64;
+  static_assert(BLOCK == 1 || kShares <= 64, "a token's threads are the workgroup or in one wave");
   __shared__ float ms[kShares][BLOCK + 1], ss[kShares][BLOCK + 1];
+  __shared__ double zs[4];
   const int t = blockIdx.x * BLOCK + threadIdx.x / kShares, part = threadIdx.x % kShares;
   double zt = 0.0;
   const int target = t < a.T ? a.targets[t] : -1;
@@ -125,12 +126,29 @@ __global__ __launch_bounds__(256) void k_loss_join(LossJoinArgs a) {
   __syncthreads();
   float m = ms[part][threadIdx.x / kShares], s = ss[part][threadIdx.x / kShares];
 #pragma unroll
-  for (int o = 1; o < kShares; o <<= 1) {
+  for (int o = 1; o < kWaveShares; o <<= 1) {
     const float mo = __shfl_xor(m, o, 64), so = __shfl_xor(s, o, 64), most = fmaxf(m, mo), base = not_infinite(most);
     const float mine = m == most ? s : s * exp_below(m, base), other = mo == most ? so : so * exp_below(mo, base);
     s = mine + other;
     m = most;
     zt += __shfl_xor(zt, o, 64);
+  }
+  if constexpr (BLOCK == 1) {  // the four waves'
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+      ms[threadIdx.x >> 6][0] = m;
+      ss[threadIdx.x >> 6][0] = s;
+      zs[threadIdx.x >> 6] = zt;
+    }
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int w = 1; w < 4; ++w) {
+      const float mo = ms[w][0], so = ss[w][0], most = fmaxf(m, mo), base = not_infinite(most);
+      const float mine = m == most ? s : s * exp_below(m, base), other = mo == most ? so : so * exp_below(mo, base);
+      s = mine + other;
+      m = most;
+      zt += zs[w];
+    }
   }
   if (part || t >= a.T) return;
   float loss = 0.0f, lse = 0.0f;
@@ -155,6 +173,7 @@ __global__ __launch_bounds__(256) void k_loss_join(LossJoinArgs a) {
 template <typename T>
 static hipError_t start_join(const LossJoinArgs& j, hipStream_t st) {
   if (j.T >= 4096) k_loss_join<T, 16><<<(j.T + 15) / 16, 256, 0, st>>>(j);
+  else if (j.T <= 256) k_loss_join<T, 1><<<j.T, 256, 0, st>>>(j);
   else k_loss_join<T, 4><<<(j.T + 3) / 4, 256, 0, st>>>(j);
   return hipGetLastError();
 }
@@ -168,6 +187,7 @@ __global__ __launch_bounds__(1024) void k_loss_scale(const float* dloss, const i
                                                      float most_dz, float* out) {
   __shared__ float most[16];
   float m = 0.0f;
+#pragma unroll 4
   for (int t = threadIdx.x; t < T; t += 1024) {
     const float g = fabsf(dloss[t]);
     if ((uint32_t)targets[t] < (uint32_t)vocab && targets[t] != ignore && g < INFINITY) m = fmaxf(m, g);
