@@ -203,12 +203,15 @@ constexpr int kShortRows = 2048;
 
 // dW of experts with few rows: 128 x 128 tile, 4 waves of 64 x 64.  A reduction of a step or two is over before a pipeline has
 // filled, so there is none: a step's operands come into one LDS buffer of 32 KB, and the four workgroups that fit a CU
-// cover each other's loads and stores.  A wave's results leave as whole 128-byte lines.
-template <typename T, int WJ>
-__global__ __launch_bounds__(128 * WJ, 4) void k_group_dw(GroupArgs g) {
-  constexpr int HI = 128, HJ = 64 * WJ, W = 2 * WJ, F = 4;
+// cover each other's loads and stores.  A wave's results leave, through the same LDS, as whole 128-byte lines.  512 Zipf experts
+// of 80 rows, 2 x 768 x 2048 (3.2 GB written): 935 us, 4.7 TB/s of what it reads and writes; of one matrix's 483 us the stores
+// alone take 264 and everything else alone 180.  (Two workgroups per CU that walk over the tiles with the next one's operands
+// on their way: 538; 128 x 256: 550.)
+template <typename T>
+__global__ __launch_bounds__(256, 4) void k_group_dw(GroupArgs g) {
+  constexpr int HI = 128, HJ = 128, WJ = 2, W = 2 * WJ, F = 4;
   typedef typename Operand<T>::v8 v8;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[(HI + HJ) * kStepR > W * 4096 ? (HI + HJ) * kStepR : W * 4096];
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[(HI + HJ) * kStepR];
   TileArgs a;
   TileIndex x;
   if (!group_sums(g, a, x)) return;
@@ -335,7 +338,7 @@ hipError_t launch_experts(const GroupArgs& args, hipStream_t st) {
   if constexpr (OA == kCols) {
     if (whole && g_dense_plan.kernel == MOE_DENSE_AUTO && g.P <= kShortRows * (int64_t)g.E) {
       if (!group_grid<OA, KIND>(g, 128, 256, &grid)) return hipErrorInvalidConfiguration;
-      k_group_dw<T, 2><<<grid, 256, 0, st>>>(g);
+      k_group_dw<T><<<grid, 256, 0, st>>>(g);
       return hipGetLastError();
     }
   }
