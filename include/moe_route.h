@@ -97,9 +97,9 @@ enum moe_device_error {
   MOE_DERR_DUP_ID = 32,       /* a token's top-k list names one expert twice */
   MOE_DERR_RANGE = 64,        /* prefill: an activation, SwiGLU output or weighted expert row
                                  beyond the fp16 range (|v| > 65504) or not finite */
-  MOE_DERR_TARGET = 256,      /* loss: a target outside [0, vocab) that is not `ignore` */
-  MOE_DERR_ROWS = 128         /* rows by expert: a pair out of range or in two rows, a row out of
+  MOE_DERR_ROWS = 128,        /* rows by expert: a pair out of range or in two rows, a row out of
                                  range, perm and inv at odds, offsets that descend or leave the rows */
+  MOE_DERR_TARGET = 256       /* loss: a target outside [0, vocab) that is not `ignore` */
 };
 
 /* Largest token count of a decode call.  The pages' decode batches: concurrent streams (Basalt

@@ -253,7 +253,13 @@ __global__ __launch_bounds__(256) void k_combine(RowsArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] += r[i];
       }
-      store8<Y>(a.dst, t * a.ld_dst + c, n, acc);
+      if (c < col && a.res == a.dst) {  // in place: what the chunk before has belongs to it alone, which may have it no longer
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+          if (i >= col - c) ((Y*)a.dst)[t * a.ld_dst + c + i] = (Y)acc[i];
+      } else {
+        store8<Y>(a.dst, t * a.ld_dst + c, n, acc);
+      }
     }
   }
 }

@@ -149,17 +149,23 @@ def test_values_at_the_limits(N):
     assert torch.isinf(y[0]).all() and torch.isnan(y[1]).all() and torch.isinf(y[2]).all() and (y[3] == -0.75).all()
 
 
-def test_in_place_on_the_residual(N):
-    gen = gen_for(5)
-    T, k, H = 30, 3, 200
+@pytest.mark.parametrize("T,H", [(30, 200), (30, 7), (30, 65), (30, 515), (30, 521), (40, 2049), (40, 4099), (2100, 521),
+                                 (17000, 515), (17000, 1025), (17000, 131)])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_in_place_on_the_residual(N, T, H, dt):
+    """Odd widths too, whose last chunk reaches into the one before it, in another pass or wave."""
+    gen = gen_for(5 + H)
+    k = 3
     perm, inv = layout(gen, T, k, 4)
     d = N.rows_dims(H, k, N.MOE_BF16)
     ws = workspace(N, d, T)
-    rows, w, y = rnd(gen, (T * k, H), BF16), torch.rand(T, k, generator=gen, device="cuda"), rnd(gen, (T, H), F32)
-    want = torch.empty_like(y)
-    N.moe_combine_forward(d, rows, inv, w, T, want, ws, residual=y)
-    N.moe_combine_forward(d, rows, inv, w, T, y, ws, residual=y)
-    assert torch.equal(y, want)
+    rows, w, y = rnd(gen, (T * k, H), BF16), torch.rand(T, k, generator=gen, device="cuda"), rnd(gen, (T, H), dt)
+    for call in (lambda out, r: N.moe_combine_forward(d, rows, inv, w, T, out, ws, residual=r),
+                 lambda out, r: N.moe_dispatch_backward(d, rows, inv, T, out, ws, residual=r)):
+        want, got = torch.empty_like(y), y.clone()
+        call(want, y)
+        call(got, got)
+        assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("T", [6, 1200])  # the inverse map in one workgroup, and by all
