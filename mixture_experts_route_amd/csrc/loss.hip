@@ -318,17 +318,20 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
   float* scale = (float*)at(L.scale);
   k_loss_scale<<<1, 1024, 0, st>>>(dloss, targets, n_tokens, dims->vocab, dims->ignore, bf16 ? 1.0f : 0x1p11f, scale);
   if (hipGetLastError() != hipSuccess) return MOE_EHIP;
-  // Rows of whole 16-byte chunks for all three products, by one copy.
   const void *xs = x, *wt = w;
   int64_t ld_x = ldx, ld_w = ldw;
   int32_t len = dims->n_in;
   PackArgs p{};
-  if ((uintptr_t)x % 16 || ldx % 8 || dims->n_in % 8) {
+  // Rows of whole 16-byte chunks for all three products, by one copy.  With an odd n_in that copies the weights too, which few
+  // tokens do not pay for unless they are few as well: 2047 x 100003, 16 tokens 614 us, without 480; 128 tokens 704 and 641; 256
+  // tokens 757 and 889; 1001 x 5000, 16 tokens 39 and 44.
+  const bool pack = dims->n_in % 8 == 0 || n_tokens >= 192 || 2 * dims->vocab * L.ld_in <= 32 << 20;
+  if (pack && ((uintptr_t)x % 16 || ldx % 8 || dims->n_in % 8)) {
     p.m[p.count++] = {(const uint16_t*)x, (uint16_t*)at(L.x), ldx, L.ld_in, n_tokens, dims->n_in};
     xs = at(L.x);
     ld_x = L.ld_in;
   }
-  if (L.w) {
+  if (pack && L.w) {
     p.m[p.count++] = {(const uint16_t*)w, (uint16_t*)at(L.w), ldw, L.ld_in, dims->vocab, dims->n_in};
     wt = at(L.w);
     ld_w = len = L.ld_in;

@@ -88,6 +88,12 @@ def test_odd_widths(N, T, K, V, dt):
     check_all(N, T * K, T, K, V, dt)
 
 
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_odd_widths_of_large_heads(N, dt):
+    check_all(N, 25, 5, 129, 140000, dt)  # few tokens: the weights are read as they lie
+    check_all(N, 26, 200, 129, 140000, dt)
+
+
 @pytest.mark.parametrize("pad,offset", [(1, 0), (0, 3), (8, 8), (8, 0), (7, 1)])
 def test_strides_and_alignments(N, pad, offset):
     check_all(N, 30 + pad, 70, 64, 300, BF16, pad=pad, offset=offset)
