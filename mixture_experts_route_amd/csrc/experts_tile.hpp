@@ -197,9 +197,9 @@ __global__ __launch_bounds__(256, 2) void k_group_any(GroupArgs g) {
 }
 
 // Mean rows of an expert up to which dW takes k_group_dw.  Against the best of the pipelined tiles, lengths spread
-// exponentially, 768 x 2048: 512 experts of 20 rows 337 and 356 us, of 80 rows 467 and 473; 64 of 640 rows 174 and 184;
-// 16 of 2048 rows 121 and 158; 8 of 4096 rows, 4096 x 4096, 931 and 922.
-constexpr int kShortRows = 2048;
+// exponentially, 768 x 2048: 512 experts of 20 rows 337 and 361 us, of 80 rows 467 and 483; 256 of 160 rows 296 and 306; 128
+// of 320 rows 220 both; 64 of 512 rows 144 and 135, of 1024 rows 276 and 233.
+constexpr int kShortRows = 320;
 
 // dW of experts with few rows: 128 x 128 tile, 4 waves of 64 x 64.  A reduction of a step or two is over before a pipeline has
 // filled, so there is none: a step's operands come into one LDS buffer of 32 KB, and the four workgroups that fit a CU
