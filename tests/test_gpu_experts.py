@@ -174,6 +174,30 @@ def test_one_row_and_no_rows(N):
     check_all(N, 83, [0, 0, 0], 63, 61, BF16, lead=4)
 
 
+def test_many_rows(N):
+    """Two million rows of three experts, and the halves of one weight tensor as the gated block's two."""
+    check_all(N, 84, [1 << 20, 5, (1 << 20) - 70], 24, 16, BF16, lead=2, tail=3, need=("lin",))
+    E, K, M = 5, 96, 40
+    counts = [70, 0, 3, 130, 16]
+    gen = gen_for(85)
+    offs, slices, P = rows_of(counts, 0, 0)
+    w = stack(gen, E, 2 * M, K, BF16, K ** -0.5)
+    x, dh = rnd(gen, (P, K), BF16), rnd(gen, (P, M), BF16)
+    d = N.experts_dims(E, K, M, N.MOE_BF16, 1)
+    ws, whole = workspace(N, d, P, True)
+    h, g, u, dx, dw = (torch.empty(s, dtype=BF16, device="cuda") for s in ((P, M), (P, M), (P, M), (P, K), (E, 2 * M, K)))
+    N.moe_experts_gated_forward(d, x, offs, w[:, :M], w[:, M:], h, ws, gate=g, up=u)
+    N.moe_experts_gated_backward(d, x, offs, w[:, :M], w[:, M:], g, u, dh, ws, dx=dx, dw_gate=dw[:, :M], dw_up=dw[:, M:])
+    for e in (0, 2, 3, 4):
+        s = slices[e]
+        R.check("h", h[s], R.gated_forward(1, x[s], w[e, :M], w[e, M:], None, None)["h"])
+        ref = R.gated_backward(1, x[s], w[e, :M], w[e, M:], g[s], u[s], dh[s])
+        R.check("dx", dx[s], ref["dx"])
+        R.check("dw0", dw[e, :M], ref["dw0"])
+        R.check("dw1", dw[e, M:], ref["dw1"])
+    assert (dw[1] == 0).all() and guard_ok(whole) and N.moe_check_device_error(ws) == 0
+
+
 def test_bad_offsets_are_reported_and_stay_in_bounds(N):
     E, K, M, P = 4, 64, 40, 50
     gen = gen_for(90)

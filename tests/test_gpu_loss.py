@@ -120,6 +120,10 @@ def test_many_tokens_in_several_launches(N):
     check_all(N, 42, 8192 + 5, 64, 200, BF16)
 
 
+def test_most_tokens(N):
+    check_all(N, 50, 1 << 20, 16, 70, BF16)
+
+
 @pytest.mark.parametrize("dt", [BF16, F16])
 def test_vocabulary_in_several_pieces(N, dt):
     check_all(N, 43, 40000, 40, 4000, dt)  # pieces of 2048 and 1952 columns

@@ -294,3 +294,28 @@ def test_more_than_2_31_elements(N):
     N.moe_combine_backward(d, x, T, perm, inv, w, ws, ys=xs, dys=dys, dtopk_w=dw)
     assert torch.equal(dys, x.flip(0))
     assert N.moe_check_device_error(ws) == 0
+
+
+def test_most_tokens(N):
+    """2^24 tokens, the limit, a pair each, reversed."""
+    T, H = 1 << 24, 8
+    gen = gen_for(13)
+    d = N.rows_dims(H, 1, N.MOE_BF16)
+    ws = workspace(N, d, T)
+    x = rnd(gen, (T, H), BF16)
+    perm = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")
+    perm[5], perm[T - 7] = -1, -1
+    xs, inv = torch.empty_like(x), torch.empty(T, 1, dtype=torch.int32, device="cuda")
+    N.moe_dispatch_forward(d, x, T, perm, xs, inv, ws)
+    want = x.flip(0)
+    want[5], want[T - 7] = 0, 0
+    assert torch.equal(xs, want) and (inv == -1).sum() == 2 and inv[0, 0] == T - 1
+    y, w = torch.empty_like(x), torch.ones(T, 1, device="cuda")
+    N.moe_combine_forward(d, xs, inv, w, T, y, ws)
+    assert torch.equal(y, want.flip(0))
+    dys = torch.full_like(x, 7.0)
+    N.moe_combine_backward(d, x, T, perm, inv, w, ws, dys=dys)
+    assert torch.equal(dys, want) and N.moe_check_device_error(ws) == 0
+    with pytest.raises(N.MoeError) as e:
+        N.moe_combine_forward(d, xs, inv, w, T + 1, y, ws)
+    assert e.value.code == N.MOE_EINVAL
