@@ -79,40 +79,36 @@ static int run_experts_products(const moe_experts_dims* d, int mats, const Group
                                 const void* const* w, int64_t ldw, int64_t stride, const void* const* dz, int64_t ldz,
                                 int32_t len_dz, void* dx, int64_t ld_dx, void* const* dw, int64_t ld_dw, int64_t dw_stride,
                                 hipStream_t st) {
+  GroupArgs gx = base, gw = base;
+  gx.tile.nseg = gw.mats = 0;
   if (dx) {
-    GroupArgs g = base;
     for (int m = 0; m < mats; ++m) {
-      g.tile.a[m] = dz[m];
-      g.tile.lda[m] = ldz;
-      g.tile.b[m] = w[m];
-      g.tile.ldb[m] = ldw;
+      gx.tile.a[m] = dz[m];
+      gx.tile.lda[m] = ldz;
+      gx.tile.b[m] = w[m];
+      gx.tile.ldb[m] = ldw;
     }
-    g.stride = stride;
-    g.tile.N = d->n_in;
-    g.tile.R = d->n_out;
-    g.tile.len_a = len_dz;
-    g.tile.nseg = mats;
-    g.tile.epi.y[0] = dx;
-    g.tile.epi.ldy[0] = ld_dx;
-    const int rc = dense_status(d->dtype == MOE_BF16 ? launch_experts_dx_bf16(g, st) : launch_experts_dx_f16(g, st));
-    if (rc) return rc;
+    gx.stride = stride;
+    gx.tile.N = d->n_in;
+    gx.tile.R = d->n_out;
+    gx.tile.len_a = len_dz;
+    gx.tile.nseg = mats;
+    gx.tile.epi.y[0] = dx;
+    gx.tile.epi.ldy[0] = ld_dx;
   }
-  GroupArgs g = base;
-  g.mats = 0;
   for (int m = 0; m < mats; ++m)
     if (dw[m]) {
-      g.tile.a[g.mats] = dz[m];
-      g.tile.epi.y[g.mats++] = dw[m];
+      gw.tile.a[gw.mats] = dz[m];
+      gw.tile.epi.y[gw.mats++] = dw[m];
     }
-  if (!g.mats) return MOE_OK;
-  g.tile.lda[0] = ldz;
-  g.tile.b[0] = x;
-  g.tile.ldb[0] = ldx;
-  g.stride = dw_stride;
-  g.tile.M = d->n_out;
-  g.tile.N = d->n_in;
-  g.tile.epi.ldy[0] = ld_dw;
-  return dense_status(d->dtype == MOE_BF16 ? launch_experts_dw_bf16(g, st) : launch_experts_dw_f16(g, st));
+  gw.tile.lda[0] = ldz;
+  gw.tile.b[0] = x;
+  gw.tile.ldb[0] = ldx;
+  gw.stride = dw_stride;
+  gw.tile.M = d->n_out;
+  gw.tile.N = d->n_in;
+  gw.tile.epi.ldy[0] = ld_dw;
+  return dense_status(d->dtype == MOE_BF16 ? launch_experts_backward_bf16(gx, gw, st) : launch_experts_backward_f16(gx, gw, st));
 }
 
 }  // namespace moe

@@ -22,9 +22,8 @@ struct GroupArgs {
 // experts_bf16.hip, experts_f16.hip
 hipError_t launch_experts_forward_bf16(const GroupArgs& a, int epi_kind, hipStream_t st);
 hipError_t launch_experts_forward_f16(const GroupArgs& a, int epi_kind, hipStream_t st);
-hipError_t launch_experts_dx_bf16(const GroupArgs& a, hipStream_t st);
-hipError_t launch_experts_dx_f16(const GroupArgs& a, hipStream_t st);
-hipError_t launch_experts_dw_bf16(const GroupArgs& a, hipStream_t st);
-hipError_t launch_experts_dw_f16(const GroupArgs& a, hipStream_t st);
+// dx.tile.nseg or dw.mats 0: not wanted
+hipError_t launch_experts_backward_bf16(const GroupArgs& dx, const GroupArgs& dw, hipStream_t st);
+hipError_t launch_experts_backward_f16(const GroupArgs& dx, const GroupArgs& dw, hipStream_t st);
 
 }  // namespace moe

@@ -5,8 +5,8 @@ namespace moe {
 
 hipError_t launch_experts_forward_bf16(const GroupArgs& g, int kind, hipStream_t st) { return launch_experts_forward_t<__bf16>(g, kind, st); }
 
-hipError_t launch_experts_dx_bf16(const GroupArgs& g, hipStream_t st) { return launch_experts<__bf16, kRows, kCols, kEpiStore>(g, st); }
-
-hipError_t launch_experts_dw_bf16(const GroupArgs& g, hipStream_t st) { return launch_experts<__bf16, kCols, kCols, kEpiStore>(g, st); }
+hipError_t launch_experts_backward_bf16(const GroupArgs& dx, const GroupArgs& dw, hipStream_t st) {
+  return launch_experts_backward_t<__bf16>(dx, dw, st);
+}
 
 }  // namespace moe

@@ -107,17 +107,16 @@ MOE_DEV bool group_rows(const GroupArgs& g, TileArgs& a, TileIndex& x) {
 struct DwTile {
   int e, m, ti, tj, row0, rows, steps;
 };
-MOE_DEV uint32_t dw_run(const GroupArgs& g) { return ((uint32_t)g.tile.tiles_i * (uint32_t)g.tile.tiles_j + 7) / 8; }
-// Tile `at` of this XCD's; false: there is none there.
-MOE_DEV bool dw_tile(const GroupArgs& g, const int32_t* offsets, uint32_t run, uint32_t at, DwTile& x) {
+// Tile `id` of the launch's; false: there is none.
+MOE_DEV bool dw_tile(const GroupArgs& g, uint32_t id, DwTile& x) {
   const uint32_t ti = (uint32_t)g.tile.tiles_i, tj = (uint32_t)g.tile.tiles_j;
-  const uint32_t me = at / run, in = blockIdx.x % 8 * run + (at - me * run);
+  const uint32_t run = (ti * tj + 7) / 8, at = id / 8, me = at / run, in = id % 8 * run + (at - me * run);
   if (in >= ti * tj) return false;
   x.e = (int)(me / (uint32_t)g.mats);
   x.m = (int)(me - (uint32_t)x.e * g.mats);
   x.ti = (int)(ti < tj ? in % ti : in / tj);
   x.tj = (int)(ti < tj ? in / ti : in % tj);
-  const int o0 = __builtin_amdgcn_readfirstlane(offsets[x.e]), o1 = __builtin_amdgcn_readfirstlane(offsets[x.e + 1]);
+  const int o0 = __builtin_amdgcn_readfirstlane(g.offsets[x.e]), o1 = __builtin_amdgcn_readfirstlane(g.offsets[x.e + 1]);
   const int lo = clamp_rows(o0, g.P), hi = clamp_rows(o1, g.P);
   if (in == 0 && threadIdx.x == 0 && (o0 != lo || o1 != hi || hi < lo)) set_error(g.ctrl, MOE_DERR_ROWS);
   x.row0 = lo;
@@ -126,9 +125,9 @@ MOE_DEV bool dw_tile(const GroupArgs& g, const int32_t* offsets, uint32_t run, u
   return true;
 }
 // This workgroup's tile of dW, as arguments of its expert's product; false: there is none.
-MOE_DEV bool group_sums(const GroupArgs& g, TileArgs& a, TileIndex& x) {
+MOE_DEV bool group_sums(const GroupArgs& g, uint32_t id, TileArgs& a, TileIndex& x) {
   DwTile t;
-  if (!dw_tile(g, g.offsets, dw_run(g), blockIdx.x / 8, t)) return false;
+  if (!dw_tile(g, id, t)) return false;
   a = g.tile;
   x = {0, t.ti, t.tj, 0, 1};
   a.R = t.rows;
@@ -159,7 +158,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 2) void k_group_big(GroupArgs g) {
   TileArgs a;
   TileIndex x;
   if constexpr (OA == kCols) {
-    if (!group_sums(g, a, x)) return;
+    if (!group_sums(g, blockIdx.x, a, x)) return;
     if (a.R == 0) return zero_tile<T, 64 * WI * WJ>(a, (int64_t)x.ti * TI, TI, (int64_t)x.tj * TJ, TJ);
   } else if (!group_rows<TI>(g, a, x)) {
     return;
@@ -173,7 +172,7 @@ __global__ __launch_bounds__(256, 2) void k_group_deep(GroupArgs g) {
   TileArgs a;
   TileIndex x;
   if constexpr (OA == kCols) {
-    if (!group_sums(g, a, x)) return;
+    if (!group_sums(g, blockIdx.x, a, x)) return;
     if (a.R == 0) return zero_tile<T, 256>(a, (int64_t)x.ti * 64, 64, (int64_t)x.tj * 64, 64);
   } else if (!group_rows<64>(g, a, x)) {
     return;
@@ -188,7 +187,7 @@ __global__ __launch_bounds__(256, 2) void k_group_any(GroupArgs g) {
   TileArgs a;
   TileIndex x;
   if constexpr (OA == kCols) {
-    if (!group_sums(g, a, x)) return;
+    if (!group_sums(g, blockIdx.x, a, x)) return;
     if (a.R == 0) return zero_tile<T, 256>(a, (int64_t)x.ti * TT, TT, (int64_t)x.tj * TT, TT);
   } else if (!group_rows<TT>(g, a, x)) {
     return;
@@ -207,14 +206,14 @@ constexpr int kShortRows = 320;
 // of 80 rows, 2 x 768 x 2048 (3.2 GB written): 935 us, 4.7 TB/s of what it reads and writes; of one matrix's 483 us the stores
 // alone take 264 and everything else alone 180.  (Two workgroups per CU that walk over the tiles with the next one's operands
 // on their way: 538; 128 x 256: 550.)
+constexpr int kDwLds = (128 + 128) * kStepR;  // elements
 template <typename T>
-__global__ __launch_bounds__(256, 4) void k_group_dw(GroupArgs g) {
+MOE_DEV void short_dw(const GroupArgs& g, uint32_t id, uint16_t* lds) {
   constexpr int HI = 128, HJ = 128, WJ = 2, W = 2 * WJ, F = 4;
   typedef typename Operand<T>::v8 v8;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[(HI + HJ) * kStepR];
   TileArgs a;
   TileIndex x;
-  if (!group_sums(g, a, x)) return;
+  if (!group_sums(g, id, a, x)) return;
   const int64_t i0 = (int64_t)x.ti * HI, j0 = (int64_t)x.tj * HJ;
   if (a.R == 0) return zero_tile<T, 64 * W>(a, i0, HI, j0, HJ);
   const int lane = threadIdx.x & 63;
@@ -253,6 +252,38 @@ __global__ __launch_bounds__(256, 4) void k_group_dw(GroupArgs g) {
     copies_barrier<0>();  // every wave has read the step
   }
   store_block<T, F, F>(a.epi.y[0], a.epi.ldy[0], i0 + wi * 64, j0 + wj * 64, a.M, a.N, a.epi.stream, acc, lds + wave * 4096, lane);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256, 4) void k_group_dw(GroupArgs g) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[kDwLds];
+  short_dw<T>(g, blockIdx.x, lds);
+}
+
+// dx's 128-square tiles up to which dx and dW are one launch: a round of them, two workgroups a CU.
+constexpr uint32_t kOneRound = 512;
+
+// A backward pass whose dx has few tiles: those first, dW's beside and behind them, in one launch.  dx alone leaves CUs idle,
+// more so where few experts hold most rows, and a launch costs two to three microseconds (lengths spread exponentially: 8
+// experts of 40 rows, gated 768 of 2048, 49.2 -> 40.9 us; 24 of 28 rows, 1360 of 1000, 50.3 -> 45.4; 64 of 64 rows, 512 of 512,
+// 33 -> 24.7; 4 of 300 rows, 2048 of 2048, 61.8 -> 52.7).  Behind more than a round of dx's tiles, dW's run two to a CU here
+// instead of k_group_dw's four: 32 experts of 40 rows, gated 768 of 2048, 107 alone and 113 joined; 256 experts, 768 of 2048,
+// 392 and 460.  dx's 64-square tiles are only taken where 704 at most are needed, and gained throughout.
+template <typename T, int TILE>
+__global__ __launch_bounds__(256, 2) void k_group_backward(GroupArgs dx, GroupArgs dw, uint32_t n_dx) {
+  constexpr int kLds = TILE == 64 ? kDeepStages * kDeepStageBytes / 2 : big_lds(2, 2, 2, 2);
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[kLds > kDwLds ? kLds : kDwLds];
+  if (blockIdx.x >= n_dx) {
+    short_dw<T>(dw, blockIdx.x - n_dx, lds);
+    return;
+  }
+  TileArgs a;
+  TileIndex x;
+  if (!group_rows<TILE>(dx, a, x)) return;
+  if constexpr (TILE == 64)
+    deep_tile<T, kRows, kCols, kEpiStore>(a, x, lds);
+  else
+    big_tile<T, kRows, kCols, kEpiStore, 2, 2, 2, 2, true>(a, x, lds);
 }
 
 // The tile of a product over rows of whole 16-byte chunks.  How many rows an expert has is not known here: rows of tiles are taken
@@ -322,21 +353,28 @@ bool group_grid(GroupArgs& g, int tile, int threads, uint32_t* grid) {
   return count <= (int64_t)0xFFFFFFFF / threads;
 }
 
-template <typename T, int OA, int OB, int KIND>
-hipError_t launch_experts(const GroupArgs& args, hipStream_t st) {
-  GroupArgs g = args;
+// What a launch is made of beside its grid; returns the kernel (kShortDw: k_group_dw).
+constexpr int kShortDw = 100;
+template <int OA, int OB, int KIND>
+int prepare_experts(GroupArgs& g) {
   bool whole = g.stride % 8 == 0 || OA == kCols;
   for (int m = 0; m < (OA == kCols ? g.mats : g.tile.nseg); ++m) whole = whole && whole_chunks(OA, g.tile.a[m], g.tile.lda[0], g.tile.len_a);
   for (int m = 0; m < (OA == kCols ? 1 : KIND == kEpiGated || g.tile.nseg > 1 ? 2 : 1); ++m)
     whole = whole && whole_chunks(OB, g.tile.b[m], g.tile.ldb[m], g.tile.R);
-  int kernel = g_dense_plan.kernel;
-  if (kernel == MOE_DENSE_AUTO || (!whole && kernel < MOE_DENSE_ANY64)) kernel = plan_group<OA, KIND>(g, whole);
   g.tile.splits = 1;
   const double out = OA == kCols ? 2.0 * g.E * g.mats * g.tile.M * g.tile.N : 2.0 * g.P * g.tile.N;
   g.tile.epi.stream = out >= 16e6;
+  const int kernel = g_dense_plan.kernel;
+  if (kernel != MOE_DENSE_AUTO && (whole || kernel >= MOE_DENSE_ANY64)) return kernel;
+  if (OA == kCols && whole && g.P <= kShortRows * (int64_t)g.E) return kShortDw;
+  return plan_group<OA, KIND>(g, whole);
+}
+
+template <typename T, int OA, int OB, int KIND>
+hipError_t run_experts(GroupArgs g, int kernel, hipStream_t st) {
   uint32_t grid;
   if constexpr (OA == kCols) {
-    if (whole && g_dense_plan.kernel == MOE_DENSE_AUTO && g.P <= kShortRows * (int64_t)g.E) {
+    if (kernel == kShortDw) {
       if (!group_grid<OA, KIND>(g, 128, 256, &grid)) return hipErrorInvalidConfiguration;
       k_group_dw<T><<<grid, 256, 0, st>>>(g);
       return hipGetLastError();
@@ -364,6 +402,33 @@ hipError_t launch_experts(const GroupArgs& args, hipStream_t st) {
       k_group_any<T, OA, OB, KIND, 2><<<grid, 256, 0, st>>>(g);
   }
   return hipGetLastError();
+}
+
+template <typename T, int OA, int OB, int KIND>
+hipError_t launch_experts(const GroupArgs& args, hipStream_t st) {
+  GroupArgs g = args;
+  const int kernel = prepare_experts<OA, OB, KIND>(g);
+  return run_experts<T, OA, OB, KIND>(g, kernel, st);
+}
+
+// dx (tile.nseg 0: not wanted) and dW (mats 0: not wanted).
+template <typename T>
+hipError_t launch_experts_backward_t(const GroupArgs& dx_args, const GroupArgs& dw_args, hipStream_t st) {
+  GroupArgs dx = dx_args, dw = dw_args;
+  const int kx = dx.tile.nseg ? prepare_experts<kRows, kCols, kEpiStore>(dx) : 0;
+  const int kw = dw.mats ? prepare_experts<kCols, kCols, kEpiStore>(dw) : 0;
+  const int tile = kx == MOE_DENSE_TILE64 ? 64 : kx == MOE_DENSE_TILE128 ? 128 : 0;
+  uint32_t nx, nw;
+  if (tile && kw == kShortDw && group_grid<kRows, kEpiStore>(dx, tile, 256, &nx) && (tile == 64 || nx <= kOneRound) &&
+      group_grid<kCols, kEpiStore>(dw, 128, 256, &nw) && nw <= 0x7FFFFFFF / 256) {
+    nx = (nx + 7) / 8 * 8;  // dW's tiles keep their XCDs
+    if (tile == 64) k_group_backward<T, 64><<<nx + nw, 256, 0, st>>>(dx, dw, nx);
+    else k_group_backward<T, 128><<<nx + nw, 256, 0, st>>>(dx, dw, nx);
+    return hipGetLastError();
+  }
+  hipError_t e = hipSuccess;
+  if (kx) e = run_experts<T, kRows, kCols, kEpiStore>(dx, kx, st);
+  return e != hipSuccess || !kw ? e : run_experts<T, kCols, kCols, kEpiStore>(dw, kw, st);
 }
 
 template <typename T>

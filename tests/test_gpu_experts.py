@@ -221,6 +221,36 @@ def test_bad_offsets_are_reported_and_stay_in_bounds(N):
         assert y.untouched() and dx.untouched() and torch.isnan(dw[0]).all() and torch.isnan(dw[-1]).all() and guard_ok(whole)
 
 
+@pytest.mark.parametrize("E,K,M", [(4, 64, 40), (200, 136, 72)])  # dx beside dW in 64- and in 128-square tiles
+def test_bad_offsets_of_a_whole_backward_pass(N, E, K, M):
+    P = 3 * E
+    gen = gen_for(94)
+    x, dy, wg, wu = rnd(gen, (P, K), BF16), rnd(gen, (P, M), BF16), *(stack(gen, E, M, K, BF16, 0.1) for _ in range(2))
+    d, dl = N.experts_dims(E, K, M, N.MOE_BF16, 1), N.experts_dims(E, K, M, N.MOE_BF16)
+    ws, whole = workspace(N, d, P, True)
+    good = torch.arange(0, P + 1, 3, dtype=torch.int32, device="cuda")
+    for at, value in ((0, -1), (1, -2 ** 31), (2, 2 ** 31 - 1), (E // 2, P + 1), (E, P + 1), (E, 0)):
+        offs = good.clone()
+        offs[at] = value
+        dx, dw = Out((P, K), BF16), torch.full((2, E + 2, M, K), float("nan"), dtype=BF16, device="cuda")
+        N.moe_experts_linear_backward(dl, x, offs, wg, dy, ws, dx=dx.t, dw=dw[0, 1:E + 1])
+        assert N.moe_check_device_error(ws) == N.DERR_ROWS, (at, value)
+        N.moe_experts_gated_backward(d, x, offs, wg, wu, dy, dy, dy, ws, dx=dx.t, dw_gate=dw[0, 1:E + 1], dw_up=dw[1, 1:E + 1])
+        assert N.moe_check_device_error(ws) == N.DERR_ROWS, (at, value)
+        assert dx.untouched() and torch.isnan(dw[:, 0]).all() and torch.isnan(dw[:, -1]).all() and guard_ok(whole)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("counts,K,M", [
+    ([0, 40, 3, 0, 129, 257, 1, 0] * 2, 1544, 264),  # dx of 13 columns of 128-square tiles
+    ([5, 0, 300, 131], 2056, 136),  # of 33 columns of 64-square ones
+    ([2] * 260, 136, 392),  # more than a round of tiles: dx alone, then dW
+    ([3, 1] * 64, 264, 136),
+])
+def test_dx_and_dw_together(N, counts, K, M, dt):
+    check_all(N, K + M, counts, K, M, dt, lead=2, tail=3)
+
+
 def test_nan_and_infinity_stay_with_their_expert(N):
     gen = gen_for(91)
     counts, K, M = [40, 3, 70], 128, 96
