@@ -715,8 +715,9 @@ MOE_API int moe_experts_gated_backward(const moe_experts_dims* dims, const void*
  *   - Sums are in a fixed order: equal calls give equal bits.
  *   - 1 <= n_in, vocab <= MOE_DENSE_MAX_WIDTH; 1 <= n_tokens <= MOE_LOSS_MAX_TOKENS (beyond: MOE_EUNSUPPORTED).
  *   - moe_debug_force_dense_plan holds here too.
- *   - `ws`: moe_loss_workspace_bytes(dims, n_tokens, backward) bytes: for the backward pass about 256 MiB of dz and, with
- *     more than one piece, dx in fp32.
+ *   - `ws`: moe_loss_workspace_bytes(dims, n_tokens or more, backward) bytes.  Forward: 8 bytes per 64 columns and a copy of x,
+ *     both for 8192 tokens at most, and a copy of W where n_in is no multiple of 8.  Backward: that with a copy of all of x, up
+ *     to 256 MiB of dz (beyond 2^19 tokens 512 bytes per token), with more than one piece dx in fp32, up to 32 MiB of split sums.
  */
 #define MOE_LOSS_MAX_TOKENS (1 << 20)
 

@@ -31,18 +31,22 @@ static int64_t piece_columns(int64_t T, int64_t V) {
   return c < all ? c : all;
 }
 
+// Every part's room never falls as tokens are added, so that the workspace of one count serves those below it: dz has at most
+// max(kLossDzBytes / 2, 256 T) elements however its piece is rounded, and a smaller count's larger piece (all of the vocabulary at
+// most) bounds the split sums of dW.
 static LossWs loss_ws(const moe_loss_dims* d, int64_t T, bool backward) {
   LossWs L{};
-  const int64_t V = d->vocab, chunk = T < kLossTokens ? T : kLossTokens;
+  const int64_t V = d->vocab, whole = (V + 7) / 8 * 8, chunk = T < kLossTokens ? T : kLossTokens;
   L.ld_in = ((int64_t)d->n_in + 7) / 8 * 8;
   size_t off = kCtrlBytes;
   L.scale = off;
   off = dense_align(off + 2 * sizeof(float));
   L.part = off;
   off = dense_align(off + sizeof(float2) * (size_t)(chunk * ((V + kLossTile - 1) / kLossTile)));
-  // copies of operands without whole 16-byte rows: x always (its stride is the caller's), the weights when n_in says so
+  // copies of operands without whole 16-byte rows: x always (its stride is the caller's; the forward pass takes a launch's tokens
+  // at a time), the weights when n_in says so
   L.x = off;
-  off = dense_align(off + 2 * (size_t)(T * L.ld_in));
+  off = dense_align(off + 2 * (size_t)((backward ? T : chunk) * L.ld_in));
   if (d->n_in % 8) {
     L.w = off;
     off = dense_align(off + 2 * (size_t)(V * L.ld_in));
@@ -50,15 +54,18 @@ static LossWs loss_ws(const moe_loss_dims* d, int64_t T, bool backward) {
   if (backward) {
     L.piece = piece_columns(T, V);
     L.ldz = L.piece;
+    const int64_t limit = (int64_t)(kLossDzBytes / 2) > 256 * T ? (int64_t)(kLossDzBytes / 2) : 256 * T;
     L.dz = off;
-    off = dense_align(off + 2 * (size_t)(T * L.ldz));
+    off = dense_align(off + 2 * (size_t)(T * whole < limit ? T * whole : limit));
     L.acc = off;
     if (L.piece < V) off = dense_align(off + sizeof(float) * (size_t)(T * L.ld_in));
     L.sums = off;
-    const size_t dx = split_bytes(kMaxSplits, 1, T, d->n_in), dw = split_bytes(kMaxSplits, 1, L.piece, d->n_in);
-    L.sums_bytes = dx > dw ? dx : dw;
-    if (L.sums_bytes > kDensePartBytes) L.sums_bytes = kDensePartBytes;
-    off = dense_align(off + L.sums_bytes);
+    auto sums = [&](int64_t piece) {
+      const size_t dx = split_bytes(kMaxSplits, 1, T, d->n_in), dw = split_bytes(kMaxSplits, 1, piece, d->n_in), most = dx > dw ? dx : dw;
+      return most < kDensePartBytes ? most : kDensePartBytes;
+    };
+    L.sums_bytes = sums(L.piece);
+    off = dense_align(off + sums(whole));
   }
   L.total = off;
   return L;

@@ -130,6 +130,25 @@ def test_vocabulary_in_several_pieces(N, dt):
     check_all(N, 44, 40001, 33, 3077, dt)
 
 
+def test_fewer_tokens_on_the_workspace_of_more(N):
+    """A workspace sized for one count serves those below it, whose pieces of the vocabulary are larger."""
+    K, V, many, few = 40, 32768, 4229, 4228
+    gen = gen_for(51)
+    x, w, targets = inputs(gen, many, K, V, BF16)
+    d = N.loss_dims(K, V, N.MOE_BF16, IGNORE)
+    got = []
+    for size in (few, many):
+        ws, whole = workspace(N, d, size, True)
+        loss, lse = floats(few, 2)
+        N.moe_loss_forward(d, x[:few], few, w, targets[:few], loss, lse, ws)
+        dx, dw = torch.empty_like(x[:few]), torch.empty_like(w)
+        N.moe_loss_backward(d, x[:few], few, w, targets[:few], loss, lse, torch.ones(few, device="cuda"), ws, dx=dx, dw=dw)
+        assert N.moe_check_device_error(ws) == 0 and guard_ok(whole)
+        got.append((loss, lse, dx, dw))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_small_losses_keep_their_digits(N):
     """Targets ahead by up to 40: losses down to 2^-58, each within a relative bound."""
     T, V = 41, 300

@@ -82,6 +82,18 @@ def test_workspace_does_not_hold_the_logits(N):
     assert N.moe_loss_workspace_bytes(d, 65536) < 65536 * 2048 * 2 + (256 << 20)
 
 
+@pytest.mark.parametrize("K,V", [(2048, 100003), (2048, 32768), (1024, 50304), (33, 3077), (64, 300), (1, 1 << 20)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_workspace_serves_every_smaller_count(N, K, V, backward):
+    """The size for max_tokens is enough for each count up to it: it never falls as tokens are added."""
+    d = N.loss_dims(K, V, N.MOE_BF16)
+    most = 0
+    for t in [*range(1, 16385), *range(16385, (1 << 20) - 300, 997), *range((1 << 20) - 300, (1 << 20) + 1)]:
+        n = N.moe_loss_workspace_bytes(d, t, backward)
+        assert n >= most, t
+        most = n
+
+
 def test_binding_refuses_mismatched_tensors(N):
     d = N.loss_dims(64, 32, N.MOE_BF16)
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(32, 64, dtype=torch.bfloat16)
