@@ -29,7 +29,8 @@ MOE_DEV int clamp_rows(int v, int P) { return v < 0 ? 0 : (v > P ? P : v); }
 
 // Rows of tiles of TI rows over all experts, and this lane's share: experts lane * per .. + per - 1.  Offsets that do not
 // ascend within 0 .. P are taken as clamped to it and an expert's negative rows as none: no row outside the matrices
-// is ever named; one workgroup reports them.
+// is ever named; one workgroup reports them.  Rows that such offsets name many times over would take the sums past 32 bits (1024
+// experts of 2^28 rows each), so a lane counts no more tiles than good offsets can give it.
 template <int TI>
 MOE_DEV int count_tiles(const GroupArgs& g, int per, int& mine, int& incl) {
   const int lane = threadIdx.x & 63;
@@ -52,6 +53,7 @@ MOE_DEV int count_tiles(const GroupArgs& g, int per, int& mine, int& incl) {
     }
   }
   if (blockIdx.x == 0 && threadIdx.x < 64 && bad) set_error(g.ctrl, MOE_DERR_ROWS);
+  mine = mine < g.P / TI + per ? mine : g.P / TI + per;
   incl = wave_scan(mine);
   return __builtin_amdgcn_readlane(incl, 63);
 }

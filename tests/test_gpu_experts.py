@@ -221,6 +221,27 @@ def test_bad_offsets_are_reported_and_stay_in_bounds(N):
         assert y.untouched() and dx.untouched() and torch.isnan(dw[0]).all() and torch.isnan(dw[-1]).all() and guard_ok(whole)
 
 
+@pytest.mark.parametrize("kernel", [1, 4])  # the two of 64 rows, which count the most tiles
+def test_offsets_that_name_every_row_many_times(N, kernel):
+    """2^28 rows, the limit, named by every other of 1024 experts: 2^31 rows of tiles."""
+    P, E, K, M = 1 << 28, 1024, 8, 8
+    d = N.experts_dims(E, K, M, N.MOE_BF16)
+    offs = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offs[1::2] = P
+    x, w = torch.ones(P, K, dtype=BF16, device="cuda"), torch.ones(E, M, K, dtype=BF16, device="cuda")
+    ws, whole = workspace(N, d, P, True)
+    N.moe_debug_force_dense_plan(kernel)
+    try:
+        y = Out((P, M), BF16)
+        N.moe_experts_linear_forward(d, x, offs, w, y.t, ws)
+        assert N.moe_check_device_error(ws) == N.DERR_ROWS
+        N.moe_experts_linear_backward(d, x, offs, w, x, ws, dx=y.t)
+        assert N.moe_check_device_error(ws) == N.DERR_ROWS
+        assert torch.isnan(y.buf[0]).all() and torch.isnan(y.buf[-1]).all() and guard_ok(whole)
+    finally:
+        N.moe_debug_force_dense_plan()
+
+
 @pytest.mark.parametrize("E,K,M", [(4, 64, 40), (200, 136, 72)])  # dx beside dW in 64- and in 128-square tiles
 def test_bad_offsets_of_a_whole_backward_pass(N, E, K, M):
     P = 3 * E
