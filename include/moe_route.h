@@ -708,8 +708,11 @@ MOE_API int moe_experts_gated_backward(const moe_experts_dims* dims, const void*
  *     that a small loss keeps its relative precision; the gradient takes both saved values for the same reason
  *     (exp(z - lse) - 1 at the target is expm1(-loss)).
  *   - The backward pass computes the logits again and rounds dz to dims->dtype before the products, with dloss taken
- *     relative to the largest |dloss| of the call (fp16: brought to 2^11; undone in fp32 afterwards): in fp16 a token whose dloss is
- *     less than 2^-20 of the largest loses precision.  A result past 65504 is an infinity, one below 2^-25 zero: scale dloss.
+ *     relative to the largest |dloss| of the call (undone in fp32 afterwards).  fp16: relative to a power of two near the
+ *     token's own, so that its probabilities keep fp16's precision down to 2^-27 and are zero below 2^-38, however its dloss
+ *     compares; dW then takes x times the token's share of the largest |dloss| (a power of two), rounded to fp16 with the call's
+ *     largest |x| at 2^14: exact down to 2^-28 of that, zero below 2^-39.  A result past 65504 is an infinity, one below 2^-25
+ *     zero: scale dloss.
  *   - An infinite logit gives the limits: loss 0 where it is the target's alone, infinite where it is another's (the
  *     gradient of that column is then NaN), NaN where it is both; a NaN stays in its token, its dx and the dW it reaches.
  *   - Sums are in a fixed order: equal calls give equal bits.
@@ -717,7 +720,8 @@ MOE_API int moe_experts_gated_backward(const moe_experts_dims* dims, const void*
  *   - moe_debug_force_dense_plan holds here too.
  *   - `ws`: moe_loss_workspace_bytes(dims, n_tokens or more, backward) bytes.  Forward: 8 bytes per 64 columns and a copy of x,
  *     both for 8192 tokens at most, and a copy of W where n_in is no multiple of 8.  Backward: that with a copy of all of x, up
- *     to 256 MiB of dz (beyond 2^19 tokens 512 bytes per token), with more than one piece dx in fp32, up to 32 MiB of split sums.
+ *     to 256 MiB of dz (beyond 2^19 tokens 512 bytes per token), with more than one piece dx in fp32, up to 32 MiB of split sums;
+ *     fp16: another copy of x.
  */
 #define MOE_LOSS_MAX_TOKENS (1 << 20)
 

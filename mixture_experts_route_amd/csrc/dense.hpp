@@ -169,10 +169,11 @@ enum DenseEpiKind { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2,
 // The loss's epilogues (moe_loss_*); the arrays are indexed by the product's rows.
 struct LossEpi {
   const int32_t* targets;
-  const float *loss, *lse, *dloss;  // kEpiLossDz
+  const float *loss, *lse, *dloss;  // kEpiLossDz (fp16's dloss: scaled already)
   float2* part;                     // kEpiLoss: [tiles_j][M], the target's column left out
-  const float* scale;               // kEpiLossDz: dloss's factor; kEpiSum: the results' (NULL: 1, for sums that go on)
+  const float* scale;               // kEpiLossDz, bf16: dloss's factor; kEpiSum: the results' (NULL: 1, for sums that go on)
   const float* acc;                 // kEpiSum: the earlier sums, row stride DenseEpi::ldr (NULL: none)
+  const float* row_scale;           // kEpiSum: a factor for each row in scale's place (NULL: none)
   int32_t* ctrl;
   int32_t col0, vocab, ignore;      // the product's first column, and all of them
 };
@@ -243,7 +244,7 @@ MOE_DEV void finish8(const DenseEpi& e, int batch, int64_t i, int j, int n, floa
       for (int c = 0; c < 8; ++c) s0[c] += t[c];
     }
     if (e.loss.scale) {
-      const float f = *e.loss.scale;
+      const float f = e.loss.row_scale ? e.loss.row_scale[i] : *e.loss.scale;
 #pragma unroll
       for (int c = 0; c < 8; ++c) s0[c] *= f;
     }

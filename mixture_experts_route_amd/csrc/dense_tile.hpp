@@ -218,11 +218,12 @@ MOE_DEV void gate_block(const float4v (&g)[FI][FJ], const float4v (&u)[FI][FJ], 
 
 // All of a wave's sums: NI x 2 blocks, block (h, hj) at rows i0 + h di, columns j0 + hj dj (gated: hj = 0 the
 // gate's, 1 the up's sums of the same outputs).
-template <typename T, int KIND, int NI, int FI, int FJ>
+template <typename T, int KIND, int OA, int NI, int FI, int FJ>
 MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, int64_t di, int64_t j0, int64_t dj,
                            const float4v (&s)[NI][2][FI][FJ], float* lds, int lane) {
   const DenseEpi& e = a.epi;
   constexpr bool kGated = KIND == kEpiGated;
+  constexpr bool kRowScale = __is_same(T, _Float16) && OA == kRows;  // kEpiSum: dx, whose rows are tokens
   if constexpr (kGated) {
     if (x.splits == 1 && !e.bias[0] && !e.bias[1] && !e.pre[0]) {
 #pragma unroll
@@ -243,7 +244,8 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
   }
   if constexpr (KIND == kEpiLossDz) {
     const LossEpi& l = e.loss;
-    const float scale = *l.scale;
+    constexpr bool kScaled = __is_same(T, _Float16);
+    const float scale = kScaled ? 1.0f : *l.scale;
     const bool inside = j0 + dj + FJ * 16 <= a.N;
 #pragma unroll
     for (int h = 0; h < NI; ++h) {
@@ -255,7 +257,7 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
         const int target = l.targets[row];
         const bool live = (uint32_t)target < (uint32_t)l.vocab && target != l.ignore;
         if (!live && target != l.ignore && j0 == 0 && l.col0 == 0) set_error(l.ctrl, MOE_DERR_TARGET);
-        const float lse = l.lse[row], g = l.dloss[row] * scale;
+        const float lse = l.lse[row], g = kScaled ? l.dloss[row] : l.dloss[row] * scale;
         const int at = target - l.col0 - (int)j0;  // its column in this block
 #pragma unroll
         for (int hj = 0; hj < 2; ++hj)
@@ -288,18 +290,24 @@ MOE_DEV void finish_blocks(const TileArgs& a, const TileIndex& x, int64_t i0, in
   }
   if constexpr (KIND == kEpiSum) {
     if (x.splits == 1 && !e.loss.acc && !e.y_f32) {  // scaled in the registers
-      const float scale = *e.loss.scale;
+      const float scale = kRowScale ? 1.0f : *e.loss.scale;
 #pragma unroll
       for (int h = 0; h < NI; ++h)
 #pragma unroll
         for (int hj = 0; hj < 2; ++hj) {
           float4v v[FI][FJ];
 #pragma unroll
-          for (int f = 0; f < FI; ++f)
+          for (int f = 0; f < FI; ++f) {
+            float of_row = scale;
+            if constexpr (kRowScale) {
+              const int64_t i = i0 + h * di + f * 16 + (lane & 15);
+              of_row = e.loss.row_scale[i < a.M ? i : a.M - 1];
+            }
 #pragma unroll
             for (int n = 0; n < FJ; ++n)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) v[f][n][c] = s[h][hj][f][n][c] * scale;
+              for (int c = 0; c < 4; ++c) v[f][n][c] = s[h][hj][f][n][c] * of_row;
+          }
           store_block<T, FI, FJ>(e.y[0], e.ldy[0], i0 + h * di, j0 + hj * dj, a.M, a.N, e.stream, v, (uint16_t*)lds, lane);
         }
       return;
@@ -576,7 +584,7 @@ MOE_DEV void any_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   if constexpr (KIND == kEpiLoss)
     finish_loss<2 * H, 2>(a, x, i0 + wi * 16 * F, H, j0 + wj * 16 * F, H, wj, acc, (float*)lds, lane);
   else
-    finish_blocks<T, KIND>(a, x, i0 + wi * 16 * F, H, j0 + wj * 16 * F, H, acc,
+    finish_blocks<T, KIND, OA>(a, x, i0 + wi * 16 * F, H, j0 + wj * 16 * F, H, acc,
                            (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * F * F * 256, lane);
 }
 
@@ -819,7 +827,7 @@ MOE_DEV void deep_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   if constexpr (KIND == kEpiLoss)
     finish_loss<HI, 2>(a, x, i0 + wi * 32, 0, j0 + wj * 16, HJ, wj, s, (float*)lds, lane);
   else
-    finish_blocks<T, KIND>(a, x, i0 + wi * 32, 0, j0 + wj * 16, HJ, s, (float*)lds + wave * 1024, lane);
+    finish_blocks<T, KIND, OA>(a, x, i0 + wi * 32, 0, j0 + wj * 16, HJ, s, (float*)lds + wave * 1024, lane);
 }
 
 template <typename T, int OA, int OB, int KIND>
@@ -993,7 +1001,7 @@ MOE_DEV void big_tile(const TileArgs& a, const TileIndex& x, uint16_t* lds) {
   if constexpr (KIND == kEpiLoss)
     finish_loss<2 * HI, WJ>(a, x, i0 + wi * FI * 16, HI, j0 + wj * FJ * 16, HJ, wj, acc, (float*)lds, lane);
   else
-    finish_blocks<T, KIND>(a, x, i0 + wi * FI * 16, HI, j0 + wj * FJ * 16, HJ, acc,
+    finish_blocks<T, KIND, OA>(a, x, i0 + wi * FI * 16, HI, j0 + wj * FJ * 16, HJ, acc,
                            (float*)lds + wave * (KIND == kEpiGated ? 2 : 1) * FI * FJ * 256, lane);
 }
 

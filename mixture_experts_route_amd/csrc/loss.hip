@@ -16,9 +16,11 @@ constexpr int kLossTokens = 8192;          // tokens of a forward launch: bounds
 // head, 325 us in one piece, 372 in pieces of 128 MiB of weights.
 constexpr size_t kLossDzBytes = 256u << 20;
 constexpr int kLossTile = 64;              // the smallest tile's columns
+constexpr int kMostBlocks = 256;           // workgroups that look for fp16's largest |x|
+constexpr int64_t kLiftFew = 1 << 17;      // elements of x up to which each does so for itself (5 x 2048: 333 us against 340)
 
 struct LossWs {
-  size_t part, scale, x, w, dz, acc, sums, sums_bytes, total;
+  size_t part, scale, scaled, undo, most, x, lifted, w, dz, acc, sums, sums_bytes, total;
   int64_t ld_in, piece, ldz;
 };
 
@@ -40,7 +42,7 @@ static LossWs loss_ws(const moe_loss_dims* d, int64_t T, bool backward) {
   L.ld_in = ((int64_t)d->n_in + 7) / 8 * 8;
   size_t off = kCtrlBytes;
   L.scale = off;
-  off = dense_align(off + 2 * sizeof(float));
+  off = dense_align(off + 4 * sizeof(float));
   L.part = off;
   off = dense_align(off + sizeof(float2) * (size_t)(chunk * ((V + kLossTile - 1) / kLossTile)));
   // copies of operands without whole 16-byte rows: x always (its stride is the caller's; the forward pass takes a launch's tokens
@@ -52,6 +54,16 @@ static LossWs loss_ws(const moe_loss_dims* d, int64_t T, bool backward) {
     off = dense_align(off + 2 * (size_t)(V * L.ld_in));
   }
   if (backward) {
+    if (d->dtype == MOE_F16) {
+      L.scaled = off;
+      off = dense_align(off + sizeof(float) * (size_t)T);
+      L.undo = off;
+      off = dense_align(off + sizeof(float) * (size_t)T);
+      L.most = off;
+      off = dense_align(off + sizeof(float) * kMostBlocks);
+      L.lifted = off;
+      off = dense_align(off + 2 * (size_t)(T * L.ld_in));
+    }
     L.piece = piece_columns(T, V);
     L.ldz = L.piece;
     const int64_t limit = (int64_t)(kLossDzBytes / 2) > 256 * T ? (int64_t)(kLossDzBytes / 2) : 256 * T;
@@ -192,26 +204,136 @@ static hipError_t start_join(const LossJoinArgs& j, hipStream_t st) {
 // dz is formed with dloss over the largest |dloss|, and the products are multiplied by that again, in fp32: with the same dloss
 // for every token, a mean's 1 / count, an unsure token's dz at its target is then near -1, which no rounding moves, and not
 // near -dloss, which one and the same rounding moves for all of them (bf16: dx and dW of a few tokens up to 2.6e-3 off their
-// definition that way, 1.7e-3 to 2.0e-3 so; the plain form 1.7e-3).  fp16's dz is brought to 2^11 by it: at most 2048 at a target,
-// normal down to probabilities of 2^-25, 8 bits left at 2^-32.  out = {factor of dloss, factor of the products}.
-__global__ __launch_bounds__(1024) void k_loss_scale(const float* dloss, const int32_t* targets, int T, int vocab, int ignore,
-                                                     float most_dz, float* out) {
-  __shared__ float most[16];
+// definition that way, 1.7e-3 to 2.0e-3 so; the plain form 1.7e-3).
+// fp16 has not the range for one factor: a token whose dloss is 2^-20 of the largest would have no probabilities below 2^-16 left, most
+// of its softmax (its dx had the wrong sign).  So each token has a power of two of its own besides, 2^lift, that brings its dz to
+// 2^13 .. 2^15 at a probability of 1: normal down to probabilities of 2^-27, zero below 2^-38.  dx undoes it row by row; for
+// dW, whose sum runs over the tokens, x carries 2^-lift in a copy, the call's largest |x| brought to 2^14 (exact down to 2^-28 of
+// that).  Up to kLiftFew elements of x every workgroup finds the maxima by itself, in one launch, else two.  Against one factor,
+// fp16: 5 tokens, 100003 x 2048, 328 -> 333 us; 333 tokens, 32771 x 1000, 134 -> 140; 8192 tokens, 100003 x 2048, 8.33 -> 8.35 ms.
+struct LossScaleArgs {
+  const float* dloss;
+  const int32_t* targets;
+  const void* x;
+  float* scale;             // {factor of dloss, of the products, of fp16's dW, the largest |dloss|}
+  float *scaled, *undo;     // fp16: each token's dloss with its factor; what dx undoes
+  float* most;              // the largest |x| of each workgroup behind the first
+  void* lifted;
+  int64_t ldx, ld_lifted;
+  float most_dz;
+  int32_t T, K, vocab, ignore, blocks;  // blocks: that `most` has
+  MOE_DEV bool live(int t) const { return (uint32_t)targets[t] < (uint32_t)vocab && targets[t] != ignore; }
+};
+
+// The largest m and x of 1024 threads, for all of them.
+MOE_DEV void most_of_all(float& m, float& x) {
+  __shared__ float2 most[16];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    m = fmaxf(m, __shfl_xor(m, o, 64));
+    x = fmaxf(x, __shfl_xor(x, o, 64));
+  }
+  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = make_float2(m, x);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    m = fmaxf(m, most[i].x);
+    x = fmaxf(x, most[i].y);
+  }
+}
+
+// A thread's share of the largest |dloss|.
+MOE_DEV float most_dloss(const LossScaleArgs& a) {
   float m = 0.0f;
 #pragma unroll 4
-  for (int t = threadIdx.x; t < T; t += 1024) {
-    const float g = fabsf(dloss[t]);
-    if ((uint32_t)targets[t] < (uint32_t)vocab && targets[t] != ignore && g < INFINITY) m = fmaxf(m, g);
+  for (int t = threadIdx.x; t < a.T; t += 1024) {
+    const float g = fabsf(a.dloss[t]);
+    if (a.live(t) && g < INFINITY) m = fmaxf(m, g);
   }
+  return m;
+}
+MOE_DEV float scale_base(float m) { return fminf(fmaxf(m, 0x1p-100f), 0x1p100f); }
+
+// A thread's share of the largest finite |x| of the tokens first, first + step ..., a wave each.
+MOE_DEV float most_x(const LossScaleArgs& a, int first, int step) {
+  const int lane = threadIdx.x & 63;
+  float m = 0.0f;
+  for (int t = first + (threadIdx.x >> 6); t < a.T; t += step) {
+    if (!a.live(t)) continue;
+#pragma unroll 4
+    for (int c = lane * 8; c < a.K; c += 512) {
+      float v[8];
+      load8<_Float16>(a.x, t * a.ldx + c, a.K - c < 8 ? a.K - c : 8, v);
 #pragma unroll
-  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x) return;
-  for (int i = 1; i < 16; ++i) m = fmaxf(m, most[i]);
-  m = fminf(fmaxf(m, 0x1p-100f), 0x1p100f);
-  out[0] = most_dz / m;
-  out[1] = m / most_dz;
+      for (int i = 0; i < 8; ++i) m = fabsf(v[i]) < INFINITY ? fmaxf(m, fabsf(v[i])) : m;
+    }
+  }
+  return m;
+}
+
+MOE_DEV int lift_of(float m, float dloss) {
+  const float g = fabsf(dloss);
+  const int below = ilogbf(m) - (g > 0.0f && g < INFINITY ? ilogbf(g) : 1000);
+  return below < 0 || below > 150 ? 0 : below;
+}
+
+// By the workgroup that writes them: the factors, and fp16's of every token.
+MOE_DEV void store_scale(const LossScaleArgs& a, float m) {
+  const float scale = a.most_dz / m, back = m / a.most_dz;
+  if (threadIdx.x == 0) {
+    a.scale[0] = scale;
+    a.scale[1] = back;
+    a.scale[3] = m;
+  }
+  if (!a.scaled) return;
+#pragma unroll 4
+  for (int t = threadIdx.x; t < a.T; t += 1024) {
+    const float g = a.dloss[t];
+    const int lift = lift_of(m, g);
+    a.scaled[t] = __builtin_ldexpf(g * scale, lift);
+    a.undo[t] = __builtin_ldexpf(back, -lift);
+  }
+}
+
+__global__ __launch_bounds__(1024) void k_loss_scale(LossScaleArgs a) {
+  float m = 0.0f, x = 0.0f;
+  if (blockIdx.x == 0) m = most_dloss(a);
+  else x = most_x(a, ((int)blockIdx.x - 1) * 16, a.blocks * 16);
+  most_of_all(m, x);
+  if (blockIdx.x == 0) store_scale(a, scale_base(m));
+  else if (threadIdx.x == 0) a.most[blockIdx.x - 1] = x;
+}
+
+// lifted = x 2^(k - lift) in rows of whole chunks, zero for a token without a gradient; dW's factor is the products' times 2^-k.
+template <bool FEW>
+__global__ __launch_bounds__(1024) void k_loss_lift(LossScaleArgs a) {
+  const int lane = threadIdx.x & 63;
+  float m = 0.0f, x = 0.0f;
+  if constexpr (FEW) {
+    m = most_dloss(a);
+    x = most_x(a, 0, 16);
+    most_of_all(m, x);
+    m = scale_base(m);
+    if (blockIdx.x == 0) store_scale(a, m);
+  } else {
+    m = a.scale[3];
+    for (int i = lane; i < a.blocks; i += 64) x = fmaxf(x, a.most[i]);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
+  }
+  const int k = x > 0.0f ? 14 - ilogbf(x) : 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.scale[2] = __builtin_ldexpf(m / a.most_dz, -k);
+  for (int t = blockIdx.x * 16 + (threadIdx.x >> 6); t < a.T; t += gridDim.x * 16) {
+    const bool live = a.live(t);
+    const int by = k - lift_of(m, a.dloss[t]);
+    for (int c = lane * 8; c < a.K; c += 512) {
+      float v[8];
+      load8<_Float16>(a.x, t * a.ldx + c, a.K - c < 8 ? a.K - c : 8, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = live ? __builtin_ldexpf(v[i], by) : 0.0f;
+      store8<_Float16>(a.lifted, t * a.ld_lifted + c, 8, v);
+    }
+  }
 }
 
 static int check_loss(const moe_loss_dims* d) {
@@ -323,8 +445,6 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
   const LossWs L = loss_ws(dims, n_tokens, true);
   auto at = [&](size_t off) { return (uint8_t*)ws + off; };
   float* scale = (float*)at(L.scale);
-  k_loss_scale<<<1, 1024, 0, st>>>(dloss, targets, n_tokens, dims->vocab, dims->ignore, bf16 ? 1.0f : 0x1p11f, scale);
-  if (hipGetLastError() != hipSuccess) return MOE_EHIP;
   const void *xs = x, *wt = w;
   int64_t ld_x = ldx, ld_w = ldw;
   int32_t len = dims->n_in;
@@ -344,6 +464,37 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
     ld_w = len = L.ld_in;
   }
   if (p.count && (rc = dense_status(launch_pack(p, st)))) return rc;
+  LossScaleArgs f{};
+  f.dloss = dloss;
+  f.targets = targets;
+  f.x = xs;
+  f.ldx = ld_x;
+  f.scale = scale;
+  if (!bf16) {
+    f.scaled = (float*)at(L.scaled);
+    f.undo = (float*)at(L.undo);
+  }
+  f.most_dz = bf16 ? 1.0f : 0x1p14f;
+  f.T = n_tokens;
+  f.K = dims->n_in;
+  f.vocab = dims->vocab;
+  f.ignore = dims->ignore;
+  const void* x_dw = xs;  // dW's x and its stride
+  int64_t ld_xdw = ld_x;
+  const int32_t rows = (n_tokens + 15) / 16;  // a wave each
+  if (!bf16 && dw_or_null) {
+    f.most = (float*)at(L.most);
+    x_dw = f.lifted = at(L.lifted);
+    ld_xdw = f.ld_lifted = L.ld_in;
+    f.blocks = rows < kMostBlocks ? rows : kMostBlocks;
+  }
+  if (f.lifted && (int64_t)n_tokens * dims->n_in <= kLiftFew) {
+    k_loss_lift<true><<<rows, 1024, 0, st>>>(f);
+  } else {
+    k_loss_scale<<<1 + f.blocks, 1024, 0, st>>>(f);
+    if (f.lifted) k_loss_lift<false><<<rows < 1024 ? rows : 1024, 1024, 0, st>>>(f);
+  }
+  if (hipGetLastError() != hipSuccess) return MOE_EHIP;
   for (int32_t c0 = 0; c0 < dims->vocab; c0 += L.piece) {
     const int32_t cols = dims->vocab - c0 < L.piece ? dims->vocab - c0 : (int32_t)L.piece, whole = (cols + 7) / 8 * 8;
     const bool first = c0 == 0, last = c0 + cols == dims->vocab;
@@ -360,7 +511,7 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
     z.epi.ldy[0] = L.ldz;
     z.epi.loss.loss = loss;
     z.epi.loss.lse = lse;
-    z.epi.loss.dloss = dloss;
+    z.epi.loss.dloss = bf16 ? dloss : f.scaled;
     z.epi.loss.scale = scale;
     z.epi.loss.col0 = c0;
     if ((rc = dense_status(bf16 ? launch_loss_dz_bf16(z, st) : launch_loss_dz_f16(z, st)))) return rc;
@@ -372,12 +523,12 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
     s.lda[0] = L.ldz;
     if (dw_or_null) {
       TileArgs a = s;
-      a.b[0] = xs;
-      a.ldb[0] = ld_x;
+      a.b[0] = x_dw;
+      a.ldb[0] = ld_xdw;
       a.M = cols;
       a.N = dims->n_in;
       a.R = n_tokens;
-      a.epi.loss.scale = scale + 1;
+      a.epi.loss.scale = bf16 ? scale + 1 : scale + 2;
       a.epi.y[0] = (uint16_t*)dw_or_null + c0 * ld_dw;
       a.epi.ldy[0] = ld_dw;
       if ((rc = dense_status(bf16 ? launch_loss_dw_bf16(a, st) : launch_loss_dw_f16(a, st)))) return rc;
@@ -396,6 +547,7 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
       a.epi.y[0] = last ? dx_or_null : at(L.acc);
       a.epi.ldy[0] = last ? ld_dx : L.ld_in;
       a.epi.loss.scale = last ? scale + 1 : nullptr;
+      a.epi.loss.row_scale = f.undo;
       if ((rc = dense_status(bf16 ? launch_loss_dx_bf16(a, st) : launch_loss_dx_f16(a, st)))) return rc;
     }
   }

@@ -170,6 +170,58 @@ def test_small_losses_keep_their_digits(N):
     assert ((dx[:, 0].double() - want).abs() <= want.abs() * (2 * R.half_step(BF16) + 300 * R.E)).all()
 
 
+def spread_bounds(x, w, targets, loss, lse, dloss):
+    """dx and dW of fp16 with the bounds of loss_reference.backward, but each token's dz rounded relative to its own dloss: brought
+    to 2^13 .. 2^15, so that an error of half of fp16's smallest number is 2^-25 / 2^13 of dloss; and x times the token's share s of
+    the largest dloss (a power of two: within a factor of two of it) rounded to 2^-25 where the largest |x| is at 2^14 or above, which
+    is 2^-39 of it; undone by a share of at least half of dloss's."""
+    dz, e = L.dz_of(x, w, targets, IGNORE, loss, lse, dloss)
+    live = (targets != IGNORE)[:, None]
+    x, w, g = x.double(), w.double(), dloss.double().abs()[:, None]
+    r = e + R.half_step(F16) * (dz.abs() + e) + torch.where(live, g * 2.0 ** -38, 0.0)
+    dx, dw = dz @ w, dz.T @ x
+    e_dx = r @ w.abs() + 2 * w.shape[0] * R.E * ((dz.abs() + r) @ w.abs())
+    share = torch.where(live, 2 * g / g[live].max(), 0.0).clamp(max=1.0)
+    ex = 2.0 ** -39 * x[live[:, 0]].abs().max() * 4 / share.clamp(min=2.0 ** -60)
+    e_dw = r.T @ x.abs() + (dz.abs() + r).T @ torch.where(live, ex, 0.0) + 2 * len(x) * R.E * ((dz.abs() + r).T @ x.abs())
+    return {"dx": (dx, R._round(dx, e_dx, F16)), "dw": (dw, R._round(dw, e_dw, F16))}
+
+
+def check_past_range(name, got, ref):
+    """R.check, but fp16's largest number is 65504 and its half step there 16: what is 65520 or more is infinite."""
+    val, bound = ref
+    inf = torch.isinf(got) & (val.abs() + bound >= 65520) & (torch.sign(got) == torch.sign(val))
+    assert inf[val.abs() - bound >= 65520].all()
+    R.check(name, torch.where(inf, 0.0, got), (torch.where(inf, 0.0, val), bound))
+
+
+@pytest.mark.parametrize("T,K,V,pad", [(24, 64, 50000, 0), (24, 61, 20011, 0), (240, 40, 30000, 3), (700, 33, 5001, 0)])
+def test_fp16_tokens_of_very_different_weight(N, T, K, V, pad):
+    """dloss over twenty-three powers of two: every token's dx keeps its softmax part, relative to its own dloss.  The weights have a
+    mean, so that this part is as large as the target's; dloss is large enough for the results to be normal numbers."""
+    gen = gen_for(52 + T)
+    x = rnd(gen, (T, K), F16, pad=pad)
+    w = ((torch.randn(V, K, generator=gen, device="cuda") * 0.3 + 1.0) * K ** -0.5).to(F16)
+    targets = torch.randint(0, V, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    targets[3::17] = IGNORE
+    dloss = (1.0 + torch.rand(T, generator=gen, device="cuda")) * 2.0 ** (14.0 - torch.arange(T, device="cuda") % 24)
+    dloss[::2] *= -1
+    dloss[3::17] = 1e30
+    d = N.loss_dims(K, V, N.MOE_F16, IGNORE)
+    ws, whole = workspace(N, d, T, True)
+    loss, lse = floats(T, 2)
+    N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+    dx, dw = Out((T, K), F16, pad), Out((V, K), F16, pad)
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dx=dx.t, dw=dw.t)
+    ref = spread_bounds(x, w, targets, loss, lse, dloss)
+    check_past_range("dx", dx.t, ref["dx"])
+    check_past_range("dw", dw.t, ref["dw"])
+    one, two = torch.empty_like(dx.t), torch.empty_like(dw.t)
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dx=one)
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dw=two)
+    assert torch.equal(one, dx.t) and torch.equal(two, dw.t) and guard_ok(whole) and N.moe_check_device_error(ws) == 0
+
+
 def test_targets_out_of_range_are_reported(N):
     T, K, V = 40, 64, 300
     gen = gen_for(45)
