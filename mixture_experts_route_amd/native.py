@@ -468,11 +468,12 @@ def _rows(t, cols: int, types, device, where: str):
 
 def moe_dispatch_forward(d: moe_rows_dims, x, n_tokens: int, perm, xs, inv, ws, stream=None):
     """``xs[r] = x[perm[r] // k]`` (zero where ``perm[r]`` is negative); ``inv`` receives each pair's row, or -1."""
-    H, T, dev, ty, P = d.width, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ()), xs.shape[0]
+    H, T, dev, ty = d.width, n_tokens, x.device, _DENSE_TYPES.get(d.dtype, ())
+    pxs, ld_xs, P = _rows(xs, H, ty, dev, "moe_dispatch_forward, xs")
     _dense_call(_lib.moe_dispatch_forward, "moe_dispatch_forward", d, dev, ws, stream, (
         *_mat(x, T, H, ty, dev, "moe_dispatch_forward, x"), T,
         _array(perm, (P,), torch.int32, dev, "moe_dispatch_forward, perm"), P,
-        *_mat(xs, P, H, ty, dev, "moe_dispatch_forward, xs"),
+        pxs, ld_xs,
         _array(inv, (T, d.top_k), torch.int32, dev, "moe_dispatch_forward, inv")))
 
 
@@ -503,7 +504,7 @@ def moe_combine_backward(d: moe_rows_dims, dy, n_tokens: int, perm, inv, topk_w,
                          stream=None):
     """Gradients of moe_combine_forward from ``dy`` (the rows' type or float32); None: not computed.  ``dtopk_w`` needs
     the forward pass's ``ys``."""
-    H, T, dev, ty, yd, P = d.width, n_tokens, dy.device, _DENSE_TYPES.get(d.dtype, ()), dtype_code(dy), perm.shape[0]
+    H, T, dev, ty, yd, P = d.width, n_tokens, dy.device, _DENSE_TYPES.get(d.dtype, ()), dtype_code(dy), perm.numel()
     _dense_call(_lib.moe_combine_backward, "moe_combine_backward", d, dev, ws, stream, (
         *_mat(dy, T, H, _DENSE_TYPES[yd], dev, "moe_combine_backward, dy"), yd, T,
         _array(perm, (P,), torch.int32, dev, "moe_combine_backward, perm"),

@@ -118,3 +118,21 @@ def test_binding_refuses_mismatched_tensors(N):
         with pytest.raises(N.MoeError) as e:
             call()
         assert e.value.code == N.MOE_EINVAL
+
+
+@pytest.mark.parametrize("shape", [(), (2, 4), (2, 4, 64), (0,)])
+def test_binding_refuses_other_numbers_of_dimensions(N, shape):
+    """The arguments that say themselves how many rows there are, a scalar among them."""
+    d = N.rows_dims(64, 2, N.MOE_BF16)
+    x, xs = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16)
+    perm, inv, w = torch.arange(8, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    ws = torch.zeros(1024, dtype=torch.int32)
+    rows, pairs = torch.zeros(shape, dtype=torch.bfloat16), torch.zeros(shape, dtype=torch.int32)
+    for call in (lambda: N.moe_dispatch_forward(d, x, 4, perm, rows, inv, ws),
+                 lambda: N.moe_dispatch_forward(d, x, 4, pairs, xs, inv, ws),
+                 lambda: N.moe_dispatch_backward(d, rows, inv, 4, x, ws),
+                 lambda: N.moe_combine_forward(d, rows, inv, w, 4, x, ws),
+                 lambda: N.moe_combine_backward(d, x, 4, pairs, inv, w, ws, dys=xs)):
+        with pytest.raises(N.MoeError) as e:
+            call()
+        assert e.value.code == N.MOE_EINVAL
