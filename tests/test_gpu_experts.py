@@ -381,3 +381,53 @@ def test_more_than_2_31_elements(N):
         R.check("dx", dx[s], ref["dx"])
         R.check("dw", dw[e], ref["dw0"])
     assert (dw[598] == 0).all() and (dw[512].abs().sum() > 0)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("act,at_low,at_high", [(0, (-1, 1), (1, 1)), (1, (0, 0), (1, 1)), (2, (0, 0), (1, 1)),
+                                                (3, (0, 0), (1, 1)), (4, (0, 0), (1, 1)), (5, (0, 0), (0, 0))])
+def test_saved_infinities_and_nan_of_the_gated_block(N, act, at_low, at_high, dt):
+    """g saved as an infinity: du = dh act(g) and dg = dh u act'(g) are the limits (at_*: the sign of an infinite act, 0: finite;
+    act'), zero where dh is, whatever lies beside; a NaN stays in its row and expert."""
+    inf = float("inf")
+    E, K, M, P = 3, 8, 8, 15
+    counts = [5, 4, 6]
+    offs, slices, P = rows_of(counts, 0, 0)
+    eye = torch.eye(M, dtype=dt, device="cuda").repeat(E, 1, 1)
+    x, u = torch.ones(P, K, dtype=dt, device="cuda"), torch.ones(P, M, dtype=dt, device="cuda")
+    g = torch.ones(P, M, dtype=dt, device="cuda")
+    g[5:9, ::2], g[5:9, 1::2] = -inf, inf  # the second expert's
+    dh = torch.ones(P, M, dtype=dt, device="cuda")
+    d = N.experts_dims(E, K, M, N.dtype_code(x), act)
+    ws, _ = workspace(N, d, P, True)
+
+    def run():
+        dx, dwg, dwu = torch.empty_like(x), torch.empty_like(eye), torch.empty_like(eye)
+        N.moe_experts_gated_backward(d, x, offs, eye, eye, g, u, dh, ws, dx=dx, dw_gate=dwg, dw_up=dwu)
+        assert N.moe_check_device_error(ws) == 0
+        return dx, dwg, dwu
+
+    dx, dwg, dwu = run()
+    slope = torch.tensor([at_low[1], at_high[1]] * 4, dtype=torch.float64, device="cuda")
+    assert torch.equal(dwg[1].double(), (4 * slope)[:, None].expand(M, K))
+    sign = torch.tensor([at_low[0], at_high[0]] * 4, device="cuda")
+    for j in range(M):
+        if sign[j]:
+            assert (dwu[1, j] == sign[j].item() * inf).all()
+        else:  # act's limit: sigmoid 0 and 1, the others 0 below
+            assert (dwu[1, j] == (4.0 if act == 5 and j % 2 else 0.0)).all()
+    assert torch.isfinite(dx[:5]).all() and torch.isfinite(dx[9:]).all() and torch.isfinite(dwu[[0, 2]]).all()
+    # nothing comes back where dh is zero
+    dh[5:9] = 0
+    u[5:9] = inf
+    dx0, dwg0, dwu0 = run()
+    assert (dx0[5:9] == 0).all() and (dwg0[1] == 0).all() and (dwu0[1] == 0).all()
+    # a NaN: its row's dx, and its output's row of dW of its expert
+    g[10, 3] = float("nan")
+    dx1, dwg1, dwu1 = run()
+    assert torch.isnan(dx1[10]).all() and torch.isnan(dwu1[2, 3]).all()
+    # without an activation, and with relu, act' of a NaN is a number
+    assert torch.isnan(dwg1[2, 3]).all() if act not in (0, 4) else torch.isfinite(dwg1[2, 3]).all()
+    rows, outs = torch.ones(P, dtype=torch.bool, device="cuda"), torch.ones(E, M, dtype=torch.bool, device="cuda")
+    rows[10], outs[2, 3] = False, False
+    assert torch.equal(dx1[rows], dx0[rows]) and torch.equal(dwg1[outs], dwg0[outs]) and torch.equal(dwu1[outs], dwu0[outs])

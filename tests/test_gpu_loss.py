@@ -365,3 +365,79 @@ def test_large_vocabulary_and_2_31_elements(N):
     # as the sum of magnitudes
     R.check("dx", dx, (val, R._round(val, mag * (R.half_step(BF16) + bound + 2 * V * R.E), BF16)))
     assert guard_ok(whole) and N.moe_check_device_error(ws) == 0
+
+
+def test_infinities_and_nan_in_the_backward_pass(N):
+    """Logits past fp32 from finite operands: the gradients are the limits; a NaN reaches its token's dx and the dW of the columns
+    that it has a gradient for, which are all; a token that is left out reaches nothing."""
+    V, K, T, g = 100, 64, 6, 0.5
+    far = 2.0 ** 65  # its square is infinite in fp32
+    w = torch.zeros(V, K, dtype=BF16, device="cuda")
+    w[:, 0], w[5, 1], w[9, 2] = 1.0, far, -far
+    x = torch.zeros(T, K, dtype=BF16, device="cuda")
+    x[:, 0] = 1.0
+    x[0, 1], x[1, 1], x[2, 2], x[3, 2], x[4, 1] = far, far, far, far, far
+    targets = torch.tensor([5, 7, 7, 9, IGNORE, 0], dtype=torch.int32, device="cuda")
+    d = N.loss_dims(K, V, N.MOE_BF16, IGNORE)
+    ws, _ = workspace(N, d, T, True)
+
+    def run(x, targets):
+        loss, lse = floats(T, 2)
+        N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+        dx, dw = torch.full_like(x, 7.0), torch.full_like(w, 7.0)
+        N.moe_loss_backward(d, x, T, w, targets, loss, lse, torch.full((T,), g, device="cuda"), ws, dx=dx, dw=dw)
+        assert N.moe_check_device_error(ws) == 0
+        return loss, lse, dx, dw
+
+    # without the token whose gradient is not a number: probabilities that are 0, 1 or one of 99 (98) equal logits
+    targets[1] = IGNORE
+    loss, lse, dx, dw = run(x, targets)
+    assert loss[0] == 0 and lse[0] == math.inf and loss[3] == math.inf and (loss[[1, 4]] == 0).all()
+    p = torch.zeros(T, V, dtype=torch.float64, device="cuda")
+    p[2], p[3], p[5] = 1 / 99, 1 / 99, 1 / 100  # tokens 2 and 3: z_9 is -infinity
+    p[2, 9] = p[3, 9] = 0
+    p[2, 7] -= 1
+    p[3, 9] -= 1
+    p[5, 0] -= 1
+    dz = g * p
+    # the sum of 99 or 100 exponentials, exp, expm1, a few products: 300 e; dz to bf16; then sums of 100 (6) terms
+    r = (R.half_step(BF16) + 300 * R.E) * dz.abs()
+    for name, got, a, b in (("dx", dx, dz, w), ("dw", dw, dz.T, x)):
+        val, mag = a @ b.double(), a.abs() @ b.double().abs()
+        err = (r if name == "dx" else r.T) @ b.double().abs() + 2 * a.shape[1] * R.E * mag
+        R.check(name, got, (val, R._round(val, err, BF16)))
+    # with it: its dx, and its column of dW, are NaN; its target's column has -g x of it, the others nothing
+    targets[1] = 7
+    loss, lse, dx1, dw1 = run(x, targets)
+    assert loss[1] == math.inf and torch.isnan(dx1[1, 1]) and torch.isnan(dx1[1, 0])
+    keep = torch.arange(T, device="cuda") != 1
+    assert torch.equal(dx1[keep], dx[keep])
+    same = torch.ones(V, dtype=torch.bool, device="cuda")
+    same[5] = same[7] = False
+    assert torch.equal(dw1[same], dw[same]) and torch.isnan(dw1[5, 0]) and dw1[7, 1] == -g * far
+    # a NaN in x
+    targets[1], x[5, 3] = IGNORE, math.nan
+    loss, lse, dx2, dw2 = run(x, targets)
+    assert torch.isnan(loss[5]) and torch.isnan(lse[5]) and torch.isnan(dx2[5]).all()
+    assert torch.equal(dx2[:5], dx[:5]) and torch.isnan(dw2[:, 3]).all()
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("T,K,V", [(70, 64, 131072), (9, 40, 300000), (1, 61, 100003)])
+def test_the_softmax_part_of_dx_over_a_large_vocabulary(N, T, K, V, dt):
+    """Weights with a mean: sum_v p_v w_v is then as large as the target's row, and far beyond the bound, 2 V e (1.6 % of both at
+    131072 columns, 3.6 % at 300000) and the roundings of dz; without it no element would be within."""
+    gen = gen_for(60 + T)
+    x = rnd(gen, (T, K), dt)
+    w = ((torch.randn(V, K, generator=gen, device="cuda") * 0.1 + 1.0) * K ** -0.5).to(dt)
+    targets = torch.randint(0, V, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    d = N.loss_dims(K, V, N.dtype_code(x), IGNORE)
+    ws, _ = workspace(N, d, T, True)
+    loss, lse = floats(T, 2)
+    N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+    dx, dloss = torch.empty_like(x), torch.ones(T, device="cuda")
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dx=dx)
+    val, bound = L.backward(x, w, targets, IGNORE, loss, lse, dloss, dt)["dx"]
+    R.check("dx", dx, (val, bound))
+    own = torch.expm1(-loss.double())[:, None] * w.double()[targets.long()]
+    assert ((own - val).abs() > 4 * bound).all()

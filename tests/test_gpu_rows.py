@@ -319,3 +319,19 @@ def test_most_tokens(N):
     with pytest.raises(N.MoeError) as e:
         N.moe_combine_forward(d, xs, inv, w, T + 1, y, ws)
     assert e.value.code == N.MOE_EINVAL
+
+
+@pytest.mark.parametrize("T,H", [(30, 7), (30, 65), (30, 521), (2100, 521), (17000, 131)])
+def test_in_place_on_the_residual_in_fp16(N, T, H):
+    gen = gen_for(15 + H)
+    k = 3
+    perm, inv = layout(gen, T, k, 4, pad=4, drop=0.2)
+    d = N.rows_dims(H, k, N.MOE_F16)
+    ws = workspace(N, d, T)
+    rows, w, y = rnd(gen, (perm.numel(), H), F16), torch.rand(T, k, generator=gen, device="cuda"), rnd(gen, (T, H), F16)
+    for call in (lambda out, r: N.moe_combine_forward(d, rows, inv, w, T, out, ws, residual=r),
+                 lambda out, r: N.moe_dispatch_backward(d, rows, inv, T, out, ws, residual=r)):
+        want, got = torch.empty_like(y), y.clone()
+        call(want, y)
+        call(got, got)
+        assert torch.equal(got, want)
