@@ -17,7 +17,8 @@ constexpr int kLossTokens = 8192;          // tokens of a forward launch: bounds
 constexpr size_t kLossDzBytes = 256u << 20;
 constexpr int kLossTile = 64;              // the smallest tile's columns
 constexpr int kMostBlocks = 256;           // workgroups that look for fp16's largest |x|
-constexpr int64_t kLiftFew = 1 << 17;      // elements of x up to which each does so for itself (5 x 2048: 333 us against 340)
+constexpr int64_t kLiftFew = 1 << 15;      // elements of x up to which each does so for itself, and
+constexpr int32_t kLiftFewTokens = 256;    // tokens: each of their workgroups goes through all of them
 
 struct LossWs {
   size_t part, scale, scaled, undo, most, x, lifted, w, dz, acc, sums, sums_bytes, total;
@@ -209,8 +210,9 @@ static hipError_t start_join(const LossJoinArgs& j, hipStream_t st) {
 // of its softmax (its dx had the wrong sign).  So each token has a power of two of its own besides, 2^lift, that brings its dz to
 // 2^13 .. 2^15 at a probability of 1: normal down to probabilities of 2^-27, zero below 2^-38.  dx undoes it row by row; for
 // dW, whose sum runs over the tokens, x carries 2^-lift in a copy, the call's largest |x| brought to 2^14 (exact down to 2^-28 of
-// that).  Up to kLiftFew elements of x every workgroup finds the maxima by itself, in one launch, else two.  Against one factor,
-// fp16: 5 tokens, 100003 x 2048, 328 -> 333 us; 333 tokens, 32771 x 1000, 134 -> 140; 8192 tokens, 100003 x 2048, 8.33 -> 8.35 ms.
+// that).  Up to kLiftFew elements of x and kLiftFewTokens every workgroup finds the maxima by itself, in one launch, else two.
+// Against one factor for all, fp16: 5 tokens, 100003 x 2048, 331 -> 333 us; 333 tokens, 32771 x 1000, 138 -> 145; 8192 tokens,
+// 100003 x 2048, 8.69 -> 8.73 ms; 16 tokens, 300 x 2048 (in one launch) 25.9 -> 30.6, 64 tokens (in two) 26.0 -> 32.2.
 struct LossScaleArgs {
   const float* dloss;
   const int32_t* targets;
@@ -254,19 +256,18 @@ MOE_DEV float most_dloss(const LossScaleArgs& a) {
 }
 MOE_DEV float scale_base(float m) { return fminf(fmaxf(m, 0x1p-100f), 0x1p100f); }
 
-// A thread's share of the largest finite |x| of the tokens first, first + step ..., a wave each.
-MOE_DEV float most_x(const LossScaleArgs& a, int first, int step) {
-  const int lane = threadIdx.x & 63;
+// A thread's share of the largest finite |x|: chunks of 8 elements, from `first` on by `step`.
+MOE_DEV float most_x(const LossScaleArgs& a, int64_t first, int64_t step) {
+  const int64_t chunks = (a.K + 7) / 8, total = a.T * chunks;
   float m = 0.0f;
-  for (int t = first + (threadIdx.x >> 6); t < a.T; t += step) {
-    if (!a.live(t)) continue;
 #pragma unroll 4
-    for (int c = lane * 8; c < a.K; c += 512) {
-      float v[8];
-      load8<_Float16>(a.x, t * a.ldx + c, a.K - c < 8 ? a.K - c : 8, v);
+  for (int64_t id = first; id < total; id += step) {
+    const int t = (int)(id / chunks), c = (int)(id - t * chunks) * 8;
+    float v[8];
+    load8<_Float16>(a.x, t * a.ldx + c, a.K - c < 8 ? a.K - c : 8, v);
+    const bool live = a.live(t);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fabsf(v[i]) < INFINITY ? fmaxf(m, fabsf(v[i])) : m;
-    }
+    for (int i = 0; i < 8; ++i) m = live && fabsf(v[i]) < INFINITY ? fmaxf(m, fabsf(v[i])) : m;
   }
   return m;
 }
@@ -298,7 +299,7 @@ MOE_DEV void store_scale(const LossScaleArgs& a, float m) {
 __global__ __launch_bounds__(1024) void k_loss_scale(LossScaleArgs a) {
   float m = 0.0f, x = 0.0f;
   if (blockIdx.x == 0) m = most_dloss(a);
-  else x = most_x(a, ((int)blockIdx.x - 1) * 16, a.blocks * 16);
+  else x = most_x(a, (int64_t)(blockIdx.x - 1) * 1024 + threadIdx.x, a.blocks * 1024);
   most_of_all(m, x);
   if (blockIdx.x == 0) store_scale(a, scale_base(m));
   else if (threadIdx.x == 0) a.most[blockIdx.x - 1] = x;
@@ -307,32 +308,31 @@ __global__ __launch_bounds__(1024) void k_loss_scale(LossScaleArgs a) {
 // lifted = x 2^(k - lift) in rows of whole chunks, zero for a token without a gradient; dW's factor is the products' times 2^-k.
 template <bool FEW>
 __global__ __launch_bounds__(1024) void k_loss_lift(LossScaleArgs a) {
-  const int lane = threadIdx.x & 63;
   float m = 0.0f, x = 0.0f;
   if constexpr (FEW) {
     m = most_dloss(a);
-    x = most_x(a, 0, 16);
+    x = most_x(a, threadIdx.x, 1024);
     most_of_all(m, x);
     m = scale_base(m);
     if (blockIdx.x == 0) store_scale(a, m);
   } else {
     m = a.scale[3];
-    for (int i = lane; i < a.blocks; i += 64) x = fmaxf(x, a.most[i]);
+    for (int i = threadIdx.x & 63; i < a.blocks; i += 64) x = fmaxf(x, a.most[i]);
 #pragma unroll
     for (int o = 32; o; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
   }
   const int k = x > 0.0f ? 14 - ilogbf(x) : 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) a.scale[2] = __builtin_ldexpf(m / a.most_dz, -k);
-  for (int t = blockIdx.x * 16 + (threadIdx.x >> 6); t < a.T; t += gridDim.x * 16) {
+  const int64_t chunks = (a.K + 7) / 8, total = a.T * chunks;
+  for (int64_t id = (int64_t)blockIdx.x * 1024 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 1024) {
+    const int t = (int)(id / chunks), c = (int)(id - t * chunks) * 8;
     const bool live = a.live(t);
     const int by = k - lift_of(m, a.dloss[t]);
-    for (int c = lane * 8; c < a.K; c += 512) {
-      float v[8];
-      load8<_Float16>(a.x, t * a.ldx + c, a.K - c < 8 ? a.K - c : 8, v);
+    float v[8];
+    load8<_Float16>(a.x, t * a.ldx + c, a.K - c < 8 ? a.K - c : 8, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = live ? __builtin_ldexpf(v[i], by) : 0.0f;
-      store8<_Float16>(a.lifted, t * a.ld_lifted + c, 8, v);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = live ? __builtin_ldexpf(v[i], by) : 0.0f;
+    store8<_Float16>(a.lifted, t * a.ld_lifted + c, 8, v);
   }
 }
 
@@ -481,18 +481,18 @@ MOE_API int moe_loss_backward(const moe_loss_dims* dims, const void* x, int64_t 
   f.ignore = dims->ignore;
   const void* x_dw = xs;  // dW's x and its stride
   int64_t ld_xdw = ld_x;
-  const int32_t rows = (n_tokens + 15) / 16;  // a wave each
+  const int64_t chunks = n_tokens * (L.ld_in / 8), copies = (chunks + 1023) / 1024;
   if (!bf16 && dw_or_null) {
     f.most = (float*)at(L.most);
     x_dw = f.lifted = at(L.lifted);
     ld_xdw = f.ld_lifted = L.ld_in;
-    f.blocks = rows < kMostBlocks ? rows : kMostBlocks;
+    f.blocks = copies / 2 + 1 < kMostBlocks ? (int32_t)(copies / 2 + 1) : kMostBlocks;  // two chunks a thread at least
   }
-  if (f.lifted && (int64_t)n_tokens * dims->n_in <= kLiftFew) {
-    k_loss_lift<true><<<rows, 1024, 0, st>>>(f);
+  if (f.lifted && n_tokens <= kLiftFewTokens && (int64_t)n_tokens * dims->n_in <= kLiftFew) {
+    k_loss_lift<true><<<(uint32_t)copies, 1024, 0, st>>>(f);
   } else {
     k_loss_scale<<<1 + f.blocks, 1024, 0, st>>>(f);
-    if (f.lifted) k_loss_lift<false><<<rows < 1024 ? rows : 1024, 1024, 0, st>>>(f);
+    if (f.lifted) k_loss_lift<false><<<(uint32_t)(copies < 1024 ? copies : 1024), 1024, 0, st>>>(f);
   }
   if (hipGetLastError() != hipSuccess) return MOE_EHIP;
   for (int32_t c0 = 0; c0 < dims->vocab; c0 += L.piece) {

@@ -195,7 +195,8 @@ def check_past_range(name, got, ref):
     R.check(name, torch.where(inf, 0.0, got), (torch.where(inf, 0.0, val), bound))
 
 
-@pytest.mark.parametrize("T,K,V,pad", [(24, 64, 50000, 0), (24, 61, 20011, 0), (240, 40, 30000, 3), (700, 33, 5001, 0)])
+@pytest.mark.parametrize("T,K,V,pad", [(24, 64, 50000, 0), (24, 61, 20011, 0), (240, 40, 30000, 3), (700, 33, 5001, 0), (9, 2048, 400, 0),
+                                       (20000, 1, 40, 0), (400, 300, 900, 5)])
 def test_fp16_tokens_of_very_different_weight(N, T, K, V, pad):
     """dloss over twenty-three powers of two: every token's dx keeps its softmax part, relative to its own dloss.  The weights have a
     mean, so that this part is as large as the target's; dloss is large enough for the results to be normal numbers."""
