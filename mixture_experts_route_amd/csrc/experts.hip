@@ -3,7 +3,10 @@
 
 namespace moe {
 
-// Workspace: control words, then for a backward pass dz (gated: dg, du) with rows padded to whole 16-byte chunks.
+// Workspace: control words, then for a backward pass dz (gated: dg, du) with rows padded to whole 16-byte chunks.  dims do not say
+// which call: the linear one uses one matrix of dz where dys has no whole chunks, else none.  dg and du are rounded to 16 bits for the
+// matrix cores, which costs dx and dW the whole of their distance to sums of unrounded ones: 512 experts, 40960 rows, bf16 2.3e-3 off the
+// definition, from unrounded dz 1.7e-3 (the results' own rounding).
 struct ExpertsWs {
   size_t dz0, dz1, total;
   int64_t ldz;

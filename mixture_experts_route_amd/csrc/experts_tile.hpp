@@ -107,7 +107,7 @@ MOE_DEV bool group_rows(const GroupArgs& g, TileArgs& a, TileIndex& x) {
 // on average, the longest three times that, 4096 x 4096, 2273 us; spread 922), along the shorter side first, which reads the
 // fewest different operand columns.
 struct DwTile {
-  int e, m, ti, tj, row0, rows, steps;
+  int e, m, ti, tj, row0, rows;
 };
 // Tile `id` of the launch's; false: there is none.
 MOE_DEV bool dw_tile(const GroupArgs& g, uint32_t id, DwTile& x) {
@@ -123,7 +123,6 @@ MOE_DEV bool dw_tile(const GroupArgs& g, uint32_t id, DwTile& x) {
   if (in == 0 && threadIdx.x == 0 && (o0 != lo || o1 != hi || hi < lo)) set_error(g.ctrl, MOE_DERR_ROWS);
   x.row0 = lo;
   x.rows = hi > lo ? hi - lo : 0;
-  x.steps = x.rows ? (x.rows + kStepR - 1) / kStepR : 1;
   return true;
 }
 // This workgroup's tile of dW, as arguments of its expert's product; false: there is none.
@@ -292,7 +291,8 @@ __global__ __launch_bounds__(256, 2) void k_group_backward(GroupArgs dx, GroupAr
 // as P / tile + half the experts that can have rows, but at least those.  128-square tiles carry everything but the ends:
 // they draw the weights fastest even where an expert has two rows (16 tokens' ten of 512 experts, 2048 x 768: 56 us, 64-square
 // 71), but below two for three CUs the 64-square ones' number counts for more (one token, 768 gated of 2048: 15.5 and 23.5 us;
-// 24 experts of 28 rows, 1360 of 1000, 264 tiles: 21.6 and 16.9), and from 256 rows per expert on the 256-square ones'
+// 24 experts of 28 rows, 1360 of 1000, 264 tiles: 21.6 and 16.9; near the limit it goes by the sizes: 140 tiles, 8 experts of 162
+// rows, 1280 of 512: 8.3 and 9.9, 160 tiles of 200 rows 12.4 and 10.0, 216 tiles, 18 of 17 rows, 1536 of 2048: 22.8 and 26.0), and from 256 rows per expert on the 256-square ones'
 // reuse does (128 experts of 320 rows, 2048 x 768: 176 us, 128-square 197; 256 of 160: 241 and 250, 512 Zipf ones of 160 980
 // and 966).
 template <int KIND>

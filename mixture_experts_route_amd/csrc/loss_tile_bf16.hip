@@ -1,25 +1,11 @@
 // Tile products of the loss with bf16 operands.
-#include "dense_tile.hpp"
-#include "loss.hpp"
+#include "loss_tile.hpp"
 
 namespace moe {
 
-hipError_t launch_loss_bf16(const TileArgs& args, int* tiles, hipStream_t st) {
-  TileArgs a = args;
-  DensePlan plan{};
-  double us;
-  const hipError_t e = prepare_tile<kRows, kRows, kEpiLoss>(a, plan, us, st);
-  if (e != hipSuccess) return e;
-  plan.kernel = few_tokens_kernel(a, plan.kernel);
-  const int tile = plan.kernel == MOE_DENSE_TILE256 ? 256 : plan.kernel == MOE_DENSE_TILE64 || plan.kernel == MOE_DENSE_ANY64 ? 64 : 128;
-  *tiles = (a.N + tile - 1) / tile;
-  return start_plan<__bf16, kRows, kRows, kEpiLoss>(a, plan.kernel, st);
-}
-
-hipError_t launch_loss_dz_bf16(const TileArgs& a, hipStream_t st) { return launch_tile_k<__bf16, kRows, kRows, kEpiLossDz>(a, st); }
-
-hipError_t launch_loss_dx_bf16(const TileArgs& a, hipStream_t st) { return launch_tile_k<__bf16, kRows, kCols, kEpiSum>(a, st); }
-
-hipError_t launch_loss_dw_bf16(const TileArgs& a, hipStream_t st) { return launch_tile_k<__bf16, kCols, kCols, kEpiSum>(a, st); }
+hipError_t launch_loss_bf16(const TileArgs& a, int* tiles, hipStream_t st) { return launch_loss_t<__bf16>(a, tiles, st); }
+hipError_t launch_loss_dz_bf16(const TileArgs& a, hipStream_t st) { return launch_loss_dz_t<__bf16>(a, st); }
+hipError_t launch_loss_dx_bf16(const TileArgs& a, hipStream_t st) { return launch_loss_dx_t<__bf16>(a, st); }
+hipError_t launch_loss_dw_bf16(const TileArgs& a, hipStream_t st) { return launch_loss_dw_t<__bf16>(a, st); }
 
 }  // namespace moe
