@@ -431,3 +431,24 @@ def test_saved_infinities_and_nan_of_the_gated_block(N, act, at_low, at_high, dt
     rows, outs = torch.ones(P, dtype=torch.bool, device="cuda"), torch.ones(E, M, dtype=torch.bool, device="cuda")
     rows[10], outs[2, 3] = False, False
     assert torch.equal(dx1[rows], dx0[rows]) and torch.equal(dwg1[outs], dwg0[outs]) and torch.equal(dwu1[outs], dwu0[outs])
+
+
+@pytest.mark.parametrize("K,M", [(1 << 20, 24), (24, 1 << 20), ((1 << 20) - 1, 9)])
+def test_widest_rows(N, K, M):
+    """2^20 inputs or outputs, of whole numbers: every sum is exact in fp32."""
+    gen = gen_for(95)
+    counts = [5, 0, 70]
+    offs, slices, P = rows_of(counts, 1, 1)
+    whole = lambda *s: torch.randint(-1, 2, s, generator=gen, device="cuda").to(BF16)  # noqa: E731
+    x, w, dy = whole(P, K), whole(3, M, K), whole(P, M)
+    d = N.experts_dims(3, K, M, N.MOE_BF16)
+    ws, guard = workspace(N, d, P, True)
+    y, dx, dw = Out((P, M), BF16), Out((P, K), BF16), torch.empty_like(w)
+    N.moe_experts_linear_forward(d, x, offs, w, y.t, ws)
+    N.moe_experts_linear_backward(d, x, offs, w, dy, ws, dx=dx.t, dw=dw)
+    for e in range(3):
+        s = slices[e]
+        assert torch.equal(y.t[s], (x[s].double() @ w[e].double().T).to(BF16))
+        assert torch.equal(dx.t[s], (dy[s].double() @ w[e].double()).to(BF16))
+        assert torch.equal(dw[e], (dy[s].double().T @ x[s].double()).to(BF16))
+    assert y.untouched() and dx.untouched() and guard_ok(guard) and N.moe_check_device_error(ws) == 0

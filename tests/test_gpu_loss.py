@@ -442,3 +442,41 @@ def test_the_softmax_part_of_dx_over_a_large_vocabulary(N, T, K, V, dt):
     R.check("dx", dx, (val, bound))
     own = torch.expm1(-loss.double())[:, None] * w.double()[targets.long()]
     assert ((own - val).abs() > 4 * bound).all()
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("K", [1 << 20, (1 << 20) - 1])
+def test_longest_rows(N, K, dt):
+    """2^20 inputs, whole multiples of 2^-7: the logits are exact in fp32 (at most 2^20 terms of one unit), so loss_reference's bounds hold
+    with none of their part for the logits."""
+    T, V = 5, 70
+    gen = gen_for(70)
+    x = torch.randint(-1, 2, (T, K), generator=gen, device="cuda").to(dt)
+    w = (torch.randint(-1, 2, (V, K), generator=gen, device="cuda") * 2.0 ** -7).to(dt)
+    targets = torch.tensor([3, 69, 0, IGNORE, 12], dtype=torch.int32, device="cuda")
+    d = N.loss_dims(K, V, N.dtype_code(x), IGNORE)
+    ws, whole = workspace(N, d, T, True)
+    loss, lse = floats(T, 2)
+    N.moe_loss_forward(d, x, T, w, targets, loss, lse, ws)
+    z = x.double() @ w.double().T
+    live = targets != IGNORE
+    at = targets.clamp(min=0).long()[:, None]
+    want = torch.where(live, torch.logsumexp(z, 1), 0.0)
+    span = z.abs().max()
+    # the sum of 70 exponentials of arguments up to 2 span, then a few roundings of lse and of the logits' distance
+    bound = 2 * R.E * (2 * span + 4 + 70) + 16 * R.E * span
+    assert ((lse.double() - want).abs() <= bound).all()
+    assert ((loss.double() - torch.where(live, want - z.gather(1, at)[:, 0], 0.0)).abs() <= bound).all()
+    dloss = torch.tensor([1.0, -2.0, 0.5, 1.0, 0.25], device="cuda")
+    dx, dw = Out((T, K), dt), Out((V, K), dt)
+    N.moe_loss_backward(d, x, T, w, targets, loss, lse, dloss, ws, dx=dx.t, dw=dw.t)
+    p = torch.exp(z - lse.double()[:, None]).scatter(1, at, torch.expm1(-loss.double())[:, None])
+    dz = torch.where(live[:, None], p * dloss.double()[:, None], 0.0)
+    tiny = R.tiny_step(dt) * 2 / (2.0 ** 11 if dt == F16 else 1.0)
+    r = dz.abs() * (R.half_step(dt) + 2 * R.E * (4 * span + 20)) + tiny
+    for name, got, a, ra, b in (("dx", dx, dz, r, w), ("dw", dw, dz.T, r.T, x)):
+        val = a @ b.double()
+        err = ra @ b.double().abs() + 2 * a.shape[1] * R.E * ((a.abs() + ra) @ b.double().abs())
+        R.check(name, got.t, (val, R._round(val, err, dt)))
+        assert got.untouched()
+    assert guard_ok(whole) and N.moe_check_device_error(ws) == 0

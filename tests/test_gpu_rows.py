@@ -335,3 +335,8 @@ def test_in_place_on_the_residual_in_fp16(N, T, H):
         call(want, y)
         call(got, got)
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("H", [1 << 20, (1 << 20) - 3])
+def test_widest_rows(N, H):
+    check_all(N, 16, 5, 3, 4, H, BF16, f32=True, res=True, pad=2, drop=0.2)
